@@ -112,7 +112,8 @@ typedef enum {
     VG_ERR_NULL_PTR = 1,           /* a required pointer is NULL, or residual_out
                                       and residual are not both set or both NULL  */
     VG_ERR_BAD_SHAPE = 2,          /* num_tokens < 0, row length not a multiple
-                                      of 8, < 8, or > VG_MAX_ROW                  */
+                                      of 8, < 8, or > VG_MAX_ROW; other sizes
+                                      an entry point's comment rules out          */
     VG_ERR_MISALIGNED = 3,         /* a tensor pointer breaks the alignment rule */
     VG_ERR_BAD_MODE = 4,           /* mode is not a vg_scale_mode (with valid
                                       per-group options)                          */
@@ -287,6 +288,131 @@ vg_status vg_fused_qk_norm_rope(uint16_t *qkv, const uint16_t *q_weight, const u
                                 vg_stream_t stream);
 
 /*
+ * The same with several position axes (text, images and video: time, height,
+ * width).  Pair i turns by the position on its axis: c_i and s_i come from row
+ * positions[axis(i), t] of the cache.  Nothing else changes.
+ *
+ *   positions     in int64 [num_axes, T], axis by axis (8-byte aligned)
+ *   sections      HOST int32 [num_axes], >= 0, their sum D/2: how many of the
+ *                 D/2 pairs each axis turns; read before the call returns
+ *   num_axes      1..4
+ *   interleaved   0: the first sections[0] pairs turn by axis 0, the next
+ *                 sections[1] by axis 1, and so on.  Otherwise the axes take
+ *                 turns: pair i by axis x = i mod num_axes while
+ *                 i / num_axes < sections[x], else by axis 0; each axis but
+ *                 the first must get all its pairs (num_axes *
+ *                 (sections[x] - 1) + x < D/2), else VG_ERR_BAD_SHAPE.
+ *   q_weight, k_weight   both NULL: no norm, the rotation only (y = x)
+ *   A position outside [0, max_position) on any axis leaves that token's
+ *   heads unchanged and sets VG_DEVICE_BAD_POSITION.
+ *   the other arguments as for vg_fused_qk_norm_rope
+ */
+vg_status vg_fused_qk_norm_mrope(uint16_t *qkv, const uint16_t *q_weight, const uint16_t *k_weight,
+                                 const float *cos_sin_cache, const int64_t *positions,
+                                 const int32_t *sections, int32_t num_axes, int64_t num_tokens,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int64_t max_position, float eps, int32_t is_neox,
+                                 int32_t interleaved, vg_stream_t stream);
+
+/*
+ * Rotation (and QK norm) on the way into a paged key/value cache: for every
+ * token the Q heads are normalised and rotated in place, and the normalised,
+ * rotated K heads and the V heads are written to the token's slot:
+ *   k_cache[page, in_page, h] = K head h,  v_cache[page, in_page, h] = V head h
+ *   page = slot / page_size, in_page = slot mod page_size
+ * bf16 caches (k_scale and v_scale NULL) hold bf16(o), rounded as for
+ * vg_fused_qk_norm_rope, and V's own bits.  FP8 caches hold e4m3(o / k_scale)
+ * and e4m3(v / v_scale) (RNE, saturating, from the fp32 value; the kernel
+ * multiplies by the rounded 1 / scale).  The K and V heads of qkv itself are
+ * left as they are.
+ *
+ *   qkv            in/out uint16 [T, (Hq + 2 Hkv) * D] bf16 (Q heads written)
+ *   k_cache, v_cache  out uint16 bf16, or uint8 E4M3 codes; element (page,
+ *                  token, head, d) of each at page * page_stride + token *
+ *                  token_stride + head * head_stride + d.  Only the slots
+ *                  named by `slots` are written.
+ *   q_weight, k_weight  in uint16 [D] bf16; both NULL: no norm
+ *   positions      in int64 [num_axes, T]; sections, num_axes and interleaved
+ *                  as for vg_fused_qk_norm_mrope (num_axes 1 may pass
+ *                  sections NULL)
+ *   slots          in int64 [T] (8-byte aligned): the token's place in the
+ *                  cache.  A negative slot appends nothing (a padding token;
+ *                  its Q heads are still rotated); one beyond the last slot
+ *                  appends nothing and sets VG_DEVICE_BAD_SLOT.  A token
+ *                  with a bad position is left unchanged and appended
+ *                  nowhere (VG_DEVICE_BAD_POSITION).  The non-negative slots
+ *                  must be distinct: a slot named twice holds an
+ *                  unspecified mix of its tokens (no other slot changes).
+ *   k_scale, v_scale  in fp32 [1], device, > 0 and finite: FP8 caches; both
+ *                  NULL: bf16 caches
+ *   num_q_heads Hq >= 0, num_kv_heads Hkv >= 1; head_dim D in {64, 128, 256}
+ *   num_pages, page_size  >= 1, num_pages * page_size <= INT32_MAX
+ *   page_stride, token_stride, head_stride  in elements, multiples of 8, no
+ *                  two places overlapping (a stride over an extent of one is
+ *                  ignored); offsets may pass 32 bits
+ * The caches must be 16-byte aligned and overlap no other tensor.
+ */
+vg_status vg_fused_qk_norm_rope_append(
+    uint16_t *qkv, void *k_cache, void *v_cache, const uint16_t *q_weight,
+    const uint16_t *k_weight, const float *cos_sin_cache, const int64_t *positions,
+    const int64_t *slots, const float *k_scale, const float *v_scale, const int32_t *sections,
+    int32_t num_axes, int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int64_t max_position, int64_t num_pages, int64_t page_size,
+    int64_t page_stride, int64_t token_stride, int64_t head_stride, float eps, int32_t is_neox,
+    int32_t interleaved, vg_stream_t stream);
+
+/*
+ * FP8 matrix product with a scale per block of 128: the product that reads
+ * what the per-group-128 ops above write.  With b = k / 128,
+ *   out[t, n] = bf16( sum_b a_scale[t, b] w_scale[n / 128, b]
+ *                     sum_{k in block b} a[t, k] w[n, k] )
+ * The products of a block and the scaled sum over blocks are held in fp32;
+ * the result is rounded once, to nearest even bf16.
+ *
+ *   out       out uint16 [T, N] bf16
+ *   a         in  uint8 [T, K]  E4M3 codes
+ *   a_scale   in  fp32 [T, K / 128], or with VG_SCALE_COLUMN_MAJOR in
+ *                 a_options [K / 128, T4] as the per-group ops write it
+ *   w         in  uint8 [N, K]  E4M3 codes
+ *   w_scale   in  fp32 [ceil(N / 128), K / 128]: one scale per 128 x 128 block
+ *   num_tokens T in [0, VG_MAX_GEMM_TOKENS]; n N: a multiple of 8 in
+ *             [8, VG_MAX_GEMM_COLUMNS] (else VG_ERR_BAD_SHAPE); k K: a
+ *             multiple of 128 (else VG_ERR_BAD_GROUP), at most VG_MAX_ROW
+ *   a_options 0 or VG_SCALE_COLUMN_MAJOR (else VG_ERR_BAD_MODE).  UE8M0
+ *             scales are fp32 numbers like any other and need no option.
+ * NaN codes and infinite scales follow IEEE arithmetic.  No workspace.
+ */
+#define VG_MAX_GEMM_TOKENS 16777216 /* 2^24 */
+#define VG_MAX_GEMM_COLUMNS 1048576 /* 2^20 */
+vg_status vg_fp8_block_gemm(uint16_t *out, const uint8_t *a, const float *a_scale,
+                            const uint8_t *w, const float *w_scale, int64_t num_tokens, int64_t n,
+                            int64_t k, int32_t a_options, vg_stream_t stream);
+
+/*
+ * Gated feed-forward projection: the gate and up products, SiLU(gate) * up
+ * and its per-group-128 FP8 quantisation in one kernel, so that neither the
+ * gate_up tensor nor the activation reaches memory:
+ *   g = row n, u = row I + n of w in the product above (fp32, not rounded)
+ *   y = g / (1 + exp(-g)) * u,  s as for vg_silu_mul_fp8 per group of 128,
+ *   q = e4m3(y / s)
+ *
+ *   q         out uint8 [T, I]  E4M3 codes
+ *   scale     out fp32 [T, I / 128]; out_options as the per-group options:
+ *                 VG_SCALE_UE8M0, VG_SCALE_COLUMN_MAJOR ([I / 128, T4])
+ *   a, a_scale, a_options, k  as for vg_fp8_block_gemm
+ *   w         in  uint8 [2I, K]: gate rows [0, I), up rows [I, 2I)
+ *   w_scale   in  fp32 [2I / 128, K / 128]
+ *   inter I: a multiple of 128 (else VG_ERR_BAD_GROUP), at most VG_MAX_ROW
+ * y is fp32: with VG_SCALE_UE8M0 a group whose amax lies within fp32 rounding
+ * of a power-of-two boundary may get the neighbouring power.
+ */
+vg_status vg_fp8_block_gemm_silu_mul_fp8(uint8_t *q, float *scale, const uint8_t *a,
+                                         const float *a_scale, const uint8_t *w,
+                                         const float *w_scale, int64_t num_tokens, int64_t inter,
+                                         int64_t k, int32_t a_options, int32_t out_options,
+                                         vg_stream_t stream);
+
+/*
  * Device-side status of the library's kernels on the current device (no
  * counterpart on the pages; the pipelined kernels' own failure report).
  * Every wait in the library's kernels is bounded; a wait that gives up sets
@@ -298,7 +424,8 @@ vg_status vg_fused_qk_norm_rope(uint16_t *qkv, const uint16_t *q_weight, const u
  * VG_OK.
  */
 #define VG_DEVICE_WAIT_TIMEOUT 1u
-#define VG_DEVICE_BAD_POSITION 2u /* vg_fused_qk_norm_rope: a position out of range */
+#define VG_DEVICE_BAD_POSITION 2u /* the rotary entry points: a position out of range */
+#define VG_DEVICE_BAD_SLOT 8u     /* vg_fused_qk_norm_rope_append: a slot beyond the cache */
 /* Debug builds only (compiled with VG_DEBUG_CHECKS, a test copy of the
  * library): a kernel computed a store or copy address outside the tensor it
  * belongs to; the access was skipped. */

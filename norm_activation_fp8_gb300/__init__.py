@@ -1,4 +1,6 @@
-"""Fused residual-add + RMSNorm -> FP8 and SiLU-and-mul -> FP8 on GB300.
+"""Fused residual-add + RMSNorm -> FP8 and SiLU-and-mul -> FP8 on GB300, the
+block-scaled FP8 products that read them, and QK norm + rotation with a paged
+K/V cache.
 
 Thin Python binding over the C ABI of ``libvg_fused.so`` (declared in
 ``include/vg_fused.h``).  Every step of both ops runs in the library's CUDA
@@ -22,6 +24,16 @@ Entry points (same names and argument order as the C ABI):
   vg_fused_add_rms_norm_nvfp4(q4, block_scale, residual_out, x, residual, weight,
                               global_scale, eps, stream=None)
   vg_silu_mul_nvfp4(q4, block_scale, gate_up, global_scale, stream=None)
+  vg_fused_qk_norm_mrope(qkv, q_weight, k_weight, cos_sin_cache, positions, sections,
+                         num_q_heads, num_kv_heads, head_dim, eps, is_neox=True,
+                         interleaved=False, stream=None)
+  vg_fused_qk_norm_rope_append(qkv, k_cache, v_cache, q_weight, k_weight, cos_sin_cache,
+                         positions, slots, num_q_heads, num_kv_heads, head_dim, eps,
+                         is_neox=True, sections=None, interleaved=False, k_scale=None,
+                         v_scale=None, stream=None)
+  vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options=0, stream=None)
+  vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options=0,
+                         out_options=0, stream=None)
 Convenience wrappers that allocate the outputs with torch:
   fused_add_rms_norm_fp8(x, residual, weight, eps, mode, ...)
   silu_mul_fp8(gate_up, mode, ...)
@@ -29,6 +41,8 @@ Convenience wrappers that allocate the outputs with torch:
   mla_dual_rms_norm(q_c, q_weight, kv_c, kv_weight, eps_q, eps_kv, q_fp8=False)
   fused_add_rms_norm_nvfp4(x, residual, weight, eps, global_scale, ...)
   silu_mul_nvfp4(gate_up, global_scale, ...)
+  fp8_block_gemm(a, a_scale, w, w_scale, a_options=0)
+  fp8_block_gemm_silu_mul_fp8(a, a_scale, w, w_scale, a_options=0, out_options=0)
 """
 from __future__ import annotations
 
@@ -50,11 +64,14 @@ STATUS_NAMES = {
 EXPORTED_SYMBOLS = ("vg_fused_add_rms_norm_fp8", "vg_silu_mul_fp8", "vg_fused_add_rms_norm_pad",
                     "vg_fused_mla_dual_rms_norm", "vg_fused_qk_norm_rope",
                     "vg_fused_mla_dual_rms_norm_per_token_quant", "vg_fused_add_rms_norm_nvfp4",
-                    "vg_silu_mul_nvfp4", "vg_device_status",
+                    "vg_silu_mul_nvfp4", "vg_fused_qk_norm_mrope", "vg_fused_qk_norm_rope_append",
+                    "vg_fp8_block_gemm", "vg_fp8_block_gemm_silu_mul_fp8", "vg_device_status",
                     "vg_status_string", "vg_abi_version")
 DEVICE_WAIT_TIMEOUT = 1
 DEVICE_BAD_POSITION = 2
 DEVICE_OUT_OF_BOUNDS = 4  # debug builds (VG_DEBUG_CHECKS) only
+DEVICE_BAD_SLOT = 8
+BLOCK = 128  # columns of an activation scale, rows and columns of a weight scale
 
 _lock = threading.Lock()
 _lib = None
@@ -101,6 +118,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.vg_fused_add_rms_norm_nvfp4.restype = ctypes.c_int
         lib.vg_silu_mul_nvfp4.argtypes = [P, P, P, P, i64, i64, P]
         lib.vg_silu_mul_nvfp4.restype = ctypes.c_int
+        lib.vg_fused_qk_norm_mrope.argtypes = [P, P, P, P, P, P, i32, i64, i32, i32, i32, i64, f32,
+                                               i32, i32, P]
+        lib.vg_fused_qk_norm_mrope.restype = ctypes.c_int
+        lib.vg_fused_qk_norm_rope_append.argtypes = [P] * 10 + [P, i32, i64, i32, i32, i32, i64, i64,
+                                                                i64, i64, i64, i64, f32, i32, i32, P]
+        lib.vg_fused_qk_norm_rope_append.restype = ctypes.c_int
+        lib.vg_fp8_block_gemm.argtypes = [P, P, P, P, P, i64, i64, i64, i32, P]
+        lib.vg_fp8_block_gemm.restype = ctypes.c_int
+        lib.vg_fp8_block_gemm_silu_mul_fp8.argtypes = [P, P, P, P, P, P, i64, i64, i64, i32, i32, P]
+        lib.vg_fp8_block_gemm_silu_mul_fp8.restype = ctypes.c_int
         lib.vg_status_string.argtypes = [ctypes.c_int]
         lib.vg_status_string.restype = ctypes.c_char_p
         lib.vg_abi_version.argtypes = []
@@ -320,6 +347,174 @@ def vg_silu_mul_nvfp4(q4, block_scale, gate_up, global_scale, stream=None,
         inter, _stream(stream)))
 
 
+def _on_current_device(*tensors):
+    """All tensors on the current CUDA device: the kernels are launched there,
+    on its current stream."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}: "
+                             "call under torch.cuda.device(tensor.device)")
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _sections(sections, positions):
+    """(ctypes array or None, number of axes, tokens) of a rotary position tensor."""
+    if sections is None:
+        if positions.dim() != 1:
+            raise ValueError("positions: expected a 1-D [T] tensor (or give sections)")
+        return None, 1, positions.shape[0]
+    n = len(sections)
+    if positions.dim() != 2 or positions.shape[0] != n:
+        raise ValueError(f"positions: expected a 2-D [{n}, T] tensor, one row per axis")
+    return (ctypes.c_int32 * n)(*sections), n, positions.shape[1]
+
+
+def _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_q_heads,
+               num_kv_heads, head_dim):
+    """Checked pointers and sizes that the multi-axis and cache forms share."""
+    import torch
+    bf16, _, f32 = _dtypes()
+    T, row = _rows(qkv, "qkv")
+    max_pos, D = _rows(cos_sin_cache, "cos_sin_cache")
+    sec, axes, tokens = _sections(sections, positions)
+    if row != (num_q_heads + 2 * num_kv_heads) * head_dim:
+        raise ValueError("qkv: expected (num_q_heads + 2 num_kv_heads) * head_dim columns")
+    if tokens != T:
+        raise ValueError("positions and qkv must have the same number of tokens")
+    if D != head_dim:
+        raise ValueError("cos_sin_cache: expected head_dim columns")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _shape(w, (head_dim,), name)
+    ptrs = [_ptr(q_weight, bf16, "q_weight"), _ptr(k_weight, bf16, "k_weight"),
+            _ptr(cos_sin_cache, f32, "cos_sin_cache"), _ptr(positions, (torch.int64,), "positions")]
+    return _ptr(qkv, bf16, "qkv"), ptrs, sec, axes, T, max_pos
+
+
+def vg_fused_qk_norm_mrope(qkv, q_weight, k_weight, cos_sin_cache, positions, sections,
+                           num_q_heads: int, num_kv_heads: int, head_dim: int, eps: float,
+                           is_neox: bool = True, interleaved: bool = False, stream=None):
+    """Per-head QK RMSNorm + rotation with several position axes, in place on
+    qkv [T, (Hq + 2 Hkv) * D] bf16.
+
+    positions int64 [axes, T]; sections: how many of the D/2 pairs each axis
+    turns (their sum is D/2), in runs or, ``interleaved``, taking turns.
+    q_weight and k_weight [D] bf16, or both None: the rotation only."""
+    q, ptrs, sec, axes, T, max_pos = _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions,
+                                                sections, num_q_heads, num_kv_heads, head_dim)
+    _on_current_device(qkv, q_weight, k_weight, cos_sin_cache, positions)
+    _check(load().vg_fused_qk_norm_mrope(
+        q, *ptrs, sec, axes, T, num_q_heads, num_kv_heads, head_dim, max_pos, eps,
+        1 if is_neox else 0, 1 if interleaved else 0, _stream(stream)))
+
+
+def vg_fused_qk_norm_rope_append(qkv, k_cache, v_cache, q_weight, k_weight, cos_sin_cache,
+                                 positions, slots, num_q_heads: int, num_kv_heads: int,
+                                 head_dim: int, eps: float, is_neox: bool = True, sections=None,
+                                 interleaved: bool = False, k_scale=None, v_scale=None,
+                                 stream=None):
+    """QK RMSNorm (or none) + rotation, Q in place, K and V into a paged cache.
+
+    k_cache, v_cache [pages, page_size, Hkv, D], bf16, or FP8 with k_scale and
+    v_scale fp32 [1] on the device; any strides in multiples of 8 elements
+    (the same for both) with contiguous head rows, so a [pages, Hkv,
+    page_size, D] cache is passed as its transposed view.  slots int64 [T]:
+    page * page_size + place in the page, distinct; a negative slot appends
+    nothing.  positions int64 [T], or [axes, T] with ``sections`` as for
+    vg_fused_qk_norm_mrope."""
+    import torch
+    bf16, fp8, f32 = _dtypes()
+    q, ptrs, sec, axes, T, max_pos = _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions,
+                                                sections, num_q_heads, num_kv_heads, head_dim)
+    kinds = bf16 if k_scale is None else fp8
+    for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if c.dtype not in kinds:
+            raise TypeError(f"{name}: dtype {c.dtype} not in {kinds}")
+        if not c.is_cuda:
+            raise ValueError(f"{name}: must be a CUDA tensor (there is no CPU path)")
+        if c.dim() != 4 or c.shape[2] != num_kv_heads or c.shape[3] != head_dim or c.stride(3) != 1:
+            raise ValueError(f"{name}: expected [pages, page_size, num_kv_heads, head_dim] with "
+                             "contiguous head rows")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    _shape(slots, (T,), "slots")
+    for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if x is not None and x.numel() != 1:
+            raise ValueError(f"{name}: expected one fp32 value on the device")
+    _on_current_device(qkv, k_cache, v_cache, q_weight, k_weight, cos_sin_cache, positions, slots,
+                       k_scale, v_scale)
+    pages, page_size = k_cache.shape[:2]
+    sp, st, sh, _ = k_cache.stride()
+    _check(load().vg_fused_qk_norm_rope_append(
+        q, k_cache.data_ptr(), v_cache.data_ptr(), *ptrs, _ptr(slots, (torch.int64,), "slots"),
+        _ptr(k_scale, f32, "k_scale"), _ptr(v_scale, f32, "v_scale"), sec, axes, T, num_q_heads,
+        num_kv_heads, head_dim, max_pos, pages, page_size, sp, st, sh, eps, 1 if is_neox else 0,
+        1 if interleaved else 0, _stream(stream)))
+
+
+def _block_gemm_args(a, a_scale, w, w_scale, a_options):
+    """Checked pointers and sizes of an FP8 product's operands."""
+    _, fp8, f32 = _dtypes()
+    T, K = _rows(a, "a")
+    N, K2 = _rows(w, "w")
+    if K2 != K:
+        raise ValueError("a and w must have the same number of columns")
+    kb = K // BLOCK
+    if a_options & COLUMN_MAJOR:
+        _shape(a_scale, (kb, (T + 3) // 4 * 4), "a_scale")
+    else:
+        _shape(a_scale, (T, kb), "a_scale")
+    _shape(w_scale, ((N + BLOCK - 1) // BLOCK, kb), "w_scale")
+    return [_ptr(a, fp8, "a"), _ptr(a_scale, f32, "a_scale"), _ptr(w, fp8, "w"),
+            _ptr(w_scale, f32, "w_scale")], T, N, K
+
+
+def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=None):
+    """FP8 product with a scale per block of 128 through the C ABI:
+    out [T,N] bf16 = (a * a_scale) (w * w_scale)^T.
+
+    a [T,K] fp8 with a_scale fp32 [T,K/128] (or, with COLUMN_MAJOR in
+    a_options, [K/128,T4] as the per-group ops write it); w [N,K] fp8 with
+    w_scale fp32 [ceil(N/128),K/128].  UE8M0 scales need no option."""
+    bf16, _, _ = _dtypes()
+    ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options)
+    _shape(out, (T, N), "out")
+    _on_current_device(out, a, a_scale, w, w_scale)
+    _check(load().vg_fp8_block_gemm(_ptr(out, bf16, "out"), *ptrs, T, N, K, a_options,
+                                    _stream(stream)))
+
+
+def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: int = 0,
+                                   out_options: int = 0, stream=None):
+    """Gated feed-forward projection through the C ABI: the gate and up
+    products, SiLU(gate) * up and its per-group-128 FP8 codes in one kernel.
+
+    a and a_scale as for vg_fp8_block_gemm; w [2I,K] fp8 (gate rows [0,I), up
+    rows [I,2I)) with w_scale [2I/128,K/128]; q [T,I] fp8, scale fp32
+    [T,I/128], or with COLUMN_MAJOR in out_options [I/128,T4]; UE8M0 in
+    out_options: power-of-two scales."""
+    _, fp8, f32 = _dtypes()
+    ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options)
+    inter = N // 2
+    if N % 2:
+        raise ValueError("w must have an even number of rows (gate, then up)")
+    _shape(q, (T, inter), "q")
+    if out_options & COLUMN_MAJOR:
+        _shape(scale, (inter // BLOCK, (T + 3) // 4 * 4), "scale")
+    else:
+        _shape(scale, (T, inter // BLOCK), "scale")
+    _on_current_device(q, scale, a, a_scale, w, w_scale)
+    _check(load().vg_fp8_block_gemm_silu_mul_fp8(
+        _ptr(q, fp8, "q"), _ptr(scale, f32, "scale"), *ptrs, T, inter, K, a_options, out_options,
+        _stream(stream)))
+
+
 def vg_device_status(reset: bool = False) -> int:
     """Flags the library's kernels left on the current device
     (DEVICE_WAIT_TIMEOUT: a bounded wait gave up; that call's outputs are
@@ -424,3 +619,22 @@ def silu_mul_nvfp4(gate_up, global_scale, stream=None):
     sf = torch.empty((T, two_i // 32), dtype=torch.float8_e4m3fn, device=gate_up.device)
     vg_silu_mul_nvfp4(q4, sf, gate_up, global_scale, stream)
     return q4, sf
+
+
+def fp8_block_gemm(a, a_scale, w, w_scale, a_options: int = 0, stream=None):
+    """Returns out bf16 [T,N]."""
+    import torch
+    out = torch.empty((a.shape[0], w.shape[0]), dtype=torch.bfloat16, device=a.device)
+    vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options, stream)
+    return out
+
+
+def fp8_block_gemm_silu_mul_fp8(a, a_scale, w, w_scale, a_options: int = 0, out_options: int = 0,
+                                stream=None):
+    """Returns (q float8_e4m3fn [T,I], scale)."""
+    import torch
+    T, inter = a.shape[0], w.shape[0] // 2
+    q = torch.empty((T, inter), dtype=torch.float8_e4m3fn, device=a.device)
+    s = _scale_out(PER_GROUP | out_options, T, inter, BLOCK, None, a.device)
+    vg_fp8_block_gemm_silu_mul_fp8(q, s, a, a_scale, w, w_scale, a_options, out_options, stream)
+    return q, s

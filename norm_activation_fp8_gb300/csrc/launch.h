@@ -158,7 +158,8 @@ MlaPlan plan_mla(int64_t T, int nq, int nkv, bool q_fp8, int sms);
 cudaError_t launch_mla_dual_norm(MlaArgs a, bool q_fp8, const MlaPlan &p, cudaStream_t s);
 uint32_t read_mla_status(bool reset);
 
-// QK norm + RoPE, in place on qkv [T, row] with row = (hq + 2 hkv) * D.
+// QK norm + RoPE on qkv [T, row] with row = (hq + 2 hkv) * D: in place, or
+// (slots set) Q in place and K, V into a paged cache.
 struct QkArgs {
   uint16_t *qkv;
   const uint16_t *qw;
@@ -168,14 +169,54 @@ struct QkArgs {
   int64_t T;
   int64_t row;           // elements per token row
   int64_t max_pos;
-  int32_t nh;            // heads normalised: hq + hkv
+  int32_t nh;            // heads a launch covers: hq + hkv, with a cache hq + 2 hkv
   int32_t hq;
   float eps;
   int32_t pf_ctas;       // tokens below this index prefetch their heads into L2
+  int32_t hqk;           // heads turned: hq + hkv
+  int32_t axes;          // position axes (1..4); pos is [axes, T]
+  uint32_t axis_map[8];  // axes > 1: two bits a pair, the axis it turns by
+  // paged cache (slots == nullptr: none); strides in elements
+  const int64_t *slots;  // [T]
+  void *k_cache;
+  void *v_cache;
+  const float *k_scale;  // fp32 [1]: e4m3 caches; nullptr: bf16
+  const float *v_scale;
+  int64_t num_slots;     // at most INT32_MAX
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  uint64_t cache_elems;  // elements from a cache's first to its last (debug checks)
+  int32_t page_size;
 };
-// Device status bit of the rope kernel: a position outside [0, max_pos).
+// Device status bits of the rope kernel: a position outside [0, max_pos), a
+// slot outside the cache.
 constexpr uint32_t kErrBadPosition = 2u;
+constexpr uint32_t kErrBadSlot = 8u;
 cudaError_t launch_qk_norm_rope(const QkArgs &a, int head_dim, bool neox, cudaStream_t s);
 uint32_t read_rope_status(bool reset);
+
+// FP8 product with a scale per block of 128: a [T, K] (tokens), w [rows, K]
+// (weights).  Plain: out [T, N] bf16, rows = N.  Gated: w is gate rows [0, N),
+// up rows [N, 2N); q [T, N] e4m3 and one scale per 128 columns.
+struct GemmArgs {
+  const uint8_t *a;
+  const float *a_scale;  // (t, b) at a_scale[t * a_ts + b * a_bs]
+  const uint8_t *w;
+  const float *w_scale;  // [ceil(rows / 128), K / 128]
+  uint16_t *out;
+  uint8_t *q;
+  float *scale;          // (t, g) at scale[t * s_ts + g * s_gs]
+  int64_t a_ts;
+  int64_t a_bs;
+  int64_t s_ts;
+  int64_t s_gs;
+  int32_t T;
+  int32_t N;             // output columns
+  int32_t K;
+  int32_t ue8m0;         // power-of-two output scales
+};
+cudaError_t launch_fp8_gemm(const GemmArgs &a, bool gated, int sms, cudaStream_t s);
+uint32_t read_gemm_status(bool reset);
 
 }  // namespace vg

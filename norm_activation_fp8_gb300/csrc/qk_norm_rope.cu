@@ -22,6 +22,14 @@
 // p = o * inv rounded once to bf16.  So p is within ~15u (2^-20 relative) of
 // the exact result, and its bf16 differs from the correctly rounded one only
 // where the exact value lies that close to a bf16 midpoint, by one ulp.
+//
+// Two further forms of the same kernel.  AXES: pair i turns by the position
+// on its axis, positions[axis(i), t]; the token's cos/sin row is put together
+// once per CTA in shared memory (every head of the token reads it), and the
+// heads read it from there.  APPEND: Q in place, K (normed, rotated) and V go
+// to their slot of a paged cache instead, as bf16 or as e4m3(value / scale)
+// from the fp32 value, so that the qkv row is read once and K and V are
+// written once.  A rotation without a norm takes weights of one and y = 1.
 #include "common.cuh"
 #include "launch.h"
 #include "row_norm.cuh"
@@ -46,6 +54,17 @@ __device__ __forceinline__ void load4f(const float *p, float (&v)[8], int at) {
   v[at] = a.x; v[at + 1] = a.y; v[at + 2] = a.z; v[at + 3] = a.w;
 }
 
+// The same from shared memory (the multi-axis row).
+__device__ __forceinline__ void lds4f(const float *p, float (&v)[8], int at) {
+  const float4 a = *reinterpret_cast<const float4 *>(p);
+  v[at] = a.x; v[at + 1] = a.y; v[at + 2] = a.z; v[at + 3] = a.w;
+}
+
+__device__ __forceinline__ void lds8f(const float *p, float (&v)[8]) {
+  lds4f(p, v, 0);
+  lds4f(p + 4, v, 4);
+}
+
 // Two elements of a*c -/+ b*s (Kahan), packed; a zero keeps the plain
 // expression's sign.  nb = -b for the minus form.
 __device__ __forceinline__ float2 kahan2x(float2 a, float2 c, float2 nb, float2 s) {
@@ -56,7 +75,36 @@ __device__ __forceinline__ float2 kahan2x(float2 a, float2 c, float2 nb, float2 
   return make_float2(e.x != 0.f ? o.x : f.x, e.y != 0.f ? o.y : f.y);
 }
 
-template <int G, bool NEOX>
+// Eight bf16 words' worth of fp32 values -> eight E4M3 codes of v * m.
+__device__ __forceinline__ uint2 quant8_scaled(const float *p, float m) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = p[k] * m;
+  return quant8(v);
+}
+
+// One head's two chunks of 8 (columns 8l and 8(l + G)) to its slot of a paged
+// cache: plain stores, so that L2 keeps the line for the attention that
+// reads it next.
+__device__ __forceinline__ void cache_store(const QkArgs &a, void *cache, int64_t at, int l, int g,
+                                            const uint4 &ca, const uint4 &cb) {
+  uint16_t *o = static_cast<uint16_t *>(cache) + at;
+  if (VG_ACCESS_OK(g_rope_status, o + 8 * l, 16, cache, 2ull * a.cache_elems))
+    *reinterpret_cast<uint4 *>(o + 8 * l) = ca;
+  if (VG_ACCESS_OK(g_rope_status, o + 8 * (l + g), 16, cache, 2ull * a.cache_elems))
+    *reinterpret_cast<uint4 *>(o + 8 * (l + g)) = cb;
+}
+
+__device__ __forceinline__ void cache_store(const QkArgs &a, void *cache, int64_t at, int l, int g,
+                                            const uint2 &ca, const uint2 &cb) {
+  uint8_t *o = static_cast<uint8_t *>(cache) + at;
+  if (VG_ACCESS_OK(g_rope_status, o + 8 * l, 8, cache, a.cache_elems))
+    *reinterpret_cast<uint2 *>(o + 8 * l) = ca;
+  if (VG_ACCESS_OK(g_rope_status, o + 8 * (l + g), 8, cache, a.cache_elems))
+    *reinterpret_cast<uint2 *>(o + 8 * (l + g)) = cb;
+}
+
+template <int G, bool NEOX, bool AXES, bool APPEND>
 __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
   constexpr int D = G * 16;
   const int lane = threadIdx.x & 31;
@@ -72,21 +120,61 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
     prefetch_l2(a.qkv + t * a.row + (int64_t)h0 * D, 2u * (uint32_t)(nh * D));
   }
   pdl_wait();
+  [[maybe_unused]] __shared__ __align__(16) float row_cs[AXES ? D : 4];
+  bool pos_ok = true;
+  if constexpr (AXES) {
+    // the axes' positions, then this token's cos/sin row, pair by pair
+    int64_t p4[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      p4[x] = x < a.axes ? a.pos[x * a.T + t] : 0;
+      pos_ok = pos_ok && p4[x] >= 0 && p4[x] < a.max_pos;
+    }
+    if (pos_ok)
+      for (int i = (int)threadIdx.x; i < D; i += (int)blockDim.x) {
+        const int pair = i & (D / 2 - 1);
+        const int x = (int)(a.axis_map[pair >> 4] >> (2 * (pair & 15))) & 3;
+        const int64_t p = x == 0 ? p4[0] : (x == 1 ? p4[1] : (x == 2 ? p4[2] : p4[3]));
+        row_cs[i] = __ldg(a.cache + p * D + i);
+      }
+  }
   // The head's loads do not depend on the token's position, so they go out
   // together with it (a head with a bad position is loaded but not stored);
   // only the cos/sin row waits for the position.
   const bool in_head = h < a.nh;
   uint16_t *head = a.qkv + t * a.row + (in_head ? (int64_t)h * D : 0);
   const uint16_t *w = h < a.hq ? a.qw : a.kw;
-  const int64_t pos = a.pos[t];
+  const bool norm = (!AXES && !APPEND) || (w != nullptr && h < a.hqk);
+  const int64_t pos = AXES ? 0 : a.pos[t];
+  const int64_t slot = APPEND ? a.slots[t] : 0;
   // chunk 0 of the lane: l (first half of the head), chunk 1: l + G
   const uint4 xa = in_head ? ld_stream(head + l * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
   const uint4 xb = in_head ? ld_stream(head + (l + G) * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
-  const uint4 wa = in_head ? ld_keep(w + l * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
-  const uint4 wb = in_head ? ld_keep(w + (l + G) * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
-  const bool live = in_head && pos >= 0 && pos < a.max_pos;  // same for the head's lanes
+  constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones: a rotation without a norm
+  const uint4 ones = make_uint4(kOnes, kOnes, kOnes, kOnes);
+  const uint4 wa = in_head && norm ? ld_keep(w + l * kElemsPerChunk) : ones;
+  const uint4 wb = in_head && norm ? ld_keep(w + (l + G) * kElemsPerChunk) : ones;
+  if constexpr (!AXES) pos_ok = pos >= 0 && pos < a.max_pos;
+  const bool live = in_head && pos_ok;  // same for the head's lanes
   if (in_head && !live && l == 0) atomicOr(&g_rope_status, kErrBadPosition);
   pdl_launch_dependents();
+  // Where a K or V head goes: the slot's page, the token in it, the head.
+  [[maybe_unused]] int64_t cache_at = 0;
+  [[maybe_unused]] bool to_cache = false;
+  if constexpr (APPEND) {
+    if (live && h >= a.hq && slot >= 0) {
+      if (slot < a.num_slots) {
+        const uint32_t page = (uint32_t)slot / (uint32_t)a.page_size;
+        const uint32_t in_page = (uint32_t)slot - page * (uint32_t)a.page_size;
+        const int kv = h < a.hqk ? h - a.hq : h - a.hqk;
+        cache_at = (int64_t)page * a.page_stride + (int64_t)in_page * a.token_stride +
+                   (int64_t)kv * a.head_stride;
+        to_cache = true;
+      } else if (l == 0) {
+        atomicOr(&g_rope_status, kErrBadSlot);
+      }
+    }
+  }
   float2 ta[4], tb[4];
   float cmax;
   RowAcc acc;
@@ -95,7 +183,8 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
   float ss = acc.ss.x + acc.ss.y;
 #pragma unroll
   for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-  const float y = rsqrtf(fmaf(ss, 1.0f / (float)D, a.eps));
+  const float y = norm ? rsqrtf(fmaf(ss, 1.0f / (float)D, a.eps)) : 1.0f;
+  if constexpr (AXES) __syncthreads();  // row_cs is complete
 
   // mine[0..7]: chunk 0, mine[8..15]: chunk 1; other: each element's pair
   // partner; c, s: its pair's cos and sin; submask bit k: minus sign
@@ -107,7 +196,13 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
     mine[8 + 2 * i] = tb[i].x;
     mine[8 + 2 * i + 1] = tb[i].y;
   }
-  const float *cs = a.cache + (live ? pos * D : 0);
+  const float *cs = AXES ? row_cs : a.cache + (live ? pos * D : 0);
+  const auto ld8 = [](const float *p, float(&v)[8]) {
+    if constexpr (AXES) lds8f(p, v); else load8f(p, v);
+  };
+  const auto ld4 = [](const float *p, float(&v)[8], int at) {
+    if constexpr (AXES) lds4f(p, v, at); else load4f(p, v, at);
+  };
   uint32_t submask;
   if (NEOX) {  // element k of chunk 0 pairs with element k of chunk 1: pair 8l + k
 #pragma unroll
@@ -117,8 +212,8 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
     }
     float c8[8] = {}, s8[8] = {};
     if (live) {
-      load8f(cs + 8 * l, c8);
-      load8f(cs + D / 2 + 8 * l, s8);
+      ld8(cs + 8 * l, c8);
+      ld8(cs + D / 2 + 8 * l, s8);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -131,10 +226,10 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
     for (int k = 0; k < 16; ++k) other[k] = mine[k ^ 1];
     float c4[8] = {}, s4[8] = {};
     if (live) {
-      load4f(cs + 4 * l, c4, 0);
-      load4f(cs + 4 * (l + G), c4, 4);
-      load4f(cs + D / 2 + 4 * l, s4, 0);
-      load4f(cs + D / 2 + 4 * (l + G), s4, 4);
+      ld4(cs + 4 * l, c4, 0);
+      ld4(cs + 4 * (l + G), c4, 4);
+      ld4(cs + D / 2 + 4 * l, s4, 0);
+      ld4(cs + D / 2 + 4 * (l + G), s4, 4);
     }
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -155,6 +250,25 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
     p[k] = pp.x;
     p[k + 1] = pp.y;
   }
+  if constexpr (APPEND) {
+    if (to_cache) {  // K: the rotated values; V: the row's own bits, or its values scaled
+      const bool is_v = h >= a.hqk;
+      void *cache = is_v ? a.v_cache : a.k_cache;
+      if (a.k_scale == nullptr) {
+        const uint4 ka = make_uint4(pack_bf16x2_rn(p[0], p[1]), pack_bf16x2_rn(p[2], p[3]),
+                                    pack_bf16x2_rn(p[4], p[5]), pack_bf16x2_rn(p[6], p[7]));
+        const uint4 kb = make_uint4(pack_bf16x2_rn(p[8], p[9]), pack_bf16x2_rn(p[10], p[11]),
+                                    pack_bf16x2_rn(p[12], p[13]), pack_bf16x2_rn(p[14], p[15]));
+        cache_store(a, cache, cache_at, l, G, is_v ? xa : ka, is_v ? xb : kb);
+      } else {
+        const float m = __frcp_rn(__ldg(is_v ? a.v_scale : a.k_scale));
+        // mine holds V's own values: a V head's weights are ones
+        cache_store(a, cache, cache_at, l, G, quant8_scaled(is_v ? mine : p, m),
+                    quant8_scaled(is_v ? mine + 8 : p + 8, m));
+      }
+    }
+    if (h >= a.hq) return;
+  }
   const uint4 oa = make_uint4(pack_bf16x2_rn(p[0], p[1]), pack_bf16x2_rn(p[2], p[3]),
                               pack_bf16x2_rn(p[4], p[5]), pack_bf16x2_rn(p[6], p[7]));
   const uint4 ob = make_uint4(pack_bf16x2_rn(p[8], p[9]), pack_bf16x2_rn(p[10], p[11]),
@@ -167,14 +281,25 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
 }
 
 // One token per CTA: up to 16 warps of heads; blockIdx.y covers the rest.
-template <int G>
-cudaError_t launch_g(const QkArgs &a, bool neox, cudaStream_t s) {
+template <int G, bool AXES, bool APPEND>
+cudaError_t launch_form(const QkArgs &a, bool neox, cudaStream_t s) {
   const int heads_per_warp = 32 / G;
   int warps = (a.nh + heads_per_warp - 1) / heads_per_warp;
   if (warps > 16) warps = 16;
   const dim3 grid((unsigned)a.T, (unsigned)((a.nh + warps * heads_per_warp - 1) / (warps * heads_per_warp)));
-  return neox ? launch_pdl(qk_norm_rope_kernel<G, true>, grid, dim3(warps * 32), 0, s, a)
-              : launch_pdl(qk_norm_rope_kernel<G, false>, grid, dim3(warps * 32), 0, s, a);
+  return neox ? launch_pdl(qk_norm_rope_kernel<G, true, AXES, APPEND>, grid, dim3(warps * 32), 0, s, a)
+              : launch_pdl(qk_norm_rope_kernel<G, false, AXES, APPEND>, grid, dim3(warps * 32), 0, s, a);
+}
+
+template <int G>
+cudaError_t launch_g(const QkArgs &a, bool neox, cudaStream_t s) {
+  if (a.slots)
+    return a.axes > 1 ? launch_form<G, true, true>(a, neox, s) : launch_form<G, false, true>(a, neox, s);
+  // the plain form has weights and one axis; without weights the multi-axis
+  // form turns by its one axis
+  const bool weights = (a.hq == 0 || a.qw) && (a.hqk == a.hq || a.kw);
+  return a.axes > 1 || !weights ? launch_form<G, true, false>(a, neox, s)
+                                : launch_form<G, false, false>(a, neox, s);
 }
 
 }  // namespace

@@ -312,11 +312,187 @@ vg_status mla_dual_norm(uint16_t *q_out, uint8_t *q_fp8, float *q_scale, uint16_
                                                                                : VG_ERR_CUDA;
 }
 
+// What the three rotary entry points share: the sizes they refuse ...
+vg_status check_heads(int64_t T, int32_t hq, int32_t hkv, int32_t D, int64_t max_position) {
+  if (T < 0 || T > INT32_MAX || hq < 0 || hkv < 0 || hq + hkv < 1 || hq + 2LL * hkv > 4096 ||
+      (D != 64 && D != 128 && D != 256) || max_position < 1)
+    return VG_ERR_BAD_SHAPE;
+  return VG_OK;
+}
+
+// ... their common arguments (one position axis, no cache) ...
+QkArgs qk_args(uint16_t *qkv, const uint16_t *qw, const uint16_t *kw, const float *cache,
+               const int64_t *positions, int64_t T, int32_t hq, int32_t hkv, int32_t D,
+               int64_t max_position, float eps) {
+  QkArgs a{};
+  a.qkv = qkv;
+  a.qw = qw;
+  a.kw = kw;
+  a.cache = cache;
+  a.pos = positions;
+  a.T = T;
+  a.row = (int64_t)(hq + 2 * hkv) * D;
+  a.max_pos = max_position;
+  a.nh = a.hqk = hq + hkv;
+  a.hq = hq;
+  a.eps = eps;
+  a.axes = 1;
+  return a;
+}
+
+// ... the axis each of the D/2 pairs turns by: in runs of sections[x] pairs,
+// or taking turns, where an axis that has had its share (and the remaining
+// turns) leaves the pair to the first axis ...
+vg_status set_axes(QkArgs &a, const int32_t *sections, int32_t axes, int32_t D, bool interleaved) {
+  if (axes < 1 || axes > 4 || (axes > 1 && !sections)) return VG_ERR_BAD_SHAPE;
+  const int half = D / 2;
+  a.axes = axes;
+  if (!sections) return VG_OK;
+  int64_t sum = 0;
+  for (int x = 0; x < axes; ++x) {
+    if (sections[x] < 0 || sections[x] > half) return VG_ERR_BAD_SHAPE;
+    // the last turn of an axis that takes turns lies inside the head
+    if (interleaved && x > 0 && sections[x] > 0 && axes * (sections[x] - 1) + x >= half)
+      return VG_ERR_BAD_SHAPE;
+    sum += sections[x];
+  }
+  if (sum != half) return VG_ERR_BAD_SHAPE;
+  int end = sections[0], run = 0;
+  for (int i = 0; i < half; ++i) {
+    while (!interleaved && i >= end) end += sections[++run];
+    const int turn = i % axes;
+    const int x = !interleaved ? run : (i / axes < sections[turn] ? turn : 0);
+    a.axis_map[i / 16] |= (uint32_t)x << (2 * (i % 16));
+  }
+  return VG_OK;
+}
+
+// ... the cache's geometry: whole chunks of 8 elements, and no element that
+// belongs to two (page, token, head) places ...
+vg_status set_cache(QkArgs &a, int64_t pages, int64_t page_size, int64_t page_stride,
+                    int64_t token_stride, int64_t head_stride, int32_t hkv, int32_t D) {
+  if (hkv < 1 || pages < 1 || page_size < 1 || page_size > INT32_MAX || pages > INT32_MAX / page_size)
+    return VG_ERR_BAD_SHAPE;
+  struct Dim {
+    int64_t n, stride;
+  } d[3] = {{pages, page_stride}, {page_size, token_stride}, {hkv, head_stride}};
+  int64_t reach = D;  // elements from the first to the last place so far
+  bool used[3] = {};
+  for (int k = 0; k < 3; ++k) {  // the dimensions, smallest stride first
+    int m = -1;
+    for (int x = 0; x < 3; ++x)
+      if (!used[x] && d[x].n > 1 && (m < 0 || d[x].stride < d[m].stride)) m = x;
+    if (m < 0) break;
+    used[m] = true;
+    if (d[m].stride < reach || d[m].stride % 8 != 0 ||
+        d[m].stride > (INT64_MAX / 4 - reach) / d[m].n)
+      return VG_ERR_BAD_SHAPE;
+    reach += (d[m].n - 1) * d[m].stride;
+  }
+  a.num_slots = pages * page_size;
+  a.page_size = (int32_t)page_size;
+  a.page_stride = pages > 1 ? page_stride : 0;
+  a.token_stride = page_size > 1 ? token_stride : 0;
+  a.head_stride = hkv > 1 ? head_stride : 0;
+  a.cache_elems = (uint64_t)reach;
+  return VG_OK;
+}
+
+// ... a norm for Q without one for K, or the reverse ...
+bool half_weighted(const QkArgs &a) {
+  return a.hq > 0 && a.hqk > a.hq && (a.qw == nullptr) != (a.kw == nullptr);
+}
+
+// ... and the checks of the pointers that all of them have, and the launch.
+vg_status run_qk(QkArgs a, int32_t D, int32_t is_neox, vg_stream_t stream) {
+  if (misaligned(a.qkv, 16) || misaligned(a.qw, 16) || misaligned(a.kw, 16) ||
+      misaligned(a.cache, 16) || misaligned(a.pos, 8))
+    return VG_ERR_MISALIGNED;
+  int sms = 0;
+  const vg_status st = check_device(&sms);
+  if (st != VG_OK) return st;
+  clear_stale_error();
+  a.pf_ctas = 2 * sms;
+  return launch_qk_norm_rope(a, D, is_neox != 0, (cudaStream_t)stream) == cudaSuccess ? VG_OK
+                                                                                        : VG_ERR_CUDA;
+}
+
+// The sizes and options both FP8 products refuse: whole scale blocks along K,
+// rows of codes this library writes (at most VG_MAX_ROW columns), output rows
+// of whole 16-byte chunks.
+vg_status check_gemm(int64_t T, int64_t N, int64_t K, int64_t max_n, int32_t a_options,
+                     int32_t out_options) {
+  if ((a_options & ~VG_SCALE_COLUMN_MAJOR) != 0 ||
+      (out_options & ~(VG_SCALE_COLUMN_MAJOR | VG_SCALE_UE8M0)) != 0)
+    return VG_ERR_BAD_MODE;
+  if (T < 0 || T > VG_MAX_GEMM_TOKENS || N < 8 || N % 8 != 0 || N > max_n || K < 1 || K > VG_MAX_ROW)
+    return VG_ERR_BAD_SHAPE;
+  return K % 128 == 0 ? VG_OK : VG_ERR_BAD_GROUP;
+}
+
+vg_status run_gemm(GemmArgs a, bool gated, int64_t T, int64_t N, int64_t K, int32_t a_options,
+                   int32_t out_options, vg_stream_t stream) {
+  if (misaligned(a.a, 16) || misaligned(a.w, 16) || misaligned(a.out, 16) || misaligned(a.q, 16) ||
+      misaligned(a.a_scale, 4) || misaligned(a.w_scale, 4) || misaligned(a.scale, 4))
+    return VG_ERR_MISALIGNED;
+  int sms = 0;
+  const vg_status st = check_device(&sms);
+  if (st != VG_OK) return st;
+  clear_stale_error();
+  const int64_t t4 = (T + 3) / 4 * 4;
+  const bool a_col = (a_options & VG_SCALE_COLUMN_MAJOR) != 0;
+  const bool s_col = (out_options & VG_SCALE_COLUMN_MAJOR) != 0;
+  a.a_ts = a_col ? 1 : K / 128;
+  a.a_bs = a_col ? t4 : 1;
+  a.s_ts = s_col ? 1 : N / 128;
+  a.s_gs = s_col ? t4 : 1;
+  a.ue8m0 = (out_options & VG_SCALE_UE8M0) != 0;
+  a.T = (int32_t)T;
+  a.N = (int32_t)N;
+  a.K = (int32_t)K;
+  return launch_fp8_gemm(a, gated, sms, (cudaStream_t)stream) == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+}
+
 }  // namespace
 
 }  // namespace vg
 
 extern "C" {
+
+vg_status vg_fp8_block_gemm(uint16_t *out, const uint8_t *a, const float *a_scale,
+                            const uint8_t *w, const float *w_scale, int64_t num_tokens, int64_t n,
+                            int64_t k, int32_t a_options, vg_stream_t stream) {
+  const vg_status st = vg::check_gemm(num_tokens, n, k, VG_MAX_GEMM_COLUMNS, a_options, 0);
+  if (st != VG_OK || num_tokens == 0) return st;
+  if (!out || !a || !a_scale || !w || !w_scale) return VG_ERR_NULL_PTR;
+  vg::GemmArgs g{};
+  g.a = a;
+  g.a_scale = a_scale;
+  g.w = w;
+  g.w_scale = w_scale;
+  g.out = out;
+  return vg::run_gemm(g, false, num_tokens, n, k, a_options, 0, stream);
+}
+
+vg_status vg_fp8_block_gemm_silu_mul_fp8(uint8_t *q, float *scale, const uint8_t *a,
+                                         const float *a_scale, const uint8_t *w,
+                                         const float *w_scale, int64_t num_tokens, int64_t inter,
+                                         int64_t k, int32_t a_options, int32_t out_options,
+                                         vg_stream_t stream) {
+  const vg_status st = vg::check_gemm(num_tokens, inter, k, VG_MAX_ROW, a_options, out_options);
+  if (st != VG_OK) return st;
+  if (inter % 128 != 0) return VG_ERR_BAD_GROUP;
+  if (num_tokens == 0) return VG_OK;
+  if (!q || !scale || !a || !a_scale || !w || !w_scale) return VG_ERR_NULL_PTR;
+  vg::GemmArgs g{};
+  g.a = a;
+  g.a_scale = a_scale;
+  g.w = w;
+  g.w_scale = w_scale;
+  g.q = q;
+  g.scale = scale;
+  return vg::run_gemm(g, true, num_tokens, inter, k, a_options, out_options, stream);
+}
 
 vg_status vg_fused_mla_dual_rms_norm(uint16_t *q_out, uint16_t *kv_out, const uint16_t *q_c,
                                      int64_t q_stride, const uint16_t *q_weight,
@@ -488,38 +664,62 @@ vg_status vg_fused_qk_norm_rope(uint16_t *qkv, const uint16_t *q_weight, const u
                                 int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
                                 int32_t head_dim, int64_t max_position, float eps, int32_t is_neox,
                                 vg_stream_t stream) {
-  if (num_tokens < 0 || num_tokens > INT32_MAX || num_q_heads < 0 || num_kv_heads < 0 ||
-      num_q_heads + num_kv_heads < 1 || num_q_heads + 2LL * num_kv_heads > 4096 ||
-      (head_dim != 64 && head_dim != 128 && head_dim != 256) || max_position < 1)
-    return VG_ERR_BAD_SHAPE;
-  if (num_tokens == 0) return VG_OK;
+  vg_status st = vg::check_heads(num_tokens, num_q_heads, num_kv_heads, head_dim, max_position);
+  if (st != VG_OK || num_tokens == 0) return st;
   if (!qkv || !cos_sin_cache || !positions || (num_q_heads > 0 && !q_weight) ||
       (num_kv_heads > 0 && !k_weight))
     return VG_ERR_NULL_PTR;
-  if (vg::misaligned(qkv, 16) || vg::misaligned(q_weight, 16) || vg::misaligned(k_weight, 16) ||
-      vg::misaligned(cos_sin_cache, 16) || vg::misaligned(positions, 8))
-    return VG_ERR_MISALIGNED;
-  int sms = 0;
-  vg_status st = vg::check_device(&sms);
-  if (st != VG_OK) return st;
-  vg::clear_stale_error();
+  const vg::QkArgs a = vg::qk_args(qkv, q_weight, k_weight, cos_sin_cache, positions, num_tokens,
+                                   num_q_heads, num_kv_heads, head_dim, max_position, eps);
+  return vg::run_qk(a, head_dim, is_neox, stream);
+}
 
-  vg::QkArgs a{};
-  a.pf_ctas = 2 * sms;
-  a.qkv = qkv;
-  a.qw = q_weight;
-  a.kw = k_weight;
-  a.cache = cos_sin_cache;
-  a.pos = positions;
-  a.T = num_tokens;
-  a.row = (int64_t)(num_q_heads + 2 * num_kv_heads) * head_dim;
-  a.max_pos = max_position;
-  a.nh = num_q_heads + num_kv_heads;
-  a.hq = num_q_heads;
-  a.eps = eps;
-  return vg::launch_qk_norm_rope(a, head_dim, is_neox != 0, (cudaStream_t)stream) == cudaSuccess
-             ? VG_OK
-             : VG_ERR_CUDA;
+vg_status vg_fused_qk_norm_mrope(uint16_t *qkv, const uint16_t *q_weight, const uint16_t *k_weight,
+                                 const float *cos_sin_cache, const int64_t *positions,
+                                 const int32_t *sections, int32_t num_axes, int64_t num_tokens,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int64_t max_position, float eps, int32_t is_neox,
+                                 int32_t interleaved, vg_stream_t stream) {
+  vg_status st = vg::check_heads(num_tokens, num_q_heads, num_kv_heads, head_dim, max_position);
+  if (st != VG_OK) return st;
+  vg::QkArgs a = vg::qk_args(qkv, q_weight, k_weight, cos_sin_cache, positions, num_tokens,
+                             num_q_heads, num_kv_heads, head_dim, max_position, eps);
+  if ((st = vg::set_axes(a, sections, num_axes, head_dim, interleaved != 0)) != VG_OK) return st;
+  if (num_tokens == 0) return VG_OK;
+  if (!qkv || !cos_sin_cache || !positions || vg::half_weighted(a)) return VG_ERR_NULL_PTR;
+  return vg::run_qk(a, head_dim, is_neox, stream);
+}
+
+vg_status vg_fused_qk_norm_rope_append(
+    uint16_t *qkv, void *k_cache, void *v_cache, const uint16_t *q_weight,
+    const uint16_t *k_weight, const float *cos_sin_cache, const int64_t *positions,
+    const int64_t *slots, const float *k_scale, const float *v_scale, const int32_t *sections,
+    int32_t num_axes, int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int64_t max_position, int64_t num_pages, int64_t page_size,
+    int64_t page_stride, int64_t token_stride, int64_t head_stride, float eps, int32_t is_neox,
+    int32_t interleaved, vg_stream_t stream) {
+  vg_status st = vg::check_heads(num_tokens, num_q_heads, num_kv_heads, head_dim, max_position);
+  if (st != VG_OK) return st;
+  vg::QkArgs a = vg::qk_args(qkv, q_weight, k_weight, cos_sin_cache, positions, num_tokens,
+                             num_q_heads, num_kv_heads, head_dim, max_position, eps);
+  if ((st = vg::set_axes(a, sections, num_axes, head_dim, interleaved != 0)) != VG_OK ||
+      (st = vg::set_cache(a, num_pages, page_size, page_stride, token_stride, head_stride,
+                          num_kv_heads, head_dim)) != VG_OK)
+    return st;
+  if (num_tokens == 0) return VG_OK;
+  if (!qkv || !k_cache || !v_cache || !cos_sin_cache || !positions || !slots ||
+      vg::half_weighted(a) || ((k_scale == nullptr) != (v_scale == nullptr)))
+    return VG_ERR_NULL_PTR;
+  if (vg::misaligned(k_cache, 16) || vg::misaligned(v_cache, 16) || vg::misaligned(slots, 8) ||
+      vg::misaligned(k_scale, 4) || vg::misaligned(v_scale, 4))
+    return VG_ERR_MISALIGNED;
+  a.nh = num_q_heads + 2 * num_kv_heads;
+  a.slots = slots;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return vg::run_qk(a, head_dim, is_neox, stream);
 }
 
 vg_status vg_silu_mul_fp8(uint8_t *q, float *scale, const uint16_t *gate_up, int64_t num_tokens,
@@ -591,10 +791,12 @@ vg_status vg_silu_mul_nvfp4(uint8_t *q4, uint8_t *block_scale, const uint16_t *g
 vg_status vg_device_status(uint32_t *flags, int32_t reset) {
   if (!flags) return VG_ERR_NULL_PTR;
   const uint32_t v = vg::read_norm_status(reset != 0), w = vg::read_silu_status(reset != 0),
-                 r = vg::read_rope_status(reset != 0), m = vg::read_mla_status(reset != 0);
-  if (v == 0xFFFFFFFFu || w == 0xFFFFFFFFu || r == 0xFFFFFFFFu || m == 0xFFFFFFFFu)
+                 r = vg::read_rope_status(reset != 0), m = vg::read_mla_status(reset != 0),
+                 g = vg::read_gemm_status(reset != 0);
+  if (v == 0xFFFFFFFFu || w == 0xFFFFFFFFu || r == 0xFFFFFFFFu || m == 0xFFFFFFFFu ||
+      g == 0xFFFFFFFFu)
     return VG_ERR_CUDA;
-  *flags = v | w | r | m;
+  *flags = v | w | r | m | g;
   return VG_OK;
 }
 
