@@ -47,6 +47,7 @@ Convenience wrappers that allocate the outputs with torch:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -347,20 +348,39 @@ def vg_silu_mul_nvfp4(q4, block_scale, gate_up, global_scale, stream=None,
         inter, _stream(stream)))
 
 
-def _on_current_device(*tensors):
-    """All tensors on the current CUDA device: the kernels are launched there,
-    on its current stream."""
+def _arg(t, dtypes, name, dev, contiguous=True):
+    """Device pointer of a tensor on the current device (or None): one pass of
+    cheap checks, the reasons only when one fails."""
+    if t is None:
+        return None
+    if t.dtype in dtypes and t.get_device() == dev and (not contiguous or t.is_contiguous()):
+        return t.data_ptr()
+    if contiguous or t.dtype not in dtypes or not t.is_cuda:
+        _ptr(t if contiguous else t[:0], dtypes, name)
+    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}: call under "
+                     "torch.cuda.device(tensor.device)")
+
+
+def _here(stream):
+    """(current device, raw stream) of a call; without CUDA a device that no tensor is on."""
     import torch
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}: "
-                             "call under torch.cuda.device(tensor.device)")
+    if not torch.cuda.is_available():
+        return -2, 0
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, _stream(stream)
 
 
 def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+@functools.cache
+def _kinds():
+    import torch
+    return *_dtypes(), (torch.int64,)
 
 
 def _sections(sections, positions):
@@ -376,10 +396,9 @@ def _sections(sections, positions):
 
 
 def _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_q_heads,
-               num_kv_heads, head_dim):
+               num_kv_heads, head_dim, dev):
     """Checked pointers and sizes that the multi-axis and cache forms share."""
-    import torch
-    bf16, _, f32 = _dtypes()
+    bf16, _, f32, i64 = _kinds()
     T, row = _rows(qkv, "qkv")
     max_pos, D = _rows(cos_sin_cache, "cos_sin_cache")
     sec, axes, tokens = _sections(sections, positions)
@@ -389,12 +408,13 @@ def _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_
         raise ValueError("positions and qkv must have the same number of tokens")
     if D != head_dim:
         raise ValueError("cos_sin_cache: expected head_dim columns")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _shape(w, (head_dim,), name)
-    ptrs = [_ptr(q_weight, bf16, "q_weight"), _ptr(k_weight, bf16, "k_weight"),
-            _ptr(cos_sin_cache, f32, "cos_sin_cache"), _ptr(positions, (torch.int64,), "positions")]
-    return _ptr(qkv, bf16, "qkv"), ptrs, sec, axes, T, max_pos
+    if q_weight is not None:
+        _shape(q_weight, (head_dim,), "q_weight")
+    if k_weight is not None:
+        _shape(k_weight, (head_dim,), "k_weight")
+    return (_arg(qkv, bf16, "qkv", dev), _arg(q_weight, bf16, "q_weight", dev),
+            _arg(k_weight, bf16, "k_weight", dev), _arg(cos_sin_cache, f32, "cos_sin_cache", dev),
+            _arg(positions, i64, "positions", dev), sec, axes, T, max_pos)
 
 
 def vg_fused_qk_norm_mrope(qkv, q_weight, k_weight, cos_sin_cache, positions, sections,
@@ -406,12 +426,13 @@ def vg_fused_qk_norm_mrope(qkv, q_weight, k_weight, cos_sin_cache, positions, se
     positions int64 [axes, T]; sections: how many of the D/2 pairs each axis
     turns (their sum is D/2), in runs or, ``interleaved``, taking turns.
     q_weight and k_weight [D] bf16, or both None: the rotation only."""
-    q, ptrs, sec, axes, T, max_pos = _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions,
-                                                sections, num_q_heads, num_kv_heads, head_dim)
-    _on_current_device(qkv, q_weight, k_weight, cos_sin_cache, positions)
-    _check(load().vg_fused_qk_norm_mrope(
-        q, *ptrs, sec, axes, T, num_q_heads, num_kv_heads, head_dim, max_pos, eps,
-        1 if is_neox else 0, 1 if interleaved else 0, _stream(stream)))
+    dev, raw = _here(stream)
+    q, qw, kw, table, pos, sec, axes, T, max_pos = _rope_args(
+        qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_q_heads, num_kv_heads,
+        head_dim, dev)
+    _check((_lib or load()).vg_fused_qk_norm_mrope(
+        q, qw, kw, table, pos, sec, axes, T, num_q_heads, num_kv_heads, head_dim, max_pos, eps,
+        1 if is_neox else 0, 1 if interleaved else 0, raw))
 
 
 def vg_fused_qk_norm_rope_append(qkv, k_cache, v_cache, q_weight, k_weight, cos_sin_cache,
@@ -428,51 +449,41 @@ def vg_fused_qk_norm_rope_append(qkv, k_cache, v_cache, q_weight, k_weight, cos_
     page * page_size + place in the page, distinct; a negative slot appends
     nothing.  positions int64 [T], or [axes, T] with ``sections`` as for
     vg_fused_qk_norm_mrope."""
-    import torch
-    bf16, fp8, f32 = _dtypes()
-    q, ptrs, sec, axes, T, max_pos = _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions,
-                                                sections, num_q_heads, num_kv_heads, head_dim)
-    kinds = bf16 if k_scale is None else fp8
-    for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if c.dtype not in kinds:
-            raise TypeError(f"{name}: dtype {c.dtype} not in {kinds}")
-        if not c.is_cuda:
-            raise ValueError(f"{name}: must be a CUDA tensor (there is no CPU path)")
-        if c.dim() != 4 or c.shape[2] != num_kv_heads or c.shape[3] != head_dim or c.stride(3) != 1:
-            raise ValueError(f"{name}: expected [pages, page_size, num_kv_heads, head_dim] with "
-                             "contiguous head rows")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    bf16, fp8, f32, i64 = _kinds()
+    dev, raw = _here(stream)
+    q, qw, kw, table, pos, sec, axes, T, max_pos = _rope_args(
+        qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_q_heads, num_kv_heads,
+        head_dim, dev)
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[2] != num_kv_heads or shape[3] != head_dim or strides[3] != 1:
+        raise ValueError("k_cache: expected [pages, page_size, num_kv_heads, head_dim] with "
+                         "contiguous head rows")
+    if shape != v_cache.shape or strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must have the same shape and strides")
     _shape(slots, (T,), "slots")
-    for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if x is not None and x.numel() != 1:
-            raise ValueError(f"{name}: expected one fp32 value on the device")
-    _on_current_device(qkv, k_cache, v_cache, q_weight, k_weight, cos_sin_cache, positions, slots,
-                       k_scale, v_scale)
-    pages, page_size = k_cache.shape[:2]
-    sp, st, sh, _ = k_cache.stride()
-    _check(load().vg_fused_qk_norm_rope_append(
-        q, k_cache.data_ptr(), v_cache.data_ptr(), *ptrs, _ptr(slots, (torch.int64,), "slots"),
-        _ptr(k_scale, f32, "k_scale"), _ptr(v_scale, f32, "v_scale"), sec, axes, T, num_q_heads,
-        num_kv_heads, head_dim, max_pos, pages, page_size, sp, st, sh, eps, 1 if is_neox else 0,
-        1 if interleaved else 0, _stream(stream)))
+    if k_scale is not None and k_scale.numel() != 1 or v_scale is not None and v_scale.numel() != 1:
+        raise ValueError("k_scale and v_scale: expected one fp32 value on the device")
+    kinds = bf16 if k_scale is None and v_scale is None else fp8
+    _check((_lib or load()).vg_fused_qk_norm_rope_append(
+        q, _arg(k_cache, kinds, "k_cache", dev, False), _arg(v_cache, kinds, "v_cache", dev, False),
+        qw, kw, table, pos, _arg(slots, i64, "slots", dev), _arg(k_scale, f32, "k_scale", dev),
+        _arg(v_scale, f32, "v_scale", dev), sec, axes, T, num_q_heads, num_kv_heads, head_dim,
+        max_pos, shape[0], shape[1], strides[0], strides[1], strides[2], eps, 1 if is_neox else 0,
+        1 if interleaved else 0, raw))
 
 
-def _block_gemm_args(a, a_scale, w, w_scale, a_options):
+def _block_gemm_args(a, a_scale, w, w_scale, a_options, dev):
     """Checked pointers and sizes of an FP8 product's operands."""
-    _, fp8, f32 = _dtypes()
+    _, fp8, f32, _ = _kinds()
     T, K = _rows(a, "a")
     N, K2 = _rows(w, "w")
     if K2 != K:
         raise ValueError("a and w must have the same number of columns")
     kb = K // BLOCK
-    if a_options & COLUMN_MAJOR:
-        _shape(a_scale, (kb, (T + 3) // 4 * 4), "a_scale")
-    else:
-        _shape(a_scale, (T, kb), "a_scale")
+    _shape(a_scale, (kb, (T + 3) // 4 * 4) if a_options & COLUMN_MAJOR else (T, kb), "a_scale")
     _shape(w_scale, ((N + BLOCK - 1) // BLOCK, kb), "w_scale")
-    return [_ptr(a, fp8, "a"), _ptr(a_scale, f32, "a_scale"), _ptr(w, fp8, "w"),
-            _ptr(w_scale, f32, "w_scale")], T, N, K
+    return (_arg(a, fp8, "a", dev), _arg(a_scale, f32, "a_scale", dev), _arg(w, fp8, "w", dev),
+            _arg(w_scale, f32, "w_scale", dev)), T, N, K
 
 
 def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=None):
@@ -482,12 +493,11 @@ def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=No
     a [T,K] fp8 with a_scale fp32 [T,K/128] (or, with COLUMN_MAJOR in
     a_options, [K/128,T4] as the per-group ops write it); w [N,K] fp8 with
     w_scale fp32 [ceil(N/128),K/128].  UE8M0 scales need no option."""
-    bf16, _, _ = _dtypes()
-    ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options)
+    dev, raw = _here(stream)
+    ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
     _shape(out, (T, N), "out")
-    _on_current_device(out, a, a_scale, w, w_scale)
-    _check(load().vg_fp8_block_gemm(_ptr(out, bf16, "out"), *ptrs, T, N, K, a_options,
-                                    _stream(stream)))
+    _check((_lib or load()).vg_fp8_block_gemm(_arg(out, _kinds()[0], "out", dev), *ptrs, T, N, K,
+                                              a_options, raw))
 
 
 def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: int = 0,
@@ -499,20 +509,18 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     rows [I,2I)) with w_scale [2I/128,K/128]; q [T,I] fp8, scale fp32
     [T,I/128], or with COLUMN_MAJOR in out_options [I/128,T4]; UE8M0 in
     out_options: power-of-two scales."""
-    _, fp8, f32 = _dtypes()
-    ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options)
-    inter = N // 2
+    _, fp8, f32, _ = _kinds()
+    dev, raw = _here(stream)
+    ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
     if N % 2:
         raise ValueError("w must have an even number of rows (gate, then up)")
+    inter = N // 2
     _shape(q, (T, inter), "q")
-    if out_options & COLUMN_MAJOR:
-        _shape(scale, (inter // BLOCK, (T + 3) // 4 * 4), "scale")
-    else:
-        _shape(scale, (T, inter // BLOCK), "scale")
-    _on_current_device(q, scale, a, a_scale, w, w_scale)
-    _check(load().vg_fp8_block_gemm_silu_mul_fp8(
-        _ptr(q, fp8, "q"), _ptr(scale, f32, "scale"), *ptrs, T, inter, K, a_options, out_options,
-        _stream(stream)))
+    _shape(scale, (inter // BLOCK, (T + 3) // 4 * 4) if out_options & COLUMN_MAJOR
+           else (T, inter // BLOCK), "scale")
+    _check((_lib or load()).vg_fp8_block_gemm_silu_mul_fp8(
+        _arg(q, fp8, "q", dev), _arg(scale, f32, "scale", dev), *ptrs, T, inter, K, a_options,
+        out_options, raw))
 
 
 def vg_device_status(reset: bool = False) -> int:

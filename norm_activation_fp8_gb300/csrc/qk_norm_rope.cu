@@ -75,12 +75,37 @@ __device__ __forceinline__ float2 kahan2x(float2 a, float2 c, float2 nb, float2 
   return make_float2(e.x != 0.f ? o.x : f.x, e.y != 0.f ? o.y : f.y);
 }
 
-// Eight bf16 words' worth of fp32 values -> eight E4M3 codes of v * m.
-__device__ __forceinline__ uint2 quant8_scaled(const float *p, float m) {
-  float v[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = p[k] * m;
-  return quant8(v);
+// Eight fp32 values (in registers: every index is a constant) as bf16, as
+// E4M3 codes; a chunk of eight bf16 times m as E4M3 codes.
+__device__ __forceinline__ uint4 bf16x8(const float *p) {
+  return make_uint4(pack_bf16x2_rn(p[0], p[1]), pack_bf16x2_rn(p[2], p[3]),
+                    pack_bf16x2_rn(p[4], p[5]), pack_bf16x2_rn(p[6], p[7]));
+}
+
+__device__ __forceinline__ uint2 codes8(const float *p) {
+  return make_uint2(cvt_e4m3x2(p[0], p[1]) | (cvt_e4m3x2(p[2], p[3]) << 16),
+                    cvt_e4m3x2(p[4], p[5]) | (cvt_e4m3x2(p[6], p[7]) << 16));
+}
+
+__device__ __forceinline__ uint2 scaled_codes(const uint4 &x, float m) {
+  const float v[8] = {bf16_lo(x.x) * m, bf16_hi(x.x) * m, bf16_lo(x.y) * m, bf16_hi(x.y) * m,
+                      bf16_lo(x.z) * m, bf16_hi(x.z) * m, bf16_lo(x.w) * m, bf16_hi(x.w) * m};
+  return codes8(v);
+}
+
+// The element at which head kv of a token with this slot starts: the slot's
+// page, the token in it, the head.  -1: the token is not appended (a padding
+// token, or a slot beyond the cache, which `report` makes known).
+__device__ __forceinline__ int64_t cache_place(const QkArgs &a, int64_t slot, int kv, bool report) {
+  if (slot < 0) return -1;
+  if (slot >= a.num_slots) {
+    if (report) atomicOr(&g_rope_status, kErrBadSlot);
+    return -1;
+  }
+  const uint32_t page = (uint32_t)slot / (uint32_t)a.page_size;
+  const uint32_t in_page = (uint32_t)slot - page * (uint32_t)a.page_size;
+  return (int64_t)page * a.page_stride + (int64_t)in_page * a.token_stride +
+         (int64_t)kv * a.head_stride;
 }
 
 // One head's two chunks of 8 (columns 8l and 8(l + G)) to its slot of a paged
@@ -105,7 +130,7 @@ __device__ __forceinline__ void cache_store(const QkArgs &a, void *cache, int64_
 }
 
 template <int G, bool NEOX, bool AXES, bool APPEND>
-__global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
+__global__ void __launch_bounds__(512, 3) qk_norm_rope_kernel(const QkArgs a) {
   constexpr int D = G * 16;
   const int lane = threadIdx.x & 31;
   const int l = lane & (G - 1);
@@ -122,22 +147,6 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
   pdl_wait();
   [[maybe_unused]] __shared__ __align__(16) float row_cs[AXES ? D : 4];
   bool pos_ok = true;
-  if constexpr (AXES) {
-    // the axes' positions, then this token's cos/sin row, pair by pair
-    int64_t p4[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      p4[x] = x < a.axes ? a.pos[x * a.T + t] : 0;
-      pos_ok = pos_ok && p4[x] >= 0 && p4[x] < a.max_pos;
-    }
-    if (pos_ok)
-      for (int i = (int)threadIdx.x; i < D; i += (int)blockDim.x) {
-        const int pair = i & (D / 2 - 1);
-        const int x = (int)(a.axis_map[pair >> 4] >> (2 * (pair & 15))) & 3;
-        const int64_t p = x == 0 ? p4[0] : (x == 1 ? p4[1] : (x == 2 ? p4[2] : p4[3]));
-        row_cs[i] = __ldg(a.cache + p * D + i);
-      }
-  }
   // The head's loads do not depend on the token's position, so they go out
   // together with it (a head with a bad position is loaded but not stored);
   // only the cos/sin row waits for the position.
@@ -154,26 +163,40 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
   const uint4 ones = make_uint4(kOnes, kOnes, kOnes, kOnes);
   const uint4 wa = in_head && norm ? ld_keep(w + l * kElemsPerChunk) : ones;
   const uint4 wb = in_head && norm ? ld_keep(w + (l + G) * kElemsPerChunk) : ones;
+  if constexpr (AXES) {
+    // the axes' positions, then this token's cos/sin row, pair by pair (after
+    // the heads' loads, which do not wait for them)
+    int64_t p4[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      p4[x] = x < a.axes ? a.pos[x * a.T + t] : 0;
+      pos_ok = pos_ok && p4[x] >= 0 && p4[x] < a.max_pos;
+    }
+    if (pos_ok)
+      for (int i = (int)threadIdx.x; i < D; i += (int)blockDim.x) {
+        const int pair = i & (D / 2 - 1);
+        const int x = (int)(a.axis_map[pair >> 4] >> (2 * (pair & 15))) & 3;
+        const int64_t p = x == 0 ? p4[0] : (x == 1 ? p4[1] : (x == 2 ? p4[2] : p4[3]));
+        row_cs[i] = __ldg(a.cache + p * D + i);
+      }
+  }
   if constexpr (!AXES) pos_ok = pos >= 0 && pos < a.max_pos;
   const bool live = in_head && pos_ok;  // same for the head's lanes
   if (in_head && !live && l == 0) atomicOr(&g_rope_status, kErrBadPosition);
   pdl_launch_dependents();
-  // Where a K or V head goes: the slot's page, the token in it, the head.
-  [[maybe_unused]] int64_t cache_at = 0;
-  [[maybe_unused]] bool to_cache = false;
+  if constexpr (AXES) __syncthreads();  // row_cs is complete
   if constexpr (APPEND) {
-    if (live && h >= a.hq && slot >= 0) {
-      if (slot < a.num_slots) {
-        const uint32_t page = (uint32_t)slot / (uint32_t)a.page_size;
-        const uint32_t in_page = (uint32_t)slot - page * (uint32_t)a.page_size;
-        const int kv = h < a.hqk ? h - a.hq : h - a.hqk;
-        cache_at = (int64_t)page * a.page_stride + (int64_t)in_page * a.token_stride +
-                   (int64_t)kv * a.head_stride;
-        to_cache = true;
-      } else if (l == 0) {
-        atomicOr(&g_rope_status, kErrBadSlot);
+    // V heads go to the cache as they are; a warp of V heads is then done
+    if (live && h >= a.hqk) {
+      const int64_t at = cache_place(a, slot, h - a.hqk, l == 0);
+      if (at >= 0 && a.v_scale == nullptr) {
+        cache_store(a, a.v_cache, at, l, G, xa, xb);
+      } else if (at >= 0) {
+        const float m = __frcp_rn(__ldg(a.v_scale));
+        cache_store(a, a.v_cache, at, l, G, scaled_codes(xa, m), scaled_codes(xb, m));
       }
     }
+    if (h - lane / G >= a.hqk) return;
   }
   float2 ta[4], tb[4];
   float cmax;
@@ -184,7 +207,6 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
 #pragma unroll
   for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
   const float y = norm ? rsqrtf(fmaf(ss, 1.0f / (float)D, a.eps)) : 1.0f;
-  if constexpr (AXES) __syncthreads();  // row_cs is complete
 
   // mine[0..7]: chunk 0, mine[8..15]: chunk 1; other: each element's pair
   // partner; c, s: its pair's cos and sin; submask bit k: minus sign
@@ -251,41 +273,36 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
     p[k + 1] = pp.y;
   }
   if constexpr (APPEND) {
-    if (to_cache) {  // K: the rotated values; V: the row's own bits, or its values scaled
-      const bool is_v = h >= a.hqk;
-      void *cache = is_v ? a.v_cache : a.k_cache;
-      if (a.k_scale == nullptr) {
-        const uint4 ka = make_uint4(pack_bf16x2_rn(p[0], p[1]), pack_bf16x2_rn(p[2], p[3]),
-                                    pack_bf16x2_rn(p[4], p[5]), pack_bf16x2_rn(p[6], p[7]));
-        const uint4 kb = make_uint4(pack_bf16x2_rn(p[8], p[9]), pack_bf16x2_rn(p[10], p[11]),
-                                    pack_bf16x2_rn(p[12], p[13]), pack_bf16x2_rn(p[14], p[15]));
-        cache_store(a, cache, cache_at, l, G, is_v ? xa : ka, is_v ? xb : kb);
+    if (h >= a.hq) {  // a K head goes to its slot (a V head is already there)
+      if (!live || h >= a.hqk) return;
+      const int64_t at = cache_place(a, slot, h - a.hq, l == 0);
+      if (at < 0) return;
+      if (a.k_scale != nullptr) {
+        const float m = __frcp_rn(__ldg(a.k_scale));
+#pragma unroll
+        for (int k = 0; k < 16; ++k) p[k] *= m;
+        cache_store(a, a.k_cache, at, l, G, codes8(p), codes8(p + 8));
       } else {
-        const float m = __frcp_rn(__ldg(is_v ? a.v_scale : a.k_scale));
-        // mine holds V's own values: a V head's weights are ones
-        cache_store(a, cache, cache_at, l, G, quant8_scaled(is_v ? mine : p, m),
-                    quant8_scaled(is_v ? mine + 8 : p + 8, m));
+        cache_store(a, a.k_cache, at, l, G, bf16x8(p), bf16x8(p + 8));
       }
+      return;
     }
-    if (h >= a.hq) return;
   }
-  const uint4 oa = make_uint4(pack_bf16x2_rn(p[0], p[1]), pack_bf16x2_rn(p[2], p[3]),
-                              pack_bf16x2_rn(p[4], p[5]), pack_bf16x2_rn(p[6], p[7]));
-  const uint4 ob = make_uint4(pack_bf16x2_rn(p[8], p[9]), pack_bf16x2_rn(p[10], p[11]),
-                              pack_bf16x2_rn(p[12], p[13]), pack_bf16x2_rn(p[14], p[15]));
   [[maybe_unused]] const uint64_t bytes = VG_ROWS(a.T) * 2ull * (uint64_t)a.row;
   if (live && VG_ACCESS_OK(g_rope_status, head + l * kElemsPerChunk, 16, a.qkv, bytes))
-    st_stream(head + l * kElemsPerChunk, oa);
+    st_stream(head + l * kElemsPerChunk, bf16x8(p));
   if (live && VG_ACCESS_OK(g_rope_status, head + (l + G) * kElemsPerChunk, 16, a.qkv, bytes))
-    st_stream(head + (l + G) * kElemsPerChunk, ob);
+    st_stream(head + (l + G) * kElemsPerChunk, bf16x8(p + 8));
 }
 
 // One token per CTA: up to 16 warps of heads; blockIdx.y covers the rest.
 template <int G, bool AXES, bool APPEND>
 cudaError_t launch_form(const QkArgs &a, bool neox, cudaStream_t s) {
   const int heads_per_warp = 32 / G;
-  int warps = (a.nh + heads_per_warp - 1) / heads_per_warp;
-  if (warps > 16) warps = 16;
+  // up to 16 warps a CTA; more of them are dealt out evenly
+  const int all = (a.nh + heads_per_warp - 1) / heads_per_warp;
+  const int parts = (all + 15) / 16;
+  const int warps = (all + parts - 1) / parts;
   const dim3 grid((unsigned)a.T, (unsigned)((a.nh + warps * heads_per_warp - 1) / (warps * heads_per_warp)));
   return neox ? launch_pdl(qk_norm_rope_kernel<G, true, AXES, APPEND>, grid, dim3(warps * 32), 0, s, a)
               : launch_pdl(qk_norm_rope_kernel<G, false, AXES, APPEND>, grid, dim3(warps * 32), 0, s, a);
