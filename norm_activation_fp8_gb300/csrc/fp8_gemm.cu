@@ -7,13 +7,25 @@
 //           rounded to bf16), s = max(amax |y| over 128 columns, 1e-10) / 448
 //           (or the power of two above it), q = e4m3(y / s)
 //
-// A simple form on the fp32 units: a CTA computes 32 tokens by 128 columns
-// (gated: of gate and of up), a warp 4 tokens, so that a warp holds a whole
-// scale group.  A block's products are summed in fp32 and scaled into the
-// running fp32 sum.
+// Tile kernel.  A persistent CTA per SM computes tiles of 128 tokens x 256
+// weight rows (gated: 128 gate rows and the same 128 up rows), one scale
+// block (128 of K) at a time: TMA stages A and W in four 48 KB stages, one
+// thread issues four M128 N256 K32 products into one of two 256-column
+// accumulators, and eight warps take the block's sum out of tensor memory and
+// add it, times its two scales, to an fp32 sum in registers (the block scales
+// are arbitrary fp32 numbers, so the tensor cores cannot apply them).  The
+// two accumulators let the products of the next block run meanwhile.  A
+// thread holds 64 columns of either half of a token's row: for the gated form
+// gate and up of the same columns, so that the activation needs no exchange
+// and a group's amax one float from the warp beside it.
+//   warp 0: TMA   warp 1: products   warp 2: scales (global -> shared)
+//   warps 4-11: sums and epilogue (warp w: tensor memory lanes 32 (w mod 4))
+#include <atomic>
+
 #include "common.cuh"
 #include "dyn_scale.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
 
 namespace vg {
 
@@ -22,110 +34,420 @@ __device__ uint32_t g_gemm_status;
 
 namespace {
 
-constexpr int kTok = 32, kCol = 128, kStep = 32;
+constexpr int kBlockK = 128;  // codes of K per scale block (and per stage)
 
-__device__ __forceinline__ float2 e4m3x2_to_f2(uint16_t v) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
-  float2 f;
-  asm("{.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;}"
-      : "=f"(f.x), "=f"(f.y)
-      : "r"(h));
+// Waits for a barrier phase; a wait that gives up is recorded, here for the
+// CTA and in the status word for the host.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile uint32_t *failed) {
+  if (mbar_wait_bounded(bar, parity)) return true;
+  *failed = 1;
+  atomicOr(&g_gemm_status, kErrWaitTimeout);
+  return false;
+}
+
+// The same for a whole warp, with one answer for all of it.
+__device__ __forceinline__ bool warp_wait_phase(uint64_t *bar, uint32_t parity, volatile uint32_t *failed) {
+  return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, failed));
+}
+
+// A barrier of `threads` threads that tells all of them whether any passed true.
+__device__ __forceinline__ bool named_sync_or(int id, int threads, bool p) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"((uint32_t)p)
+      : "memory");
+  return any != 0;
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
+// The scale of a group (an ulp or two in s moves only codes that near a
+// midpoint) and the factor that its codes are multiplied by.
+__device__ __forceinline__ float group_scale(float amax, bool ue8m0) {
+  const float a = fmaxf(amax, kAmaxFloor);
+  return ue8m0 ? exp2i(pow2_exponent_448(a)) : a * kInv448;
+}
+
+// Extent in bytes of the scale tensor (debug checks).
+[[maybe_unused]] __device__ __forceinline__ uint64_t gemm_scale_extent(const GemmArgs &a) {
+  const uint64_t rows = VG_ROWS(a.T);
+  return rows == 0 ? 0 : 4 * ((rows - 1) * (uint64_t)a.s_ts + (uint64_t)(a.N / kBlockK - 1) * a.s_gs + 1);
+}
+
+// ------------------------------------------------------------- tile kernel
+
+constexpr int kTileT = 128, kTileW = 256, kHalfW = 128;
+constexpr int kTileStages = 4;
+constexpr int kTileStageBytes = (kTileT + kTileW) * kBlockK;
+constexpr int kTileThreads = 384, kSumWarps = 8;
+constexpr int kTileGroup = 32;  // token tiles that share a sweep over the weight
+
+// Dynamic shared memory, after alignment to 1024 bytes.
+template <bool GATED>
+struct TileSmem {
+  uint8_t stage[kTileStages][kTileStageBytes];
+  uint8_t out[kSumWarps][GATED ? 1 : 2][32 * 64];  // boxes of 32 rows x 64 bytes
+  float sa[2][kTileT];
+  float sw[2][2];
+  float amax[GATED ? 2 : 1][GATED ? 2 : 1][GATED ? kTileT : 1];
+  uint64_t full[kTileStages], empty[kTileStages];
+  uint64_t acc_full[2], acc_empty[2], scale_full[2], drain;
+  uint32_t tmem;
+  uint32_t failed;
+};
+
+// The k-th tile of this CTA: token tiles run fastest within groups of
+// kTileGroup, so that the tiles in flight share weight rows and the group's
+// activations stay in L2 while the weight streams by.
+struct Tile {
+  int t0;  // first token
+  int n;   // weight tile
+};
+__device__ __forceinline__ Tile tile_at(int64_t i, int num_t, int num_n) {
+  const int64_t per_group = (int64_t)kTileGroup * num_n;
+  const int g = (int)(i / per_group);
+  const int64_t r = i - g * per_group;
+  const int rows = min(kTileGroup, num_t - g * kTileGroup);
+  return {(g * kTileGroup + (int)(r % rows)) * kTileT, (int)(r / rows)};
+}
+
+// First weight rows of a tile's two halves.
+template <bool GATED>
+__device__ __forceinline__ int half_row(const GemmArgs &a, int n, int half) {
+  return GATED ? half * a.N + n * kHalfW : n * kTileW + half * kHalfW;
+}
+
+struct GemmMaps {
+  CUtensorMap a, w, out;
+};
+
+template <bool GATED>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    fp8_gemm_tile_kernel(const GemmArgs a, const __grid_constant__ GemmMaps maps, int num_t, int num_n) {
+  extern __shared__ uint8_t raw[];
+  using Smem = TileSmem<GATED>;
+  Smem &sm = *reinterpret_cast<Smem *>(raw + (1024 - (smem_u32(raw) & 1023)) % 1024);
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  const int num_k = a.K / kBlockK;
+  const int64_t tiles = (int64_t)num_t * num_n;
+  VG_NEVER_BARRIER;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&maps.a);
+    prefetch_tensormap(&maps.w);
+    prefetch_tensormap(&maps.out);
+    for (int i = 0; i < kTileStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.acc_full[i], 1);
+      mbar_init(&sm.acc_empty[i], kSumWarps);
+      mbar_init(&sm.scale_full[i], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    VG_NEVER_BARRIER_INIT();
+    fence_mbar_init();
+    sm.failed = 0;
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem, 512);
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  const uint32_t tmem = sm.tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+  int issued = 0;  // stages this thread has filled (warp 0 lane 0)
+
+  if (warp < 4) {
+    regs_decrease<56>();
+    if (warp == 0 && lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+        const Tile t = tile_at(i, num_t, num_n);
+        const int r0 = half_row<GATED>(a, t.n, 0), r1 = half_row<GATED>(a, t.n, 1);
+        for (int kb = 0; kb < num_k; ++kb, ++it) {
+          const int s = it % kTileStages;
+          if (it >= kTileStages && !(ok = wait_phase(&sm.empty[s], (it / kTileStages - 1) & 1, &sm.failed)))
+            break;
+          mbar_arrive_expect_tx(&sm.full[s], kTileStageBytes);
+          uint8_t *p = sm.stage[s];
+          tma_load_2d(p, &maps.a, kb * kBlockK, t.t0, &sm.full[s]);
+          tma_load_2d(p + kTileT * kBlockK, &maps.w, kb * kBlockK, r0, &sm.full[s]);
+          tma_load_2d(p + (kTileT + kHalfW) * kBlockK, &maps.w, kb * kBlockK, r1, &sm.full[s]);
+          ++issued;
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      constexpr uint32_t desc = product_desc(kTileT, kTileW);
+      int it = 0;
+      bool ok = true;
+      for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x)
+        for (int kb = 0; kb < num_k; ++kb, ++it) {
+          const int s = it % kTileStages, b = it & 1;
+          if (it >= 2 && !(ok = wait_phase(&sm.acc_empty[b], (it / 2 - 1) & 1, &sm.failed))) break;
+          if (!(ok = wait_phase(&sm.full[s], (it / kTileStages) & 1, &sm.failed))) break;
+          if (VG_FORCED_TIMEOUT(it == 0)) {
+            sm.failed = 1;
+            atomicOr(&g_gemm_status, kErrWaitTimeout);
+            ok = false;
+            break;
+          }
+          tcgen05_fence_after();
+          const uint64_t da = operand_desc(smem_u32(sm.stage[s]));
+          const uint64_t dw = operand_desc(smem_u32(sm.stage[s] + kTileT * kBlockK));
+#pragma unroll
+          for (int k = 0; k < kBlockK / 32; ++k)
+            mma_e4m3(tmem + b * kTileW, da + 2 * k, dw + 2 * k, desc, k > 0);
+          mma_commit(&sm.empty[s]);
+          mma_commit(&sm.acc_full[b]);
+        }
+      // Nothing is in flight once this arrives (at once, unless a wait gave up).
+      mma_commit(&sm.drain);
+      (void)mbar_wait_bounded(&sm.drain, 0);
+    } else if (warp == 2) {
+      // Two blocks ahead: a block's scales are on their way to registers
+      // while the two before it are used.
+      float va[2][4], vw[2];
+      int64_t i = blockIdx.x;
+      int kb = 0;
+      const auto fetch = [&](float(&v)[4], float &w) {
+        if (i >= tiles) return;
+        const Tile t = tile_at(i, num_t, num_n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = t.t0 + lane + 32 * j;
+          v[j] = row < a.T ? __ldg(a.a_scale + row * a.a_ts + kb * a.a_bs) : 0.f;
+        }
+        if (lane < 2) {
+          const int r = half_row<GATED>(a, t.n, lane);
+          w = r < (GATED ? 2 : 1) * a.N ? __ldg(a.w_scale + (int64_t)(r / kBlockK) * num_k + kb) : 0.f;
+        }
+        if (++kb == num_k) {
+          kb = 0;
+          i += gridDim.x;
+        }
+      };
+      fetch(va[0], vw[0]);
+      fetch(va[1], vw[1]);
+      const int64_t mine = (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x * num_k;
+      for (int64_t it = 0; it < mine; it += 2) {
+        bool ok = true;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (it + b >= mine) break;
+          if (it >= 2 && !(ok = warp_wait_phase(&sm.acc_empty[b], (uint32_t)(it / 2 - 1) & 1, &sm.failed)))
+            break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sm.sa[b][lane + 32 * j] = va[b][j];
+          if (lane < 2) sm.sw[b][lane] = vw[b];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.scale_full[b]);
+          fetch(va[b], vw[b]);
+        }
+        if (!ok) break;
+      }
+    }
+  } else {
+    regs_increase<224>();
+    const int quarter = warp & 3, part = (warp - 4) >> 2;  // lanes, 64-column part of each half
+    const int row = quarter * 32 + lane;
+    uint8_t *box = sm.out[warp - 4][0];
+    int64_t it = 0;
+    int turn = 0;
+    bool ok = true;
+    for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x, turn ^= 1) {
+      float2 acc[2][32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[h][j] = make_float2(0.f, 0.f);
+      for (int kb = 0; kb < num_k; ++kb, ++it) {
+        const int b = (int)(it & 1);
+        const uint32_t ph = (uint32_t)(it >> 1) & 1;
+        if (!(ok = warp_wait_phase(&sm.scale_full[b], ph, &sm.failed))) break;
+        if (!(ok = warp_wait_phase(&sm.acc_full[b], ph, &sm.failed))) break;
+        tcgen05_fence_after();
+        const float s = sm.sa[b][row];
+        const float2 sc[2] = {make_float2(s * sm.sw[b][0], s * sm.sw[b][0]),
+                              make_float2(s * sm.sw[b][1], s * sm.sw[b][1])};
+        const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * kTileW + part * 64;
+        uint32_t v[2][32];
+        tmem_load32(base, v[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // 32 columns each: two of either half
+          tmem_load_wait(v[c & 1]);
+          if (c < 3) {
+            tmem_load32(base + ((c + 1) >> 1) * kHalfW + ((c + 1) & 1) * 32, v[(c + 1) & 1]);
+          } else {  // all read: the products of the block after next may start
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 &x = acc[c >> 1][(c & 1) * 16 + j];
+            x = f2_fma(make_float2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])),
+                       sc[c >> 1], x);
+          }
+        }
+      }
+      if (!GATED && !ok) break;
+
+      const Tile t = tile_at(i, num_t, num_n);
+      const int t0 = t.t0 + quarter * 32;  // this warp's first token
+      if constexpr (!GATED) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // boxes of 32 columns, 64 bytes a row
+          uint8_t *p = box + (c & 1) * (32 * 64);
+          if (lane == 0) tma_store_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 *x = &acc[c >> 1][(c & 1) * 16 + q * 4];
+            *reinterpret_cast<uint4 *>(p + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pack_bf16x2_rn(x[0].x, x[0].y), pack_bf16x2_rn(x[1].x, x[1].y),
+                           pack_bf16x2_rn(x[2].x, x[2].y), pack_bf16x2_rn(x[3].x, x[3].y));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int n = half_row<false>(a, t.n, c >> 1) + part * 64 + (c & 1) * 32;
+          if (lane == 0) {
+            if (t0 < a.T && n < a.N) tma_store_2d(&maps.out, p, n, t0);
+            tma_store_commit();
+          }
+        }
+      } else {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float2 &g = acc[0][j];
+          g = make_float2(silu_mul(g.x, acc[1][j].x), silu_mul(g.y, acc[1][j].y));
+          m = fmax3(m, fabsf(g.x), fabsf(g.y));
+        }
+        sm.amax[turn][part][row] = m;
+        // all of the warps leave together where a wait of one gave up
+        if (named_sync_or(1, kSumWarps * 32, !ok)) break;
+        m = fmaxf(m, sm.amax[turn][part ^ 1][row]);
+        const float s = group_scale(m, a.ue8m0 != 0);
+        const float2 r = make_float2(__frcp_rn(s), __frcp_rn(s));
+        if (lane == 0) tma_store_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = f2_mul(acc[0][q * 8 + 2 * k], r), y = f2_mul(acc[0][q * 8 + 2 * k + 1], r);
+            w[k] = cvt_e4m3x2(x.x, x.y) | (cvt_e4m3x2(y.x, y.y) << 16);
+          }
+          *reinterpret_cast<uint4 *>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (t0 < a.T) tma_store_2d(&maps.out, box, t.n * kHalfW + part * 64, t0);
+          tma_store_commit();
+        }
+        if (part == 0 && t0 + lane < a.T) {
+          float *p = a.scale + (int64_t)(t0 + lane) * a.s_ts + (int64_t)t.n * a.s_gs;
+          if (VG_ACCESS_OK(g_gemm_status, p, 4, a.scale, gemm_scale_extent(a))) *p = s;
+        }
+      }
+    }
+    if (lane == 0) tma_store_wait_read<0>();
+  }
+
+  __syncthreads();
+  if (sm.failed && warp == 0 && lane == 0)  // copies still in flight end here
+    for (int it = issued < kTileStages ? 0 : issued - kTileStages; it < issued; ++it)
+      (void)mbar_wait_bounded(&sm.full[it % kTileStages], (it / kTileStages) & 1);
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------- host
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder, looked up once.
+EncodeTiled encoder() {
+  static std::atomic<EncodeTiled> fn{nullptr};
+  EncodeTiled f = fn.load(std::memory_order_acquire);
+  if (f) return f;
+  void *p = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+          cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeTiled>(p);
+  fn.store(f, std::memory_order_release);
   return f;
 }
 
-// rows x 32 columns of codes from row0 on, as fp32, column by column in
-// shared memory; rows beyond `limit` are zero.
-template <int ROWS>
-__device__ __forceinline__ void stage(float (&dst)[kStep][ROWS + 1], const uint8_t *src, int64_t row0,
-                                      int64_t limit, int64_t ld, int k0) {
-  for (int i = (int)threadIdx.x; i < ROWS * (kStep / 4); i += (int)blockDim.x) {
-    const int r = i / (kStep / 4), c = i % (kStep / 4) * 4;
-    uint32_t v = 0;
-    if (row0 + r < limit) v = *reinterpret_cast<const uint32_t *>(src + (row0 + r) * ld + k0 + c);
-    const float2 lo = e4m3x2_to_f2((uint16_t)v), hi = e4m3x2_to_f2((uint16_t)(v >> 16));
-    dst[c][r] = lo.x;
-    dst[c + 1][r] = lo.y;
-    dst[c + 2][r] = hi.x;
-    dst[c + 3][r] = hi.y;
-  }
+// A row-major [rows, cols] tensor read or written in boxes of box_rows x box_cols.
+bool make_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *p, int64_t rows,
+              int64_t cols, int box_rows, int box_cols, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(cols * size)};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  const EncodeTiled f = encoder();
+  return f && f(m, type, 2, const_cast<void *>(p), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Opts `kern` in to large dynamic shared memory, once per kernel and device.
+cudaError_t opt_in_once(std::atomic<uint64_t> &opted_in, const void *kern) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (opted_in.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = opt_in_dynamic_smem(kern);
+  if (e == cudaSuccess) opted_in.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 template <bool GATED>
-__global__ void __launch_bounds__(256) fp8_gemm_simple_kernel(const GemmArgs a) {
-  constexpr int H = GATED ? 2 : 1;
-  __shared__ float sa[kStep][kTok + 1];
-  __shared__ float sw[H][kStep][kCol + 1];
-  const int tx = (int)threadIdx.x & 31, ty = (int)threadIdx.x >> 5;
-  const int64_t t0 = (int64_t)blockIdx.x * kTok, n0 = (int64_t)blockIdx.y * kCol;
-  pdl_wait();
-  float acc[H][4][4] = {};
-  const int kb = a.K / 128;
-  for (int b = 0; b < kb; ++b) {
-    float part[H][4][4] = {};
-    for (int k0 = b * 128; k0 < b * 128 + 128; k0 += kStep) {
-      __syncthreads();
-      stage<kTok>(sa, a.a, t0, a.T, a.K, k0);
-      for (int h = 0; h < H; ++h)
-        stage<kCol>(sw[h], a.w, n0 + (int64_t)h * a.N, (int64_t)(h + 1) * a.N, a.K, k0);
-      __syncthreads();
-#pragma unroll 4
-      for (int k = 0; k < kStep; ++k)
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              part[h][i][j] = fmaf(sa[k][ty * 4 + i], sw[h][k][tx + 32 * j], part[h][i][j]);
-    }
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const float ws = a.w_scale[((n0 + (int64_t)h * a.N) / 128) * kb + b];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t t = t0 + ty * 4 + i;
-        const float s = t < a.T ? a.a_scale[t * a.a_ts + b * a.a_bs] * ws : 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[h][i][j] = fmaf(part[h][i][j], s, acc[h][i][j]);
-      }
-    }
-  }
-  pdl_launch_dependents();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = t0 + ty * 4 + i;
-    if (t >= a.T) continue;
-    if constexpr (!GATED) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t n = n0 + tx + 32 * j;
-        if (n < a.N) a.out[t * a.N + n] = (uint16_t)pack_bf16x2_rn(acc[0][i][j], 0.f);
-      }
-    } else {
-      float y[4], m = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[j] = acc[0][i][j] / (1.0f + __expf(-acc[0][i][j])) * acc[1][i][j];
-        m = fmaxf(m, fabsf(y[j]));
-      }
-      m = fmaxf(warp_max(m), kAmaxFloor);
-      const float s = a.ue8m0 ? exp2i(pow2_exponent_448(m)) : m * kInv448;
-      if (tx == 0) a.scale[t * a.s_ts + (n0 / 128) * a.s_gs] = s;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        a.q[t * a.N + n0 + tx + 32 * j] = (uint8_t)cvt_e4m3x2(y[j] / s, 0.f);
-    }
-  }
+cudaError_t launch_tile(const GemmArgs &a, int sms, cudaStream_t s) {
+  static std::atomic<uint64_t> opted_in{0};
+  const cudaError_t e = opt_in_once(opted_in, (const void *)fp8_gemm_tile_kernel<GATED>);
+  if (e != cudaSuccess) return e;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  GemmMaps maps;
+  if (!make_map(&maps.a, u8, 1, a.a, a.T, a.K, kTileT, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&maps.w, u8, 1, a.w, (GATED ? 2 : 1) * (int64_t)a.N, a.K, kHalfW, kBlockK,
+                CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !(GATED ? make_map(&maps.out, u8, 1, a.q, a.T, a.N, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B)
+              : make_map(&maps.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.out, a.T, a.N, 32, 32,
+                         CU_TENSOR_MAP_SWIZZLE_64B)))
+    return cudaErrorInvalidValue;
+  const int num_t = (a.T + kTileT - 1) / kTileT;
+  const int num_n = GATED ? a.N / kHalfW : (a.N + kTileW - 1) / kTileW;
+  const int64_t tiles = (int64_t)num_t * num_n;
+  const dim3 grid((unsigned)(tiles < sms ? tiles : sms));
+  return launch_pdl(fp8_gemm_tile_kernel<GATED>, grid, dim3(kTileThreads), sizeof(TileSmem<GATED>) + 1024,
+                    s, a, maps, num_t, num_n);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const GemmArgs &a, bool gated, int sms, cudaStream_t s) {
-  (void)sms;
-  const dim3 grid((unsigned)((a.T + kTok - 1) / kTok), (unsigned)((a.N + kCol - 1) / kCol));
-  return gated ? launch_pdl(fp8_gemm_simple_kernel<true>, grid, dim3(256), 0, s, a)
-               : launch_pdl(fp8_gemm_simple_kernel<false>, grid, dim3(256), 0, s, a);
+  return gated ? launch_tile<true>(a, sms, s) : launch_tile<false>(a, sms, s);
 }
 
 uint32_t read_gemm_status(bool reset) {
