@@ -11,15 +11,15 @@
 // weight rows (gated: 128 gate rows and the same 128 up rows), one scale
 // block (128 of K) at a time: TMA stages A and W in four 48 KB stages, one
 // thread issues four M128 N256 K32 products into one of two 256-column
-// accumulators, and eight warps take the block's sum out of tensor memory and
+// accumulators, and sixteen warps take the block's sum out of tensor memory and
 // add it, times its two scales, to an fp32 sum in registers (the block scales
 // are arbitrary fp32 numbers, so the tensor cores cannot apply them).  The
 // two accumulators let the products of the next block run meanwhile.  A
-// thread holds 64 columns of either half of a token's row: for the gated form
+// thread holds 32 columns of either half of a token's row: for the gated form
 // gate and up of the same columns, so that the activation needs no exchange
-// and a group's amax one float from the warp beside it.
+// and a group's amax one float from each of the three warps beside it.
 //   warp 0: TMA   warp 1: products   warp 2: scales (global -> shared)
-//   warps 4-11: sums and epilogue (warp w: tensor memory lanes 32 (w mod 4))
+//   warps 4-19: sums and epilogue (warp w: tensor memory lanes 32 (w mod 4))
 #include <atomic>
 
 #include "common.cuh"
@@ -86,19 +86,21 @@ __device__ __forceinline__ float group_scale(float amax, bool ue8m0) {
 constexpr int kTileT = 128, kTileW = 256, kHalfW = 128;
 constexpr int kTileStages = 4;
 constexpr int kTileStageBytes = (kTileT + kTileW) * kBlockK;
-constexpr int kTileThreads = 384, kSumWarps = 8;
+constexpr int kSumWarps = 16, kTileThreads = 128 + 32 * kSumWarps;
+constexpr int kPart = kHalfW * 4 / kSumWarps;  // columns of either half that a thread sums
+// The launch holds 640 x 96 registers; the split hands out 128 x 56 + 512 x 104.
 constexpr int kTileGroup = 32;  // token tiles that share a sweep over the weight
 
 // Dynamic shared memory, after alignment to 1024 bytes.
 template <bool GATED>
 struct TileSmem {
   uint8_t stage[kTileStages][kTileStageBytes];
-  uint8_t out[kSumWarps][GATED ? 1 : 2][32 * 64];  // boxes of 32 rows x 64 bytes
+  uint8_t out[kSumWarps][32 * kPart * (GATED ? 1 : 2)];  // a box of 32 rows
   float sa[2][kTileT];
   float sw[2][2];
-  float amax[GATED ? 2 : 1][GATED ? 2 : 1][GATED ? kTileT : 1];
+  float amax[GATED ? 2 : 1][GATED ? kSumWarps / 4 : 1][GATED ? kTileT : 1];
   uint64_t full[kTileStages], empty[kTileStages];
-  uint64_t acc_full[2], acc_empty[2], scale_full[2], drain;
+  uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   uint32_t failed;
 };
@@ -110,12 +112,10 @@ struct Tile {
   int t0;  // first token
   int n;   // weight tile
 };
-__device__ __forceinline__ Tile tile_at(int64_t i, int num_t, int num_n) {
-  const int64_t per_group = (int64_t)kTileGroup * num_n;
-  const int g = (int)(i / per_group);
-  const int64_t r = i - g * per_group;
-  const int rows = min(kTileGroup, num_t - g * kTileGroup);
-  return {(g * kTileGroup + (int)(r % rows)) * kTileT, (int)(r / rows)};
+__device__ __forceinline__ Tile tile_at(uint32_t i, uint32_t num_t, uint32_t num_n) {
+  const uint32_t per_group = kTileGroup * num_n, g = i / per_group, r = i - g * per_group;
+  const uint32_t rows = min((uint32_t)kTileGroup, num_t - g * kTileGroup), n = r / rows;
+  return {(int)(g * kTileGroup + r - n * rows) * kTileT, (int)n};
 }
 
 // First weight rows of a tile's two halves.
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   Smem &sm = *reinterpret_cast<Smem *>(raw + (1024 - (smem_u32(raw) & 1023)) % 1024);
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
   const int num_k = a.K / kBlockK;
-  const int64_t tiles = (int64_t)num_t * num_n;
+  const uint32_t tiles = (uint32_t)num_t * (uint32_t)num_n;  // at most 2^29
   VG_NEVER_BARRIER;
 
   if (warp == 0 && lane == 0) {
@@ -148,9 +148,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.acc_full[i], 1);
+      mbar_init(&sm.acc_full[i], 2);  // the products and the scales
       mbar_init(&sm.acc_empty[i], kSumWarps);
-      mbar_init(&sm.scale_full[i], 1);
     }
     mbar_init(&sm.drain, 1);
     VG_NEVER_BARRIER_INIT();
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp == 0 && lane == 0) {
       int it = 0;
       bool ok = true;
-      for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+      for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
         const Tile t = tile_at(i, num_t, num_n);
         const int r0 = half_row<GATED>(a, t.n, 0), r1 = half_row<GATED>(a, t.n, 1);
         for (int kb = 0; kb < num_k; ++kb, ++it) {
@@ -190,7 +189,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       constexpr uint32_t desc = product_desc(kTileT, kTileW);
       int it = 0;
       bool ok = true;
-      for (int64_t i = blockIdx.x; i < tiles && ok; i += gridDim.x)
+      for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x)
         for (int kb = 0; kb < num_k; ++kb, ++it) {
           const int s = it % kTileStages, b = it & 1;
           if (it >= 2 && !(ok = wait_phase(&sm.acc_empty[b], (it / 2 - 1) & 1, &sm.failed))) break;
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // Two blocks ahead: a block's scales are on their way to registers
       // while the two before it are used.
       float va[2][4], vw[2];
-      int64_t i = blockIdx.x;
+      uint32_t i = blockIdx.x;
       int kb = 0;
       const auto fetch = [&](float(&v)[4], float &w) {
         if (i >= tiles) return;
@@ -238,66 +237,60 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       fetch(va[0], vw[0]);
       fetch(va[1], vw[1]);
-      const int64_t mine = (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x * num_k;
-      for (int64_t it = 0; it < mine; it += 2) {
+      const uint32_t mine = (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x * (uint32_t)num_k;
+      for (uint32_t it = 0; it < mine; it += 2) {
         bool ok = true;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           if (it + b >= mine) break;
-          if (it >= 2 && !(ok = warp_wait_phase(&sm.acc_empty[b], (uint32_t)(it / 2 - 1) & 1, &sm.failed)))
+          if (it >= 2 && !(ok = warp_wait_phase(&sm.acc_empty[b], (it / 2 - 1) & 1, &sm.failed)))
             break;
 #pragma unroll
           for (int j = 0; j < 4; ++j) sm.sa[b][lane + 32 * j] = va[b][j];
           if (lane < 2) sm.sw[b][lane] = vw[b];
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.scale_full[b]);
+          if (lane == 0) mbar_arrive(&sm.acc_full[b]);
           fetch(va[b], vw[b]);
         }
         if (!ok) break;
       }
     }
   } else {
-    regs_increase<224>();
-    const int quarter = warp & 3, part = (warp - 4) >> 2;  // lanes, 64-column part of each half
+    regs_increase<104>();
+    const int quarter = warp & 3, part = (warp - 4) >> 2;  // lanes, columns of each half
     const int row = quarter * 32 + lane;
-    uint8_t *box = sm.out[warp - 4][0];
-    int64_t it = 0;
+    uint8_t *box = sm.out[warp - 4];
+    uint32_t it = 0;
     int turn = 0;
     bool ok = true;
-    for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x, turn ^= 1) {
-      float2 acc[2][32];
+    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x, turn ^= 1) {
+      float2 acc[2][kPart / 2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) acc[h][j] = make_float2(0.f, 0.f);
+        for (int j = 0; j < kPart / 2; ++j) acc[h][j] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < num_k; ++kb, ++it) {
-        const int b = (int)(it & 1);
-        const uint32_t ph = (uint32_t)(it >> 1) & 1;
-        if (!(ok = warp_wait_phase(&sm.scale_full[b], ph, &sm.failed))) break;
-        if (!(ok = warp_wait_phase(&sm.acc_full[b], ph, &sm.failed))) break;
+        const uint32_t b = it & 1;
+        if (!(ok = warp_wait_phase(&sm.acc_full[b], (it >> 1) & 1, &sm.failed))) break;
         tcgen05_fence_after();
-        const float s = sm.sa[b][row];
-        const float2 sc[2] = {make_float2(s * sm.sw[b][0], s * sm.sw[b][0]),
-                              make_float2(s * sm.sw[b][1], s * sm.sw[b][1])};
-        const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * kTileW + part * 64;
-        uint32_t v[2][32];
-        tmem_load32(base, v[0]);
+        const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * kTileW + part * kPart;
+        uint32_t v[kPart];
+        tmem_load32(base, v);
+        const float s = sm.sa[b][row], s0 = s * sm.sw[b][0], s1 = s * sm.sw[b][1];
+        const float2 sc[2] = {make_float2(s0, s0), make_float2(s1, s1)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 32 columns each: two of either half
-          tmem_load_wait(v[c & 1]);
-          if (c < 3) {
-            tmem_load32(base + ((c + 1) >> 1) * kHalfW + ((c + 1) & 1) * 32, v[(c + 1) & 1]);
-          } else {  // all read: the products of the block after next may start
+        for (int h = 0; h < 2; ++h) {
+          if (h > 0) tmem_load32(base + kHalfW, v);
+          tmem_load_wait(v);
+          if (h > 0) {  // all read: the products of the block after next may start
             tcgen05_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float2 &x = acc[c >> 1][(c & 1) * 16 + j];
-            x = f2_fma(make_float2(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1])),
-                       sc[c >> 1], x);
-          }
+          for (int j = 0; j < kPart / 2; ++j)
+            acc[h][j] = f2_fma(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
+                               sc[h], acc[h][j]);
         }
       }
       if (!GATED && !ok) break;
@@ -306,29 +299,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int t0 = t.t0 + quarter * 32;  // this warp's first token
       if constexpr (!GATED) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // boxes of 32 columns, 64 bytes a row
-          uint8_t *p = box + (c & 1) * (32 * 64);
-          if (lane == 0) tma_store_wait_read<1>();
+        for (int h = 0; h < 2; ++h) {  // a box of 32 columns, 64 bytes a row
+          if (lane == 0) tma_store_wait_read<0>();
           __syncwarp();
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float2 *x = &acc[c >> 1][(c & 1) * 16 + q * 4];
-            *reinterpret_cast<uint4 *>(p + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+            const float2 *x = &acc[h][q * 4];
+            *reinterpret_cast<uint4 *>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
                 make_uint4(pack_bf16x2_rn(x[0].x, x[0].y), pack_bf16x2_rn(x[1].x, x[1].y),
                            pack_bf16x2_rn(x[2].x, x[2].y), pack_bf16x2_rn(x[3].x, x[3].y));
           }
           fence_proxy_async_smem();
           __syncwarp();
-          const int n = half_row<false>(a, t.n, c >> 1) + part * 64 + (c & 1) * 32;
+          const int n = half_row<false>(a, t.n, h) + part * kPart;
           if (lane == 0) {
-            if (t0 < a.T && n < a.N) tma_store_2d(&maps.out, p, n, t0);
+            if (t0 < a.T && n < a.N) tma_store_2d(&maps.out, box, n, t0);
             tma_store_commit();
           }
         }
       } else {
         float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < kPart / 2; ++j) {
           float2 &g = acc[0][j];
           g = make_float2(silu_mul(g.x, acc[1][j].x), silu_mul(g.y, acc[1][j].y));
           m = fmax3(m, fabsf(g.x), fabsf(g.y));
@@ -336,26 +328,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         sm.amax[turn][part][row] = m;
         // all of the warps leave together where a wait of one gave up
         if (named_sync_or(1, kSumWarps * 32, !ok)) break;
-        m = fmaxf(m, sm.amax[turn][part ^ 1][row]);
+#pragma unroll
+        for (int x = 0; x < kSumWarps / 4; ++x) m = fmaxf(m, sm.amax[turn][x][row]);
         const float s = group_scale(m, a.ue8m0 != 0);
         const float2 r = make_float2(__frcp_rn(s), __frcp_rn(s));
         if (lane == 0) tma_store_wait_read<0>();
         __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {  // a box of 32 columns, 32 bytes a row
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 x = f2_mul(acc[0][q * 8 + 2 * k], r), y = f2_mul(acc[0][q * 8 + 2 * k + 1], r);
             w[k] = cvt_e4m3x2(x.x, x.y) | (cvt_e4m3x2(y.x, y.y) << 16);
           }
-          *reinterpret_cast<uint4 *>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+          *reinterpret_cast<uint4 *>(box + lane * 32 + ((q ^ ((lane >> 2) & 1)) << 4)) =
               make_uint4(w[0], w[1], w[2], w[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (t0 < a.T) tma_store_2d(&maps.out, box, t.n * kHalfW + part * 64, t0);
+          if (t0 < a.T) tma_store_2d(&maps.out, box, t.n * kHalfW + part * kPart, t0);
           tma_store_commit();
         }
         if (part == 0 && t0 + lane < a.T) {
@@ -432,8 +425,8 @@ cudaError_t launch_tile(const GemmArgs &a, int sms, cudaStream_t s) {
   if (!make_map(&maps.a, u8, 1, a.a, a.T, a.K, kTileT, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&maps.w, u8, 1, a.w, (GATED ? 2 : 1) * (int64_t)a.N, a.K, kHalfW, kBlockK,
                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !(GATED ? make_map(&maps.out, u8, 1, a.q, a.T, a.N, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B)
-              : make_map(&maps.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.out, a.T, a.N, 32, 32,
+      !(GATED ? make_map(&maps.out, u8, 1, a.q, a.T, a.N, 32, kPart, CU_TENSOR_MAP_SWIZZLE_32B)
+              : make_map(&maps.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.out, a.T, a.N, 32, kPart,
                          CU_TENSOR_MAP_SWIZZLE_64B)))
     return cudaErrorInvalidValue;
   const int num_t = (a.T + kTileT - 1) / kTileT;
