@@ -7,11 +7,15 @@
 //           rounded to bf16), s = max(amax |y| over 128 columns, 1e-10) / 448
 //           (or the power of two above it), q = e4m3(y / s)
 //
-// Tile kernel.  A persistent CTA per SM computes tiles of 128 tokens x 256
-// weight rows (gated: 128 gate rows and the same 128 up rows), one scale
-// block (128 of K) at a time: TMA stages A and W in four 48 KB stages, one
-// thread issues four M128 N256 K32 products into one of two 256-column
-// accumulators, and sixteen warps take the block's sum out of tensor memory and
+// Tile kernel.  Persistent pairs of CTAs, one CTA per SM, compute tiles of 256
+// tokens x 256 weight rows (gated: 128 gate rows and the same 128 up rows), one
+// scale block (128 of K) at a time.  A CTA of the pair stages its 128 tokens
+// and one half of the weight rows by TMA in six 32 KB stages; one thread of
+// the pair issues four M256 N256 K32 products, which read the weight halves
+// of both (a CTA alone would stage and read all 256 weight rows: 96 KB of
+// shared memory traffic a block for 512 cycles of products, more than the
+// 128 bytes a cycle that there are; a pair needs 64 KB).  They go to one of
+// two 256-column accumulators, and in either CTA sixteen warps take the block's sum out of tensor memory and
 // add it, times its two scales, to an fp32 sum in registers (the block scales
 // are arbitrary fp32 numbers, so the tensor cores cannot apply them).  The
 // two accumulators let the products of the next block run meanwhile.  A
@@ -36,12 +40,11 @@ namespace {
 
 constexpr int kBlockK = 128;  // codes of K per scale block (and per stage)
 
-// Waits for a barrier phase; a wait that gives up is recorded, here for the
-// CTA and in the status word for the host.
+// Waits for a barrier phase; a wait that gives up is recorded for the CTA,
+// which reports it when it ends.
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile uint32_t *failed) {
   if (mbar_wait_bounded(bar, parity)) return true;
   *failed = 1;
-  atomicOr(&g_gemm_status, kErrWaitTimeout);
   return false;
 }
 
@@ -84,38 +87,38 @@ __device__ __forceinline__ float group_scale(float amax, bool ue8m0) {
 // ------------------------------------------------------------- tile kernel
 
 constexpr int kTileT = 128, kTileW = 256, kHalfW = 128;
-constexpr int kTileStages = 4;
-constexpr int kTileStageBytes = (kTileT + kTileW) * kBlockK;
+constexpr int kTileStages = 5, kScaleSlots = 8;
+constexpr int kTileStageBytes = (kTileT + kHalfW) * kBlockK;  // of either CTA
 constexpr int kSumWarps = 16, kTileThreads = 128 + 32 * kSumWarps;
 constexpr int kPart = kHalfW * 4 / kSumWarps;  // columns of either half that a thread sums
 // The launch holds 640 x 96 registers; the split hands out 128 x 56 + 512 x 104.
-constexpr int kTileGroup = 32;  // token tiles that share a sweep over the weight
+constexpr int kTileGroup = 16;  // token tiles of a pair that share a sweep over the weight
 
-// Dynamic shared memory, after alignment to 1024 bytes.
+// Dynamic shared memory (1024-byte aligned).
 template <bool GATED>
 struct TileSmem {
   uint8_t stage[kTileStages][kTileStageBytes];
   uint8_t out[kSumWarps][32 * kPart * (GATED ? 1 : 2)];  // a box of 32 rows
-  float sa[2][kTileT];
-  float sw[2][2];
+  float sa[kScaleSlots][kTileT];
+  float sw[kScaleSlots][2];
   float amax[GATED ? 2 : 1][GATED ? kSumWarps / 4 : 1][GATED ? kTileT : 1];
   uint64_t full[kTileStages], empty[kTileStages];
-  uint64_t acc_full[2], acc_empty[2], drain;
+  uint64_t acc_full[2], acc_empty[2], scale_full[kScaleSlots], scale_empty[kScaleSlots], drain;
   uint32_t tmem;
   uint32_t failed;
 };
 
-// The k-th tile of this CTA: token tiles run fastest within groups of
+// The i-th tile: token tiles run fastest within groups of
 // kTileGroup, so that the tiles in flight share weight rows and the group's
 // activations stay in L2 while the weight streams by.
 struct Tile {
-  int t0;  // first token
+  int t0;  // first token of the pair
   int n;   // weight tile
 };
 __device__ __forceinline__ Tile tile_at(uint32_t i, uint32_t num_t, uint32_t num_n) {
   const uint32_t per_group = kTileGroup * num_n, g = i / per_group, r = i - g * per_group;
   const uint32_t rows = min((uint32_t)kTileGroup, num_t - g * kTileGroup), n = r / rows;
-  return {(int)(g * kTileGroup + r - n * rows) * kTileT, (int)n};
+  return {(int)(g * kTileGroup + r - n * rows) * 2 * kTileT, (int)n};
 }
 
 // First weight rows of a tile's two halves.
@@ -131,12 +134,13 @@ struct GemmMaps {
 template <bool GATED>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fp8_gemm_tile_kernel(const GemmArgs a, const __grid_constant__ GemmMaps maps, int num_t, int num_n) {
-  extern __shared__ uint8_t raw[];
-  using Smem = TileSmem<GATED>;
-  Smem &sm = *reinterpret_cast<Smem *>(raw + (1024 - (smem_u32(raw) & 1023)) % 1024);
+  extern __shared__ __align__(1024) uint8_t raw[];
+  TileSmem<GATED> &sm = *reinterpret_cast<TileSmem<GATED> *>(raw);
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
   const int num_k = a.K / kBlockK;
   const uint32_t tiles = (uint32_t)num_t * (uint32_t)num_n;  // at most 2^29
+  const uint32_t rank = cluster_rank(), first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int my_t = (int)rank * kTileT;  // this CTA's tokens within the pair's
   VG_NEVER_BARRIER;
 
   if (warp == 0 && lane == 0) {
@@ -148,8 +152,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.acc_full[i], 2);  // the products and the scales
-      mbar_init(&sm.acc_empty[i], kSumWarps);
+      mbar_init(&sm.acc_full[i], 1);
+      mbar_init(&sm.acc_empty[i], 2 * kSumWarps);  // of both CTAs (the first CTA's counts)
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(&sm.scale_full[i], 32);
+      mbar_init(&sm.scale_empty[i], kSumWarps);
     }
     mbar_init(&sm.drain, 1);
     VG_NEVER_BARRIER_INIT();
@@ -159,101 +167,98 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == 1) tmem_alloc(&sm.tmem, 512);
   tcgen05_fence_before();
   __syncthreads();
+  cluster_sync();  // the pair's barriers are initialised
   tcgen05_fence_after();
   const uint32_t tmem = sm.tmem;
   pdl_wait();
   pdl_launch_dependents();
-  int issued = 0;  // stages this thread has filled (warp 0 lane 0)
+  uint32_t issued = 0;  // stages this CTA has filled (warp 0)
 
   if (warp < 4) {
     regs_decrease<56>();
-    if (warp == 0 && lane == 0) {
-      int it = 0;
+    if (warp == 0) {
+      uint32_t it = 0, s = 0, lap = 0;
       bool ok = true;
-      for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+      for (uint32_t i = first; i < tiles && ok; i += pairs) {
         const Tile t = tile_at(i, num_t, num_n);
-        const int r0 = half_row<GATED>(a, t.n, 0), r1 = half_row<GATED>(a, t.n, 1);
+        const int r0 = half_row<GATED>(a, t.n, (int)rank);
         for (int kb = 0; kb < num_k; ++kb, ++it) {
-          const int s = it % kTileStages;
-          if (it >= kTileStages && !(ok = wait_phase(&sm.empty[s], (it / kTileStages - 1) & 1, &sm.failed)))
-            break;
-          mbar_arrive_expect_tx(&sm.full[s], kTileStageBytes);
-          uint8_t *p = sm.stage[s];
-          tma_load_2d(p, &maps.a, kb * kBlockK, t.t0, &sm.full[s]);
-          tma_load_2d(p + kTileT * kBlockK, &maps.w, kb * kBlockK, r0, &sm.full[s]);
-          tma_load_2d(p + (kTileT + kHalfW) * kBlockK, &maps.w, kb * kBlockK, r1, &sm.full[s]);
+          if (lap > 0 && !(ok = warp_wait_phase(&sm.empty[s], (lap - 1) & 1, &sm.failed))) break;
+          if (elect_lane()) {
+            if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kTileStageBytes);
+            uint8_t *p = sm.stage[s];
+            const uint32_t bar = cluster_addr(&sm.full[s], 0);
+            tma_load_2d_pair(p, &maps.a, kb * kBlockK, t.t0 + my_t, bar);
+            tma_load_2d_pair(p + kTileT * kBlockK, &maps.w, kb * kBlockK, r0, bar);
+          }
+          __syncwarp();
           ++issued;
+          if (++s == kTileStages) s = 0, ++lap;
         }
       }
-    } else if (warp == 1 && lane == 0) {
-      constexpr uint32_t desc = product_desc(kTileT, kTileW);
-      int it = 0;
+    } else if (warp == 1 && rank == 0) {
+      constexpr uint32_t desc = product_desc(2 * kTileT, kTileW);
+      uint32_t it = 0, s = 0, lap = 0;
       bool ok = true;
-      for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x)
+      for (uint32_t i = first; i < tiles && ok; i += pairs)
         for (int kb = 0; kb < num_k; ++kb, ++it) {
-          const int s = it % kTileStages, b = it & 1;
-          if (it >= 2 && !(ok = wait_phase(&sm.acc_empty[b], (it / 2 - 1) & 1, &sm.failed))) break;
-          if (!(ok = wait_phase(&sm.full[s], (it / kTileStages) & 1, &sm.failed))) break;
+          const uint32_t b = it & 1;
+          // Operands staged and accumulator free: half of the lanes wait for
+          // either (one after the other would put both waits' latencies, some
+          // 200 cycles each even when nothing is left to wait for, before
+          // every block's products).
+          const bool odd = lane & 1;
+          if (!(ok = __all_sync(0xFFFFFFFFu, (odd && it < 2) ||
+                                                 wait_phase(odd ? &sm.acc_empty[b] : &sm.full[s],
+                                                            odd ? (it / 2 - 1) & 1 : lap & 1, &sm.failed))))
+            break;
           if (VG_FORCED_TIMEOUT(it == 0)) {
             sm.failed = 1;
-            atomicOr(&g_gemm_status, kErrWaitTimeout);
             ok = false;
             break;
           }
           tcgen05_fence_after();
-          const uint64_t da = operand_desc(smem_u32(sm.stage[s]));
-          const uint64_t dw = operand_desc(smem_u32(sm.stage[s] + kTileT * kBlockK));
+          if (elect_lane()) {
+            const uint64_t da = operand_desc(smem_u32(sm.stage[s]));
+            const uint64_t dw = operand_desc(smem_u32(sm.stage[s] + kTileT * kBlockK));
 #pragma unroll
-          for (int k = 0; k < kBlockK / 32; ++k)
-            mma_e4m3(tmem + b * kTileW, da + 2 * k, dw + 2 * k, desc, k > 0);
-          mma_commit(&sm.empty[s]);
-          mma_commit(&sm.acc_full[b]);
+            for (int k = 0; k < kBlockK / 32; ++k)
+              mma_e4m3(tmem + b * kTileW, da + 2 * k, dw + 2 * k, desc, k > 0);
+            mma_commit_pair(&sm.acc_full[b]);
+            mma_commit_pair(&sm.empty[s]);
+          }
+          __syncwarp();
+          if (++s == kTileStages) s = 0, ++lap;
         }
       // Nothing is in flight once this arrives (at once, unless a wait gave up).
-      mma_commit(&sm.drain);
+      if (elect_lane()) mma_commit(&sm.drain);
+      __syncwarp();
       (void)mbar_wait_bounded(&sm.drain, 0);
     } else if (warp == 2) {
-      // Two blocks ahead: a block's scales are on their way to registers
-      // while the two before it are used.
-      float va[2][4], vw[2];
-      uint32_t i = blockIdx.x;
-      int kb = 0;
-      const auto fetch = [&](float(&v)[4], float &w) {
-        if (i >= tiles) return;
+      // Scales go straight to shared memory, eight blocks ahead (measured with
+      // two blocks of them prefetched in registers: their L2 latency, not the
+      // products, set the pace, 1980 instead of 2800 TFLOP/s).
+      uint32_t it = 0, s = 0, lap = 0;
+      bool ok = true;
+      for (uint32_t i = first; i < tiles && ok; i += pairs) {
         const Tile t = tile_at(i, num_t, num_n);
+        const int r = half_row<GATED>(a, t.n, lane & 1), row = t.t0 + my_t + lane;
+        const bool w_live = r < (GATED ? 2 : 1) * a.N;
+        const float *pw = a.w_scale + (w_live ? (int64_t)(r / kBlockK) * num_k : 0);
+        for (int kb = 0; kb < num_k; ++kb, ++it) {
+          if (lap > 0 && !(ok = warp_wait_phase(&sm.scale_empty[s], (lap - 1) & 1, &sm.failed))) break;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int row = t.t0 + lane + 32 * j;
-          v[j] = row < a.T ? __ldg(a.a_scale + row * a.a_ts + kb * a.a_bs) : 0.f;
+          for (int j = 0; j < 4; ++j) {
+            const bool live = row + 32 * j < a.T;
+            copy_async4(&sm.sa[s][lane + 32 * j],
+                        a.a_scale + (live ? (row + 32 * j) * a.a_ts + kb * a.a_bs : 0), live);
+          }
+          if (lane < 2) copy_async4(&sm.sw[s][lane], pw + (w_live ? kb : 0), w_live);
+          copy_async_arrive(&sm.scale_full[s]);
+          if (++s == kScaleSlots) s = 0, ++lap;
         }
-        if (lane < 2) {
-          const int r = half_row<GATED>(a, t.n, lane);
-          w = r < (GATED ? 2 : 1) * a.N ? __ldg(a.w_scale + (int64_t)(r / kBlockK) * num_k + kb) : 0.f;
-        }
-        if (++kb == num_k) {
-          kb = 0;
-          i += gridDim.x;
-        }
-      };
-      fetch(va[0], vw[0]);
-      fetch(va[1], vw[1]);
-      const uint32_t mine = (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x * (uint32_t)num_k;
-      for (uint32_t it = 0; it < mine; it += 2) {
-        bool ok = true;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (it + b >= mine) break;
-          if (it >= 2 && !(ok = warp_wait_phase(&sm.acc_empty[b], (it / 2 - 1) & 1, &sm.failed)))
-            break;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sm.sa[b][lane + 32 * j] = va[b][j];
-          if (lane < 2) sm.sw[b][lane] = vw[b];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.acc_full[b]);
-          fetch(va[b], vw[b]);
-        }
-        if (!ok) break;
       }
+      copy_async_wait_all();
     }
   } else {
     regs_increase<104>();
@@ -263,40 +268,47 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint32_t it = 0;
     int turn = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x, turn ^= 1) {
+    for (uint32_t i = first; i < tiles; i += pairs, turn ^= 1) {
       float2 acc[2][kPart / 2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < kPart / 2; ++j) acc[h][j] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < num_k; ++kb, ++it) {
-        const uint32_t b = it & 1;
-        if (!(ok = warp_wait_phase(&sm.acc_full[b], (it >> 1) & 1, &sm.failed))) break;
+        const uint32_t b = it & 1, ss = it % kScaleSlots;
+        const bool odd = lane & 1;  // half of the lanes wait for either barrier
+        if (!(ok = warp_wait_phase(odd ? &sm.scale_full[ss] : &sm.acc_full[b],
+                                   (odd ? it / kScaleSlots : it / 2) & 1, &sm.failed)))
+          break;
         tcgen05_fence_after();
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * kTileW + part * kPart;
         uint32_t v[kPart];
         tmem_load32(base, v);
-        const float s = sm.sa[b][row], s0 = s * sm.sw[b][0], s1 = s * sm.sw[b][1];
-        const float2 sc[2] = {make_float2(s0, s0), make_float2(s1, s1)};
+        const float s = sm.sa[ss][row];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h > 0) tmem_load32(base + kHalfW, v);
+          const float sh = s * sm.sw[ss][h];
+          const float2 sc = make_float2(sh, sh);
           tmem_load_wait(v);
           if (h > 0) {  // all read: the products of the block after next may start
             tcgen05_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
+            if (lane == 0) {
+              mbar_arrive_cluster(cluster_addr(&sm.acc_empty[b], 0));
+              mbar_arrive(&sm.scale_empty[ss]);
+            }
           }
 #pragma unroll
           for (int j = 0; j < kPart / 2; ++j)
             acc[h][j] = f2_fma(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
-                               sc[h], acc[h][j]);
+                               sc, acc[h][j]);
         }
       }
       if (!GATED && !ok) break;
 
       const Tile t = tile_at(i, num_t, num_n);
-      const int t0 = t.t0 + quarter * 32;  // this warp's first token
+      const int t0 = t.t0 + my_t + quarter * 32;  // this warp's first token
       if constexpr (!GATED) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // a box of 32 columns, 64 bytes a row
@@ -361,10 +373,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 
   __syncthreads();
-  if (sm.failed && warp == 0 && lane == 0)  // copies still in flight end here
-    for (int it = issued < kTileStages ? 0 : issued - kTileStages; it < issued; ++it)
-      (void)mbar_wait_bounded(&sm.full[it % kTileStages], (it / kTileStages) & 1);
-  __syncthreads();
+  if (sm.failed && warp == 0 && lane == 0) {  // the pair's copies in flight end here
+    atomicOr(&g_gemm_status, kErrWaitTimeout);
+    if (rank == 0)
+      for (uint32_t it = issued < kTileStages ? 0 : issued - kTileStages; it < issued; ++it)
+        (void)mbar_wait_bounded(&sm.full[it % kTileStages], (it / kTileStages) & 1);
+    // copies that the other CTA issued ahead of this one's count: a millisecond
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
+  cluster_sync();  // neither CTA's memory is in use by the other any more
+  __syncwarp();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
@@ -403,6 +421,26 @@ bool make_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *p,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// launch_pdl with thread-block clusters of `cluster` CTAs along x.
+template <class... P, class... A>
+cudaError_t launch_pdl_cluster(void (*kern)(P...), dim3 g, int cluster, dim3 b, size_t smem,
+                               cudaStream_t s, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = g;
+  cfg.blockDim = b;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<A &&>(args)...);
+}
+
 // Opts `kern` in to large dynamic shared memory, once per kernel and device.
 cudaError_t opt_in_once(std::atomic<uint64_t> &opted_in, const void *kern) {
   int dev = 0;
@@ -429,12 +467,12 @@ cudaError_t launch_tile(const GemmArgs &a, int sms, cudaStream_t s) {
               : make_map(&maps.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.out, a.T, a.N, 32, kPart,
                          CU_TENSOR_MAP_SWIZZLE_64B)))
     return cudaErrorInvalidValue;
-  const int num_t = (a.T + kTileT - 1) / kTileT;
+  const int num_t = (a.T + 2 * kTileT - 1) / (2 * kTileT);
   const int num_n = GATED ? a.N / kHalfW : (a.N + kTileW - 1) / kTileW;
   const int64_t tiles = (int64_t)num_t * num_n;
-  const dim3 grid((unsigned)(tiles < sms ? tiles : sms));
-  return launch_pdl(fp8_gemm_tile_kernel<GATED>, grid, dim3(kTileThreads), sizeof(TileSmem<GATED>) + 1024,
-                    s, a, maps, num_t, num_n);
+  const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
+  return launch_pdl_cluster(fp8_gemm_tile_kernel<GATED>, dim3(2 * pairs), 2, dim3(kTileThreads),
+                            sizeof(TileSmem<GATED>), s, a, maps, num_t, num_n);
 }
 
 }  // namespace

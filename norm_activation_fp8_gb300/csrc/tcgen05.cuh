@@ -17,16 +17,60 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
-// One box of a 2-D tensor to shared memory, counted on `bar`; elements
-// outside the tensor arrive as zeros (and are counted).  x times the element
-// size must be a multiple of 16 bytes.
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
-                                            uint64_t *bar) {
+// One box of a 2-D tensor to this CTA's shared memory, counted on the barrier
+// at cluster address `bar` (of either CTA of a pair); elements outside the
+// tensor arrive as zeros (and are counted).  x times the element size must be
+// a multiple of 16 bytes.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
+                                                 uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
+      "l"(m), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+// One lane of a converged warp, the same one each time.  The warps that issue
+// copies and products run their loops as whole warps and elect the issuing
+// lane at the instruction: with the loop itself on one lane the compiler must
+// treat every operand as divergent (measured: 614 cycles of the issuing
+// thread per scale block).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+
+// ---------------------------------------------------------------- clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// The cluster address of `p` in the shared memory of CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+
+// Arrives on the barrier at a cluster address.  Relaxed: it hands over tensor
+// memory that has been read (ordered by the tcgen05 fences), not memory that
+// has been written; a release at cluster scope would cost about a thousand
+// cycles here.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// All threads of the cluster's CTAs.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // One box from shared memory to a 2-D tensor; what lies outside the tensor is
@@ -49,19 +93,37 @@ __device__ __forceinline__ void tma_store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// ------------------------------------------------------ small async copies
+
+// Four bytes from global to shared memory, or four zero bytes (nothing is
+// read) where `live` is false.
+__device__ __forceinline__ void copy_async4(void *dst, const void *src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(live ? 4u : 0u)
+               : "memory");
+}
+// Arrives on `bar` once this thread's earlier small copies have landed.
+__device__ __forceinline__ void copy_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // ------------------------------------------------------------ tensor memory
 
 // A whole warp allocates (a power of two >= 32 columns); the base address
 // lands in shared memory.  The permit is given up: one allocation per CTA.
+// Both CTAs of a pair call it, and the release, together.
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
                "r"(columns)
                : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns)
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns)
                : "memory");
 }
 
@@ -119,21 +181,32 @@ __host__ __device__ constexpr uint32_t product_desc(uint32_t m, uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// D (tensor memory) = A B^T (+ D if accumulate) over K = 32; one thread.
+// D (tensor memory) = A B^T (+ D if accumulate) over K = 32, issued by one
+// thread of the pair's first CTA: rows 0..127 of A and D and the first half
+// of B's rows are the first CTA's, the others the second's, at the same
+// addresses of either.
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                          bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
       : "memory");
 }
 
-// Arrives on `bar` once this thread's earlier products have finished.
+// Arrives on `bar` of both CTAs of the pair (or of this one alone) once this
+// thread's earlier products have finished.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
       : "memory");
 }
 
