@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     fence_mbar_init();
     sm.failed = 0;
   }
-  if (warp == 1) tmem_alloc(&sm.tmem, 512);
+  if (warp == 1) tmem_alloc<true>(&sm.tmem, 512);
   tcgen05_fence_before();
   __syncthreads();
   cluster_sync();  // the pair's barriers are initialised
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const uint64_t dw = operand_desc(smem_u32(sm.stage[s] + kTileT * kBlockK));
 #pragma unroll
             for (int k = 0; k < kBlockK / 32; ++k)
-              mma_e4m3(tmem + b * kTileW, da + 2 * k, dw + 2 * k, desc, k > 0);
+              mma_e4m3<true>(tmem + b * kTileW, da + 2 * k, dw + 2 * k, desc, k > 0);
             mma_commit_pair(&sm.acc_full[b]);
             mma_commit_pair(&sm.empty[s]);
           }
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (++s == kTileStages) s = 0, ++lap;
         }
       // Nothing is in flight once this arrives (at once, unless a wait gave up).
-      if (elect_lane()) mma_commit(&sm.drain);
+      if (elect_lane()) mma_commit<true>(&sm.drain);
       __syncwarp();
       (void)mbar_wait_bounded(&sm.drain, 0);
     } else if (warp == 2) {
@@ -383,7 +383,260 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   cluster_sync();  // neither CTA's memory is in use by the other any more
   __syncwarp();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc<true>(tmem, 512);
+}
+
+// ----------------------------------------------------------- stream kernel
+//
+// For few tokens, where the weight's bytes are the cost.  Operands change
+// places: a CTA's tile is 128 weight rows (gated: 64 gate rows and the same 64
+// up rows) x TN tokens, so that sixteen tokens fill a product, and K is split
+// over a cluster, as many ways as fill the GPU.  The sums stay in fp32
+// registers, a thread a weight row; at the end each CTA puts its partial sums
+// in shared memory and the cluster adds them in a fixed order, every CTA some
+// of the tokens, a warp a token: for the gated form the two CTAs of a scale
+// group (64 columns each) meet there too.
+//   warp 0: TMA   warp 1: products   warp 2: scales   warps 4-7: sums
+// Up to 64 tokens two CTAs share an SM (each asks for more than a third of its
+// shared memory and for at most half of its tensor memory, so no allocation
+// ever waits).
+
+constexpr int kStreamThreads = 256;
+constexpr int kMaxSplit = 8;
+
+template <int TN>
+struct StreamSmem {
+  static constexpr int kStageBytes = (kHalfW + TN) * kBlockK;
+  static constexpr int kStages = TN <= 32 ? 5 : (TN == 64 ? 4 : 6);
+  static constexpr int kBufs = TN <= 64 ? 4 : 2;  // accumulators
+  static constexpr int kColumns = kBufs * TN;     // of tensor memory
+  union {
+    uint8_t stage[kStages][kStageBytes];
+    float part[TN][kHalfW];  // partial sums, once the products are done
+  };
+  float sa[kScaleSlots][TN];
+  float sw[kScaleSlots][2];
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[kBufs], acc_empty[kBufs], scale_full[kScaleSlots], scale_empty[kScaleSlots], drain;
+  uint32_t tmem;
+  uint32_t failed;
+};
+
+template <bool GATED, int TN>
+__global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
+    fp8_gemm_stream_kernel(const GemmArgs a, const __grid_constant__ GemmMaps maps, int splits) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  using Smem = StreamSmem<TN>;
+  Smem &sm = *reinterpret_cast<Smem *>(raw);
+  constexpr int kStages = Smem::kStages, kBufs = Smem::kBufs;
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  const int num_k = a.K / kBlockK;
+  const int rank = (int)cluster_rank(), ctas = GATED ? 2 * splits : splits;
+  const int tile = (int)blockIdx.x / ctas, split = GATED ? rank >> 1 : rank;
+  // first weight rows of the tile's two halves, first token, scale blocks
+  const int r0 = tile * kHalfW + (GATED ? (rank & 1) * (kHalfW / 2) : 0);
+  const int r1 = GATED ? a.N + r0 : r0 + kHalfW / 2;
+  const int t0 = (int)blockIdx.y * TN;
+  const int k0 = num_k * split / splits, k1 = num_k * (split + 1) / splits;
+  VG_NEVER_BARRIER;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&maps.a);
+    prefetch_tensormap(&maps.w);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&sm.acc_full[i], 1);
+      mbar_init(&sm.acc_empty[i], 4);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(&sm.scale_full[i], 32);
+      mbar_init(&sm.scale_empty[i], 4);
+    }
+    mbar_init(&sm.drain, 1);
+    VG_NEVER_BARRIER_INIT();
+    fence_mbar_init();
+    sm.failed = 0;
+  }
+  if (warp == 1) tmem_alloc<false>(&sm.tmem, Smem::kColumns);
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  const uint32_t tmem = sm.tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+  int issued = 0;  // stages filled (warp 0)
+
+  if (warp == 0) {
+    int s = 0, lap = 0;
+    for (int kb = k0; kb < k1; ++kb) {
+      if (lap > 0 && !warp_wait_phase(&sm.empty[s], (lap - 1) & 1, &sm.failed)) break;
+      if (elect_lane()) {
+        mbar_arrive_expect_tx(&sm.full[s], Smem::kStageBytes);
+        uint8_t *p = sm.stage[s];
+        tma_load_2d(p, &maps.w, kb * kBlockK, r0, &sm.full[s]);
+        tma_load_2d(p + kHalfW / 2 * kBlockK, &maps.w, kb * kBlockK, r1, &sm.full[s]);
+        tma_load_2d(p + kHalfW * kBlockK, &maps.a, kb * kBlockK, t0, &sm.full[s]);
+      }
+      __syncwarp();
+      ++issued;
+      if (++s == kStages) s = 0, ++lap;
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t desc = product_desc(kHalfW, TN);
+    int s = 0, lap = 0;
+    for (int kb = k0; kb < k1; ++kb) {
+      const int it = kb - k0, b = it % kBufs;
+      const bool odd = lane & 1;  // half of the lanes wait for either barrier
+      if (!__all_sync(0xFFFFFFFFu, (odd && it < kBufs) ||
+                                       wait_phase(odd ? &sm.acc_empty[b] : &sm.full[s],
+                                                  odd ? (it / kBufs - 1) & 1 : lap & 1, &sm.failed)))
+        break;
+      if (VG_FORCED_TIMEOUT(it == 0)) {
+        sm.failed = 1;
+        break;
+      }
+      tcgen05_fence_after();
+      if (elect_lane()) {
+        const uint64_t dw = operand_desc(smem_u32(sm.stage[s]));
+        const uint64_t da = operand_desc(smem_u32(sm.stage[s] + kHalfW * kBlockK));
+#pragma unroll
+        for (int k = 0; k < kBlockK / 32; ++k)
+          mma_e4m3<false>(tmem + b * TN, dw + 2 * k, da + 2 * k, desc, k > 0);
+        mma_commit<false>(&sm.acc_full[b]);
+        mma_commit<false>(&sm.empty[s]);
+      }
+      __syncwarp();
+      if (++s == kStages) s = 0, ++lap;
+    }
+    if (elect_lane()) mma_commit<false>(&sm.drain);
+    __syncwarp();
+    (void)mbar_wait_bounded(&sm.drain, 0);
+  } else if (warp == 2) {
+    const int r = lane & 1 ? r1 : r0;
+    const bool w_live = r < (GATED ? 2 : 1) * a.N;
+    const float *pw = a.w_scale + (w_live ? (int64_t)(r / kBlockK) * num_k : 0);
+    int s = 0, lap = 0;
+    for (int kb = k0; kb < k1; ++kb) {
+      if (lap > 0 && !warp_wait_phase(&sm.scale_empty[s], (lap - 1) & 1, &sm.failed)) break;
+#pragma unroll
+      for (int j = 0; j < (TN + 31) / 32; ++j) {
+        const int t = lane + 32 * j;
+        const bool live = t0 + t < a.T;
+        if (t < TN)
+          copy_async4(&sm.sa[s][t], a.a_scale + (live ? (t0 + t) * a.a_ts + kb * a.a_bs : 0), live);
+      }
+      if (lane < 2) copy_async4(&sm.sw[s][lane], pw + (w_live ? kb : 0), w_live);
+      copy_async_arrive(&sm.scale_full[s]);
+      if (++s == kScaleSlots) s = 0, ++lap;
+    }
+    copy_async_wait_all();
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    float2 acc[TN / 2];
+#pragma unroll
+    for (int j = 0; j < TN / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+    for (int kb = k0; kb < k1; ++kb) {
+      const int it = kb - k0, b = it % kBufs, ss = it % kScaleSlots;
+      const bool odd = lane & 1;
+      if (!warp_wait_phase(odd ? &sm.scale_full[ss] : &sm.acc_full[b],
+                           (odd ? it / kScaleSlots : it / kBufs) & 1, &sm.failed))
+        break;
+      tcgen05_fence_after();
+      const float w = sm.sw[ss][quarter >> 1];
+      const float2 w2 = make_float2(w, w);
+      constexpr int kLoad = TN < 32 ? TN : 32;
+#pragma unroll
+      for (int c = 0; c < TN / kLoad; ++c) {
+        uint32_t v[kLoad];
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + b * TN + c * kLoad;
+        if constexpr (kLoad == 16) {
+          tmem_load16(at, v);
+        } else {
+          tmem_load32(at, v);
+          tmem_load_wait(v);
+        }
+        float4 sa[kLoad / 4];
+#pragma unroll
+        for (int j = 0; j < kLoad / 4; ++j)
+          sa[j] = *reinterpret_cast<const float4 *>(&sm.sa[ss][c * kLoad + 4 * j]);
+        if (c == TN / kLoad - 1) {  // all read
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.acc_empty[b]);
+            mbar_arrive(&sm.scale_empty[ss]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kLoad / 4; ++j) {
+          const float2 s0 = f2_mul(make_float2(sa[j].x, sa[j].y), w2), s1 = f2_mul(make_float2(sa[j].z, sa[j].w), w2);
+          float2 &x = acc[c * kLoad / 2 + 2 * j], &y = acc[c * kLoad / 2 + 2 * j + 1];
+          x = f2_fma(make_float2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), s0, x);
+          y = f2_fma(make_float2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), s1, y);
+        }
+      }
+    }
+    // The last block's products are done, so nothing reads the stages.
+    if (!sm.failed) {
+#pragma unroll
+      for (int j = 0; j < TN / 2; ++j) {
+        sm.part[2 * j][row] = acc[j].x;
+        sm.part[2 * j + 1][row] = acc[j].y;
+      }
+    }
+  }
+
+  __syncthreads();
+  if (sm.failed && warp == 0 && lane == 0) {  // copies in flight end here
+    atomicOr(&g_gemm_status, kErrWaitTimeout);
+    for (int it = issued < kStages ? 0 : issued - kStages; it < issued; ++it)
+      (void)mbar_wait_bounded(&sm.full[it % kStages], (it / kStages) & 1);
+  }
+  cluster_sync();  // every CTA's partial sums are in place
+  __syncwarp();
+  if (warp == 1) tmem_dealloc<false>(tmem, Smem::kColumns);
+
+  const int tokens = min(TN, a.T - t0);
+  for (int j = rank + warp * ctas; j < tokens; j += (kStreamThreads / 32) * ctas) {
+    const int64_t t = t0 + j;
+    if constexpr (!GATED) {
+      float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = 0; x < splits; ++x) {
+        const float4 p = ld_cluster4(cluster_addr(&sm.part[j][4 * lane], (uint32_t)x));
+        c = make_float4(c.x + p.x, c.y + p.y, c.z + p.z, c.w + p.w);
+      }
+      const int n = r0 + 4 * lane;
+      uint16_t *o = a.out + t * a.N + n;
+      if (n < a.N && VG_ACCESS_OK(g_gemm_status, o, 8, a.out, VG_ROWS(a.T) * 2ull * (uint64_t)a.N))
+        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2_rn(c.x, c.y), pack_bf16x2_rn(c.z, c.w));
+    } else {
+      // lane: columns 4 lane .. of the group, from the half that has them
+      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+      const int col = (4 * lane) & (kHalfW / 2 - 1);
+      for (int x = 0; x < splits; ++x) {
+        const uint32_t from = 2 * (uint32_t)x + (uint32_t)(lane >> 4);
+        const float4 p = ld_cluster4(cluster_addr(&sm.part[j][col], from));
+        const float4 q = ld_cluster4(cluster_addr(&sm.part[j][kHalfW / 2 + col], from));
+        g = make_float4(g.x + p.x, g.y + p.y, g.z + p.z, g.w + p.w);
+        u = make_float4(u.x + q.x, u.y + q.y, u.z + q.z, u.w + q.w);
+      }
+      const float y0 = silu_mul(g.x, u.x), y1 = silu_mul(g.y, u.y);
+      const float y2 = silu_mul(g.z, u.z), y3 = silu_mul(g.w, u.w);
+      const float m = warp_max(fmax3(fmax3(fabsf(y0), fabsf(y1), fabsf(y2)), fabsf(y3), 0.f));
+      const float s = group_scale(m, a.ue8m0 != 0), r = __frcp_rn(s);
+      uint8_t *o = a.q + t * a.N + (int64_t)tile * kHalfW + 4 * lane;
+      if (VG_ACCESS_OK(g_gemm_status, o, 4, a.q, VG_ROWS(a.T) * (uint64_t)a.N))
+        *reinterpret_cast<uint32_t *>(o) = cvt_e4m3x2(y0 * r, y1 * r) | (cvt_e4m3x2(y2 * r, y3 * r) << 16);
+      if (lane == 0) {
+        float *p = a.scale + t * a.s_ts + (int64_t)tile * a.s_gs;
+        if (VG_ACCESS_OK(g_gemm_status, p, 4, a.scale, gemm_scale_extent(a))) *p = s;
+      }
+    }
+  }
+  cluster_sync();  // nobody reads this CTA's sums any more
 }
 
 // ------------------------------------------------------------------- host
@@ -475,10 +728,60 @@ cudaError_t launch_tile(const GemmArgs &a, int sms, cudaStream_t s) {
                             sizeof(TileSmem<GATED>), s, a, maps, num_t, num_n);
 }
 
+template <bool GATED, int TN>
+cudaError_t launch_stream(const GemmArgs &a, int splits, cudaStream_t s) {
+  static std::atomic<uint64_t> opted_in{0};
+  const cudaError_t e = opt_in_once(opted_in, (const void *)fp8_gemm_stream_kernel<GATED, TN>);
+  if (e != cudaSuccess) return e;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  GemmMaps maps;
+  if (!make_map(&maps.a, u8, 1, a.a, a.T, a.K, TN, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&maps.w, u8, 1, a.w, (GATED ? 2 : 1) * (int64_t)a.N, a.K, kHalfW / 2, kBlockK,
+                CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  maps.out = maps.a;  // not used: the sums are stored by threads
+  const int ctas = GATED ? 2 * splits : splits;
+  const dim3 grid((unsigned)((a.N + kHalfW - 1) / kHalfW * ctas), (unsigned)((a.T + TN - 1) / TN));
+  return launch_pdl_cluster(fp8_gemm_stream_kernel<GATED, TN>, grid, ctas, dim3(kStreamThreads),
+                            sizeof(StreamSmem<TN>), s, a, maps, splits);
+}
+
+template <bool GATED>
+cudaError_t launch_form(const GemmArgs &a, const GemmPlan &p, int sms, cudaStream_t s) {
+  switch (p.tn) {
+    case 16: return launch_stream<GATED, 16>(a, p.splits, s);
+    case 32: return launch_stream<GATED, 32>(a, p.splits, s);
+    case 64: return launch_stream<GATED, 64>(a, p.splits, s);
+    case 128: return launch_stream<GATED, 128>(a, p.splits, s);
+    default: return launch_tile<GATED>(a, sms, s);
+  }
+}
+
 }  // namespace
 
+GemmPlan plan_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
+  GemmPlan p;
+  const int64_t rows = (N + kHalfW - 1) / kHalfW;  // weight tiles of the stream kernel
+  const int64_t pairs = (T + 2 * kTileT - 1) / (2 * kTileT) * (gated ? N / kHalfW : (N + kTileW - 1) / kTileW);
+  if (T > 128 && 2 * pairs >= sms / 2) return p;  // tn 0: the tile kernel
+  p.tn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
+  const int64_t slots = (int64_t)sms * (p.tn <= 64 ? 2 : 1), blocks = K / kBlockK;
+  const int64_t tiles = rows * ((T + p.tn - 1) / p.tn) * (gated ? 2 : 1);
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= (gated ? kMaxSplit / 2 : kMaxSplit) && s <= blocks; ++s) {
+    // waves times the longest split, with six blocks' time for a CTA's start and end
+    const int64_t cost = (tiles * s + slots - 1) / slots * ((blocks + s - 1) / s + 6);
+    if (cost < best) {
+      best = cost;
+      p.splits = s;
+    }
+  }
+  return p;
+}
+
 cudaError_t launch_fp8_gemm(const GemmArgs &a, bool gated, int sms, cudaStream_t s) {
-  return gated ? launch_tile<true>(a, sms, s) : launch_tile<false>(a, sms, s);
+  const GemmPlan p = plan_gemm(a.T, a.N, a.K, gated, sms);
+  return gated ? launch_form<true>(a, p, sms, s) : launch_form<false>(a, p, sms, s);
 }
 
 uint32_t read_gemm_status(bool reset) {

@@ -216,6 +216,13 @@ struct GemmArgs {
   int32_t K;
   int32_t ue8m0;         // power-of-two output scales
 };
+// tn 0: the tile kernel (256 x 256 tiles of CTA pairs); otherwise the stream
+// kernel with tn tokens a tile and K split `splits` ways over a cluster.
+struct GemmPlan {
+  int tn = 0;
+  int splits = 1;
+};
+GemmPlan plan_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms);
 cudaError_t launch_fp8_gemm(const GemmArgs &a, bool gated, int sms, cudaStream_t s);
 uint32_t read_gemm_status(bool reset);
 

@@ -45,6 +45,22 @@ __device__ __forceinline__ bool elect_lane() {
   return r != 0;
 }
 
+// The same for a CTA that issues its products alone.
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Asks for one box to be brought into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *m, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x), "r"(y)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -66,6 +82,16 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
 // cycles here.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Four fp32 values at a cluster address.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 // All threads of the cluster's CTAs.
@@ -114,17 +140,33 @@ __device__ __forceinline__ void copy_async_wait_all() {
 
 // A whole warp allocates (a power of two >= 32 columns); the base address
 // lands in shared memory.  The permit is given up: one allocation per CTA.
-// Both CTAs of a pair call it, and the release, together.
+// PAIR: both CTAs of a pair call it, and the release, together; a kernel uses
+// the pair's forms of all of these or of none.
+#define VG_GROUP_FORM(PAIR, text_alone, text_pair, ...) \
+  do {                                                  \
+    if constexpr (PAIR) {                               \
+      asm volatile(text_pair __VA_ARGS__);              \
+    } else {                                            \
+      asm volatile(text_alone __VA_ARGS__);             \
+    }                                                   \
+  } while (0)
+
+template <bool PAIR>
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
-               "r"(columns)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  VG_GROUP_FORM(PAIR, "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;",
+                "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;", ::"r"(smem_u32(slot)),
+                "r"(columns)
+                : "memory");
+  VG_GROUP_FORM(PAIR, "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;",
+                "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;", ::
+                    : "memory");
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns)
-               : "memory");
+  VG_GROUP_FORM(PAIR, "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;",
+                "tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;", ::"r"(base), "r"(columns)
+                : "memory");
 }
 
 __device__ __forceinline__ void tcgen05_fence_before() {
@@ -132,6 +174,19 @@ __device__ __forceinline__ void tcgen05_fence_before() {
 }
 __device__ __forceinline__ void tcgen05_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// 32 lanes x 16 columns of fp32 accumulators, with the wait for them.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
 }
 
 // 32 lanes x 32 columns of fp32 accumulators, a lane a row, asynchronously.
@@ -182,17 +237,21 @@ __host__ __device__ constexpr uint32_t product_desc(uint32_t m, uint32_t n) {
 }
 
 // D (tensor memory) = A B^T (+ D if accumulate) over K = 32, issued by one
-// thread of the pair's first CTA: rows 0..127 of A and D and the first half
-// of B's rows are the first CTA's, the others the second's, at the same
+// thread.  PAIR: of the pair's first CTA; rows 0..127 of A and D and the first
+// half of B's rows are the first CTA's, the others the second's, at the same
 // addresses of either.
+template <bool PAIR>
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                          bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
-      : "memory");
+  VG_GROUP_FORM(PAIR,
+                "{\n\t.reg .pred p;\n\t"
+                "setp.ne.b32 p, %4, 0;\n\t"
+                "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}",
+                "{\n\t.reg .pred p;\n\t"
+                "setp.ne.b32 p, %4, 0;\n\t"
+                "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}", ::"r"(d),
+                "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+                : "memory");
 }
 
 // Arrives on `bar` of both CTAs of the pair (or of this one alone) once this
@@ -204,10 +263,12 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-      : "memory");
+  VG_GROUP_FORM(PAIR, "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];",
+                "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];", ::"r"(
+                    smem_u32(bar))
+                : "memory");
 }
 
 // ------------------------------------------------------------ register split
