@@ -305,6 +305,7 @@ vg_status vg_fused_qk_norm_rope(uint16_t *qkv, const uint16_t *q_weight, const u
  *   q_weight, k_weight   both NULL: no norm, the rotation only (y = x)
  *   A position outside [0, max_position) on any axis leaves that token's
  *   heads unchanged and sets VG_DEVICE_BAD_POSITION.
+ *   max_position  >= 1, max_position * D <= INT32_MAX
  *   the other arguments as for vg_fused_qk_norm_rope
  */
 vg_status vg_fused_qk_norm_mrope(uint16_t *qkv, const uint16_t *q_weight, const uint16_t *k_weight,
@@ -345,7 +346,8 @@ vg_status vg_fused_qk_norm_mrope(uint16_t *qkv, const uint16_t *q_weight, const 
  *                  unspecified mix of its tokens (no other slot changes).
  *   k_scale, v_scale  in fp32 [1], device, > 0 and finite: FP8 caches; both
  *                  NULL: bf16 caches
- *   num_q_heads Hq >= 0, num_kv_heads Hkv >= 1; head_dim D in {64, 128, 256}
+ *   num_q_heads Hq >= 0, num_kv_heads Hkv >= 1; head_dim D in {64, 128, 256};
+ *                  max_position * D <= INT32_MAX
  *   num_pages, page_size  >= 1, num_pages * page_size <= INT32_MAX
  *   page_stride, token_stride, head_stride  in elements, multiples of 8, no
  *                  two places overlapping (a stride over an extent of one is

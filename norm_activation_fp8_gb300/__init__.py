@@ -361,11 +361,12 @@ def _arg(t, dtypes, name, dev, contiguous=True):
                      "torch.cuda.device(tensor.device)")
 
 
-def _here(stream):
-    """(current device, raw stream) of a call; without CUDA a device that no tensor is on."""
-    import torch
-    if not torch.cuda.is_available():
+def _here(t, stream):
+    """(current device, raw stream) of a call whose tensors should be where ``t`` is; for a CPU
+    tensor a device that no tensor is on."""
+    if t.get_device() < 0:
         return -2, 0
+    torch = _kinds()[4]
     dev = torch.cuda.current_device()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
@@ -379,8 +380,9 @@ def _shape(t, shape, name):
 
 @functools.cache
 def _kinds():
+    """(bf16, fp8, fp32, int64 dtypes, torch)"""
     import torch
-    return *_dtypes(), (torch.int64,)
+    return *_dtypes(), (torch.int64,), torch
 
 
 def _sections(sections, positions):
@@ -398,7 +400,7 @@ def _sections(sections, positions):
 def _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_q_heads,
                num_kv_heads, head_dim, dev):
     """Checked pointers and sizes that the multi-axis and cache forms share."""
-    bf16, _, f32, i64 = _kinds()
+    bf16, _, f32, i64, _ = _kinds()
     T, row = _rows(qkv, "qkv")
     max_pos, D = _rows(cos_sin_cache, "cos_sin_cache")
     sec, axes, tokens = _sections(sections, positions)
@@ -426,7 +428,7 @@ def vg_fused_qk_norm_mrope(qkv, q_weight, k_weight, cos_sin_cache, positions, se
     positions int64 [axes, T]; sections: how many of the D/2 pairs each axis
     turns (their sum is D/2), in runs or, ``interleaved``, taking turns.
     q_weight and k_weight [D] bf16, or both None: the rotation only."""
-    dev, raw = _here(stream)
+    dev, raw = _here(qkv, stream)
     q, qw, kw, table, pos, sec, axes, T, max_pos = _rope_args(
         qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_q_heads, num_kv_heads,
         head_dim, dev)
@@ -449,8 +451,8 @@ def vg_fused_qk_norm_rope_append(qkv, k_cache, v_cache, q_weight, k_weight, cos_
     page * page_size + place in the page, distinct; a negative slot appends
     nothing.  positions int64 [T], or [axes, T] with ``sections`` as for
     vg_fused_qk_norm_mrope."""
-    bf16, fp8, f32, i64 = _kinds()
-    dev, raw = _here(stream)
+    bf16, fp8, f32, i64, _ = _kinds()
+    dev, raw = _here(qkv, stream)
     q, qw, kw, table, pos, sec, axes, T, max_pos = _rope_args(
         qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_q_heads, num_kv_heads,
         head_dim, dev)
@@ -474,14 +476,17 @@ def vg_fused_qk_norm_rope_append(qkv, k_cache, v_cache, q_weight, k_weight, cos_
 
 def _block_gemm_args(a, a_scale, w, w_scale, a_options, dev):
     """Checked pointers and sizes of an FP8 product's operands."""
-    _, fp8, f32, _ = _kinds()
+    _, fp8, f32, _, _ = _kinds()
     T, K = _rows(a, "a")
     N, K2 = _rows(w, "w")
     if K2 != K:
         raise ValueError("a and w must have the same number of columns")
     kb = K // BLOCK
-    _shape(a_scale, (kb, (T + 3) // 4 * 4) if a_options & COLUMN_MAJOR else (T, kb), "a_scale")
-    _shape(w_scale, ((N + BLOCK - 1) // BLOCK, kb), "w_scale")
+    want = (kb, (T + 3) // 4 * 4) if a_options & COLUMN_MAJOR else (T, kb)
+    if a_scale.shape != want:
+        _shape(a_scale, want, "a_scale")
+    if w_scale.shape != ((N + BLOCK - 1) // BLOCK, kb):
+        _shape(w_scale, ((N + BLOCK - 1) // BLOCK, kb), "w_scale")
     return (_arg(a, fp8, "a", dev), _arg(a_scale, f32, "a_scale", dev), _arg(w, fp8, "w", dev),
             _arg(w_scale, f32, "w_scale", dev)), T, N, K
 
@@ -493,7 +498,7 @@ def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=No
     a [T,K] fp8 with a_scale fp32 [T,K/128] (or, with COLUMN_MAJOR in
     a_options, [K/128,T4] as the per-group ops write it); w [N,K] fp8 with
     w_scale fp32 [ceil(N/128),K/128].  UE8M0 scales need no option."""
-    dev, raw = _here(stream)
+    dev, raw = _here(a, stream)
     ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
     _shape(out, (T, N), "out")
     _check((_lib or load()).vg_fp8_block_gemm(_arg(out, _kinds()[0], "out", dev), *ptrs, T, N, K,
@@ -509,8 +514,8 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     rows [I,2I)) with w_scale [2I/128,K/128]; q [T,I] fp8, scale fp32
     [T,I/128], or with COLUMN_MAJOR in out_options [I/128,T4]; UE8M0 in
     out_options: power-of-two scales."""
-    _, fp8, f32, _ = _kinds()
-    dev, raw = _here(stream)
+    _, fp8, f32, _, _ = _kinds()
+    dev, raw = _here(a, stream)
     ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
     if N % 2:
         raise ValueError("w must have an even number of rows (gate, then up)")
@@ -631,8 +636,7 @@ def silu_mul_nvfp4(gate_up, global_scale, stream=None):
 
 def fp8_block_gemm(a, a_scale, w, w_scale, a_options: int = 0, stream=None):
     """Returns out bf16 [T,N]."""
-    import torch
-    out = torch.empty((a.shape[0], w.shape[0]), dtype=torch.bfloat16, device=a.device)
+    out = a.new_empty((a.shape[0], w.shape[0]), dtype=_kinds()[0][0])
     vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options, stream)
     return out
 
@@ -640,9 +644,9 @@ def fp8_block_gemm(a, a_scale, w, w_scale, a_options: int = 0, stream=None):
 def fp8_block_gemm_silu_mul_fp8(a, a_scale, w, w_scale, a_options: int = 0, out_options: int = 0,
                                 stream=None):
     """Returns (q float8_e4m3fn [T,I], scale)."""
-    import torch
     T, inter = a.shape[0], w.shape[0] // 2
-    q = torch.empty((T, inter), dtype=torch.float8_e4m3fn, device=a.device)
-    s = _scale_out(PER_GROUP | out_options, T, inter, BLOCK, None, a.device)
+    q = a.new_empty((T, inter), dtype=_kinds()[1][0])
+    s = a.new_empty((inter // BLOCK, (T + 3) // 4 * 4) if out_options & COLUMN_MAJOR
+                    else (T, inter // BLOCK), dtype=_kinds()[2][0])
     vg_fp8_block_gemm_silu_mul_fp8(q, s, a, a_scale, w, w_scale, a_options, out_options, stream)
     return q, s

@@ -461,6 +461,12 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
     sm.failed = 0;
   }
   if (warp == 1) tmem_alloc<false>(&sm.tmem, Smem::kColumns);
+  // Launched with programmatic dependent launch: nothing but L2 prefetches of
+  // the first weight stages before the previous grid has finished.
+  if (warp == 3 && lane < 2 * kStages && blockIdx.y == 0) {
+    const int kb = k0 + (lane >> 1);
+    if (kb < k1) tma_prefetch_2d(&maps.w, kb * kBlockK, lane & 1 ? r1 : r0);
+  }
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
@@ -759,20 +765,40 @@ cudaError_t launch_form(const GemmArgs &a, const GemmPlan &p, int sms, cudaStrea
 
 }  // namespace
 
+// Which kernel, and its split, by an estimate of either one's time, in
+// microseconds (measured on GB300 over T = 1..1024, N = 1024..57344, K =
+// 4096..28672):
+//   tile kernel    a wave of pairs: 3 + 0.52 per scale block of K
+//   stream kernel  a wave of CTAs: 3.5, and 0.27 (16 tokens) .. 0.48 (128) per
+//                  block of its split or the weight's bytes at 6 TB/s (a second
+//                  token tile reads it from L2, at about three times that),
+//                  whichever is longer, with a fifth of the other
+// A wave of stream CTAs is taken as 85 % of the slots: clusters do not fill
+// every SM, and a second wave costs as much as the first (6144 x 4096, one
+// token: five ways, 240 CTAs, 6.5 us; six ways, 288 of 304 slots, 10.3 us).
+// Splits are powers of two: others pack worse (64 x 4096 x 4096: four ways
+// 7.5 us, five 9.4).
 GemmPlan plan_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
   GemmPlan p;
-  const int64_t rows = (N + kHalfW - 1) / kHalfW;  // weight tiles of the stream kernel
-  const int64_t pairs = (T + 2 * kTileT - 1) / (2 * kTileT) * (gated ? N / kHalfW : (N + kTileW - 1) / kTileW);
-  if (T > 128 && 2 * pairs >= sms / 2) return p;  // tn 0: the tile kernel
-  p.tn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
-  const int64_t slots = (int64_t)sms * (p.tn <= 64 ? 2 : 1), blocks = K / kBlockK;
-  const int64_t tiles = rows * ((T + p.tn - 1) / p.tn) * (gated ? 2 : 1);
-  int64_t best = INT64_MAX;
-  for (int s = 1; s <= (gated ? kMaxSplit / 2 : kMaxSplit) && s <= blocks; ++s) {
-    // waves times the longest split, with six blocks' time for a CTA's start and end
-    const int64_t cost = (tiles * s + slots - 1) / slots * ((blocks + s - 1) / s + 6);
+  const int64_t blocks = K / kBlockK, rows = (N + kHalfW - 1) / kHalfW * (gated ? 2 : 1);
+  const int64_t pairs =
+      (T + 2 * kTileT - 1) / (2 * kTileT) * (gated ? N / kHalfW : (N + kTileW - 1) / kTileW);
+  const int64_t pair_slots = sms < 2 ? 1 : sms / 2;
+  double best = (double)((pairs + pair_slots - 1) / pair_slots) * (3.0 + 0.52 * (double)blocks);
+  const int tn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
+  const int64_t token_tiles = (T + tn - 1) / tn, tiles = rows * token_tiles;
+  if (token_tiles > 65535) return p;
+  const int64_t slots = (int64_t)sms * (tn <= 64 ? 2 : 1), wave = slots < 8 ? slots : slots * 85 / 100;
+  const double per_block = tn <= 32 ? 0.27 : (tn == 64 ? 0.36 : 0.48);
+  const double bytes = (double)rows * kHalfW * (double)K * (1.0 + (double)(token_tiles - 1) / 3.0);
+  for (int s = 1; s <= (gated ? kMaxSplit / 2 : kMaxSplit) && s <= blocks; s *= 2) {
+    const double waves = (double)((tiles * s + wave - 1) / wave);
+    const double chain = (double)((blocks + s - 1) / s) * per_block;
+    const double traffic = bytes / waves / 6.0e6;  // 6.0 TB/s
+    const double cost = waves * (3.5 + (chain > traffic ? chain + 0.2 * traffic : traffic + 0.2 * chain));
     if (cost < best) {
       best = cost;
+      p.tn = tn;
       p.splits = s;
     }
   }

@@ -24,9 +24,10 @@
 // where the exact value lies that close to a bf16 midpoint, by one ulp.
 //
 // Two further forms of the same kernel.  AXES: pair i turns by the position
-// on its axis, positions[axis(i), t]; the token's cos/sin row is put together
-// once per CTA in shared memory (every head of the token reads it), and the
-// heads read it from there.  APPEND: Q in place, K (normed, rotated) and V go
+// on its axis, positions[axis(i), t]; each lane takes its pairs' values from
+// the rows of their axes (measured against a row put together in shared
+// memory once per CTA: its barrier couples the warps, 16411 tokens of 32 + 8
+// heads 84 us).  APPEND: Q in place, K (normed, rotated) and V go
 // to their slot of a paged cache instead, as bf16 or as e4m3(value / scale)
 // from the fp32 value, so that the qkv row is read once and K and V are
 // written once.  A rotation without a norm takes weights of one and y = 1.
@@ -42,27 +43,9 @@ __device__ uint32_t g_rope_status;
 
 namespace {
 
-__device__ __forceinline__ void load8f(const float *p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
 __device__ __forceinline__ void load4f(const float *p, float (&v)[8], int at) {
   const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
   v[at] = a.x; v[at + 1] = a.y; v[at + 2] = a.z; v[at + 3] = a.w;
-}
-
-// The same from shared memory (the multi-axis row).
-__device__ __forceinline__ void lds4f(const float *p, float (&v)[8], int at) {
-  const float4 a = *reinterpret_cast<const float4 *>(p);
-  v[at] = a.x; v[at + 1] = a.y; v[at + 2] = a.z; v[at + 3] = a.w;
-}
-
-__device__ __forceinline__ void lds8f(const float *p, float (&v)[8]) {
-  lds4f(p, v, 0);
-  lds4f(p + 4, v, 4);
 }
 
 // Two elements of a*c -/+ b*s (Kahan), packed; a zero keeps the plain
@@ -109,203 +92,237 @@ __device__ __forceinline__ int64_t cache_place(const QkArgs &a, int64_t slot, in
 }
 
 // One head's two chunks of 8 (columns 8l and 8(l + G)) to its slot of a paged
-// cache: plain stores, so that L2 keeps the line for the attention that
-// reads it next.
+// cache.  MANY: streaming stores (a long prompt's K and V pass L2 by; measured
+// 122 -> 119 us, FP8 56 -> 52); few tokens' lines stay in L2 for the attention
+// that reads them next.
+template <bool MANY, class V>
+__device__ __forceinline__ void cache_put(const QkArgs &a, void *cache, void *o, const V &v) {
+  if (!VG_ACCESS_OK(g_rope_status, o, sizeof(V), cache, sizeof(V) / 8 * a.cache_elems)) return;
+  if constexpr (MANY)
+    st_stream(o, v);
+  else
+    *static_cast<V *>(o) = v;
+}
+
+template <bool MANY>
 __device__ __forceinline__ void cache_store(const QkArgs &a, void *cache, int64_t at, int l, int g,
                                             const uint4 &ca, const uint4 &cb) {
   uint16_t *o = static_cast<uint16_t *>(cache) + at;
-  if (VG_ACCESS_OK(g_rope_status, o + 8 * l, 16, cache, 2ull * a.cache_elems))
-    *reinterpret_cast<uint4 *>(o + 8 * l) = ca;
-  if (VG_ACCESS_OK(g_rope_status, o + 8 * (l + g), 16, cache, 2ull * a.cache_elems))
-    *reinterpret_cast<uint4 *>(o + 8 * (l + g)) = cb;
+  cache_put<MANY>(a, cache, o + 8 * l, ca);
+  cache_put<MANY>(a, cache, o + 8 * (l + g), cb);
 }
 
+template <bool MANY>
 __device__ __forceinline__ void cache_store(const QkArgs &a, void *cache, int64_t at, int l, int g,
                                             const uint2 &ca, const uint2 &cb) {
   uint8_t *o = static_cast<uint8_t *>(cache) + at;
-  if (VG_ACCESS_OK(g_rope_status, o + 8 * l, 8, cache, a.cache_elems))
-    *reinterpret_cast<uint2 *>(o + 8 * l) = ca;
-  if (VG_ACCESS_OK(g_rope_status, o + 8 * (l + g), 8, cache, a.cache_elems))
-    *reinterpret_cast<uint2 *>(o + 8 * (l + g)) = cb;
+  cache_put<MANY>(a, cache, o + 8 * l, ca);
+  cache_put<MANY>(a, cache, o + 8 * (l + g), cb);
 }
 
-template <int G, bool NEOX, bool AXES, bool APPEND>
-__global__ void __launch_bounds__(512, 3) qk_norm_rope_kernel(const QkArgs a) {
-  constexpr int D = G * 16;
+// H: heads that a lane group takes, one after the other; their loads go out
+// together and they share the token's position, slot and cos/sin values.  The
+// plain form takes one.  The two further forms, whose per-token work is larger,
+// take one for few tokens (the shortest chain: a token 1.8 us against 2.5) and
+// three for many (16411 tokens of 32 + 8 heads with three axes: 80, 57, 55, 55
+// us with one to four; 32768 tokens into a bf16 cache: 171, 140, 122, 124 us,
+// the copy rate; 8191 tokens of 64 + 8 heads into an FP8 cache: 66, 59, 56, 54).
+constexpr int kManyHeads = 3;
+
+template <int G, bool NEOX, bool AXES, bool APPEND, int H>
+__global__ void __launch_bounds__(512, AXES || APPEND ? 2 : 3) qk_norm_rope_kernel(const QkArgs a) {
+  constexpr int D = G * 16, kPerWarp = 32 / G;
+  constexpr bool kPlain = !AXES && !APPEND;  // every head has a norm
   const int lane = threadIdx.x & 31;
   const int l = lane & (G - 1);
   const int64_t t = blockIdx.x;
-  const int h = ((int)blockIdx.y * (int)(blockDim.x >> 5) + (int)(threadIdx.x >> 5)) * (32 / G) + lane / G;
+  // the warp's first head; a lane group's heads: h0 + lane / G + k * kPerWarp
+  const int h0 = ((int)blockIdx.y * (int)(blockDim.x >> 5) + (int)(threadIdx.x >> 5)) * kPerWarp * H;
   // Launched with programmatic dependent launch: nothing in global memory
   // before the previous grid has finished, except that the CTA's heads are
   // asked into L2 first; the next grid may be scheduled once the loads are out.
   if (threadIdx.x == 0 && (int)blockIdx.x < a.pf_ctas) {
-    const int h0 = (int)blockIdx.y * (int)(blockDim.x >> 5) * (32 / G);
-    const int nh = a.nh - h0 < (int)(blockDim.x >> 5) * (32 / G) ? a.nh - h0 : (int)(blockDim.x >> 5) * (32 / G);
+    const int most = (int)(blockDim.x >> 5) * kPerWarp * H;
+    const int nh = a.nh - h0 < most ? a.nh - h0 : most;
     prefetch_l2(a.qkv + t * a.row + (int64_t)h0 * D, 2u * (uint32_t)(nh * D));
   }
   pdl_wait();
-  [[maybe_unused]] __shared__ __align__(16) float row_cs[AXES ? D : 4];
-  bool pos_ok = true;
-  // The head's loads do not depend on the token's position, so they go out
+  // The heads' loads do not depend on the token's position, so they go out
   // together with it (a head with a bad position is loaded but not stored);
   // only the cos/sin row waits for the position.
-  const bool in_head = h < a.nh;
-  uint16_t *head = a.qkv + t * a.row + (in_head ? (int64_t)h * D : 0);
-  const uint16_t *w = h < a.hq ? a.qw : a.kw;
-  const bool norm = (!AXES && !APPEND) || (w != nullptr && h < a.hqk);
+  uint16_t *token = a.qkv + t * a.row;
   const int64_t pos = AXES ? 0 : a.pos[t];
   const int64_t slot = APPEND ? a.slots[t] : 0;
   // chunk 0 of the lane: l (first half of the head), chunk 1: l + G
-  const uint4 xa = in_head ? ld_stream(head + l * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
-  const uint4 xb = in_head ? ld_stream(head + (l + G) * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
-  constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones: a rotation without a norm
-  const uint4 ones = make_uint4(kOnes, kOnes, kOnes, kOnes);
-  const uint4 wa = in_head && norm ? ld_keep(w + l * kElemsPerChunk) : ones;
-  const uint4 wb = in_head && norm ? ld_keep(w + (l + G) * kElemsPerChunk) : ones;
+  uint4 xa[H], xb[H], wa[H], wb[H];
+#pragma unroll
+  for (int k = 0; k < H; ++k) {
+    const int h = h0 + lane / G + k * kPerWarp;
+    const bool in_head = h < a.nh;
+    const uint16_t *head = token + (in_head ? (int64_t)h * D : 0);
+    xa[k] = in_head ? ld_stream(head + l * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
+    xb[k] = in_head ? ld_stream(head + (l + G) * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
+    if constexpr (kPlain) {
+      const uint16_t *w = h < a.hq ? a.qw : a.kw;
+      wa[k] = in_head ? ld_keep(w + l * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
+      wb[k] = in_head ? ld_keep(w + (l + G) * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  bool pos_ok = true;                       // the same for the whole CTA
+  [[maybe_unused]] uint32_t at[4] = {};     // first element of each axis's table row
   if constexpr (AXES) {
-    // the axes' positions, then this token's cos/sin row, pair by pair (after
-    // the heads' loads, which do not wait for them)
-    int64_t p4[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      p4[x] = x < a.axes ? a.pos[x * a.T + t] : 0;
-      pos_ok = pos_ok && p4[x] >= 0 && p4[x] < a.max_pos;
+      const int64_t p = x < a.axes ? a.pos[x * a.T + t] : 0;
+      pos_ok = pos_ok && p >= 0 && p < a.max_pos;
+      at[x] = (uint32_t)p * (uint32_t)D;  // max_pos * D fits 32 bits
     }
-    if (pos_ok)
-      for (int i = (int)threadIdx.x; i < D; i += (int)blockDim.x) {
-        const int pair = i & (D / 2 - 1);
-        const int x = (int)(a.axis_map[pair >> 4] >> (2 * (pair & 15))) & 3;
-        const int64_t p = x == 0 ? p4[0] : (x == 1 ? p4[1] : (x == 2 ? p4[2] : p4[3]));
-        row_cs[i] = __ldg(a.cache + p * D + i);
-      }
+  } else {
+    pos_ok = pos >= 0 && pos < a.max_pos;
   }
-  if constexpr (!AXES) pos_ok = pos >= 0 && pos < a.max_pos;
-  const bool live = in_head && pos_ok;  // same for the head's lanes
-  if (in_head && !live && l == 0) atomicOr(&g_rope_status, kErrBadPosition);
+  if (!pos_ok && h0 + lane / G < a.nh && l == 0) atomicOr(&g_rope_status, kErrBadPosition);
   pdl_launch_dependents();
-  if constexpr (AXES) __syncthreads();  // row_cs is complete
-  if constexpr (APPEND) {
-    // V heads go to the cache as they are; a warp of V heads is then done
-    if (live && h >= a.hqk) {
-      const int64_t at = cache_place(a, slot, h - a.hqk, l == 0);
-      if (at >= 0 && a.v_scale == nullptr) {
-        cache_store(a, a.v_cache, at, l, G, xa, xb);
-      } else if (at >= 0) {
-        const float m = __frcp_rn(__ldg(a.v_scale));
-        cache_store(a, a.v_cache, at, l, G, scaled_codes(xa, m), scaled_codes(xb, m));
-      }
-    }
-    if (h - lane / G >= a.hqk) return;
-  }
-  float2 ta[4], tb[4];
-  float cmax;
-  RowAcc acc;
-  pass1_chunk<false, false>(xa, xa, wa, ta, cmax, acc);
-  pass1_chunk<false, false>(xb, xb, wb, tb, cmax, acc);
-  float ss = acc.ss.x + acc.ss.y;
-#pragma unroll
-  for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-  const float y = norm ? rsqrtf(fmaf(ss, 1.0f / (float)D, a.eps)) : 1.0f;
 
-  // mine[0..7]: chunk 0, mine[8..15]: chunk 1; other: each element's pair
-  // partner; c, s: its pair's cos and sin; submask bit k: minus sign
-  float mine[16], other[16], c[16], s[16];
+  // cos and sin of the lane's pairs: neox 8l .. 8l + 7 (element k of chunk 0
+  // with element k of chunk 1), gptj 4l .. 4l + 3 and 4(l + G) .. + 3 (inside
+  // either chunk)
+  float cv[8] = {}, sv[8] = {};
+  if (pos_ok && h0 + lane / G < a.nh) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    mine[2 * i] = ta[i].x;
-    mine[2 * i + 1] = ta[i].y;
-    mine[8 + 2 * i] = tb[i].x;
-    mine[8 + 2 * i + 1] = tb[i].y;
-  }
-  const float *cs = AXES ? row_cs : a.cache + (live ? pos * D : 0);
-  const auto ld8 = [](const float *p, float(&v)[8]) {
-    if constexpr (AXES) lds8f(p, v); else load8f(p, v);
-  };
-  const auto ld4 = [](const float *p, float(&v)[8], int at) {
-    if constexpr (AXES) lds4f(p, v, at); else load4f(p, v, at);
-  };
-  uint32_t submask;
-  if (NEOX) {  // element k of chunk 0 pairs with element k of chunk 1: pair 8l + k
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      other[k] = mine[8 + k];
-      other[8 + k] = mine[k];
-    }
-    float c8[8] = {}, s8[8] = {};
-    if (live) {
-      ld8(cs + 8 * l, c8);
-      ld8(cs + D / 2 + 8 * l, s8);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      c[k] = c[8 + k] = c8[k];
-      s[k] = s[8 + k] = s8[k];
-    }
-    submask = 0x00FFu;
-  } else {  // pairs (2i, 2i + 1) inside each chunk: pair 4 chunk + k / 2
-#pragma unroll
-    for (int k = 0; k < 16; ++k) other[k] = mine[k ^ 1];
-    float c4[8] = {}, s4[8] = {};
-    if (live) {
-      ld4(cs + 4 * l, c4, 0);
-      ld4(cs + 4 * (l + G), c4, 4);
-      ld4(cs + D / 2 + 4 * l, s4, 0);
-      ld4(cs + D / 2 + 4 * (l + G), s4, 4);
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      c[k] = c4[k >> 1];
-      s[k] = s4[k >> 1];
-    }
-    submask = 0x5555u;
-  }
-
-  float p[16];
-#pragma unroll
-  for (int k = 0; k < 16; k += 2) {
-    const bool m0 = (submask >> k) & 1u, m1 = (submask >> (k + 1)) & 1u;
-    const float2 o = kahan2x(make_float2(mine[k], mine[k + 1]), make_float2(c[k], c[k + 1]),
-                             make_float2(m0 ? -other[k] : other[k], m1 ? -other[k + 1] : other[k + 1]),
-                             make_float2(s[k], s[k + 1]));
-    const float2 pp = f2_mul(o, make_float2(y, y));
-    p[k] = pp.x;
-    p[k + 1] = pp.y;
-  }
-  if constexpr (APPEND) {
-    if (h >= a.hq) {  // a K head goes to its slot (a V head is already there)
-      if (!live || h >= a.hqk) return;
-      const int64_t at = cache_place(a, slot, h - a.hq, l == 0);
-      if (at < 0) return;
-      if (a.k_scale != nullptr) {
-        const float m = __frcp_rn(__ldg(a.k_scale));
-#pragma unroll
-        for (int k = 0; k < 16; ++k) p[k] *= m;
-        cache_store(a, a.k_cache, at, l, G, codes8(p), codes8(p + 8));
+    for (int i = 0; i < 8; i += 4) {
+      const int p0 = NEOX ? 8 * l + i : 4 * (i ? l + G : l);
+      if constexpr (!AXES) {
+        load4f(a.cache + pos * D + p0, cv, i);
+        load4f(a.cache + pos * D + D / 2 + p0, sv, i);
       } else {
-        cache_store(a, a.k_cache, at, l, G, bf16x8(p), bf16x8(p + 8));
+        // from one row, or from the row of each pair's axis (one wide load
+        // where all four share it)
+        const auto row = [&](uint32_t x) { return x < 2 ? (x == 0 ? at[0] : at[1]) : (x == 2 ? at[2] : at[3]); };
+        const uint32_t m = (a.axis_map[p0 >> 4] >> (2 * (p0 & 15))) & 0xFFu;
+        if (m == (m & 3u) * 0x55u) {
+          const float *r = a.cache + row(m & 3u) + p0;
+          load4f(r, cv, i);
+          load4f(r + D / 2, sv, i);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float *r = a.cache + row((m >> (2 * k)) & 3u) + p0 + k;
+            cv[i + k] = __ldg(r);
+            sv[i + k] = __ldg(r + D / 2);
+          }
+        }
       }
-      return;
     }
   }
-  [[maybe_unused]] const uint64_t bytes = VG_ROWS(a.T) * 2ull * (uint64_t)a.row;
-  if (live && VG_ACCESS_OK(g_rope_status, head + l * kElemsPerChunk, 16, a.qkv, bytes))
-    st_stream(head + l * kElemsPerChunk, bf16x8(p));
-  if (live && VG_ACCESS_OK(g_rope_status, head + (l + G) * kElemsPerChunk, 16, a.qkv, bytes))
-    st_stream(head + (l + G) * kElemsPerChunk, bf16x8(p + 8));
+
+#pragma unroll
+  for (int k = 0; k < H; ++k) {
+    const int first = h0 + k * kPerWarp, h = first + lane / G;
+    const bool live = h < a.nh && pos_ok;  // same for the head's lanes
+    if constexpr (APPEND) {
+      // V heads go to the cache as they are, and need no more
+      if (live && h >= a.hqk) {
+        const int64_t place = cache_place(a, slot, h - a.hqk, l == 0);
+        if (place >= 0 && a.v_scale == nullptr) {
+          cache_store<(H > 1)>(a, a.v_cache, place, l, G, xa[k], xb[k]);
+        } else if (place >= 0) {
+          const float m = __frcp_rn(__ldg(a.v_scale));
+          cache_store<(H > 1)>(a, a.v_cache, place, l, G, scaled_codes(xa[k], m), scaled_codes(xb[k], m));
+        }
+      }
+    }
+    if (!kPlain && first >= (APPEND ? a.hqk : a.nh)) continue;  // the whole warp
+    bool norm = true;
+    if constexpr (!kPlain) {
+      const uint16_t *w = h < a.hq ? a.qw : a.kw;
+      norm = w != nullptr && h < a.hqk;
+      constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones: a rotation without a norm
+      const uint4 ones = make_uint4(kOnes, kOnes, kOnes, kOnes);
+      wa[k] = norm ? ld_keep(w + l * kElemsPerChunk) : ones;
+      wb[k] = norm ? ld_keep(w + (l + G) * kElemsPerChunk) : ones;
+    }
+    float2 ta[4], tb[4];
+    float cmax;
+    RowAcc acc;
+    pass1_chunk<false, false>(xa[k], xa[k], wa[k], ta, cmax, acc);
+    pass1_chunk<false, false>(xb[k], xb[k], wb[k], tb, cmax, acc);
+    float ss = acc.ss.x + acc.ss.y;
+#pragma unroll
+    for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    const float y = norm ? rsqrtf(fmaf(ss, 1.0f / (float)D, a.eps)) : 1.0f;
+
+    // mine[0..7]: chunk 0, mine[8..15]: chunk 1; other: each element's pair
+    // partner; c, s: its pair's cos and sin; submask bit i: minus sign
+    float mine[16], other[16], c[16], s[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mine[2 * i] = ta[i].x;
+      mine[2 * i + 1] = ta[i].y;
+      mine[8 + 2 * i] = tb[i].x;
+      mine[8 + 2 * i + 1] = tb[i].y;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      other[i] = mine[NEOX ? i ^ 8 : i ^ 1];
+      c[i] = cv[NEOX ? i & 7 : i >> 1];
+      s[i] = sv[NEOX ? i & 7 : i >> 1];
+    }
+    constexpr uint32_t submask = NEOX ? 0x00FFu : 0x5555u;
+
+    float p[16];
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const bool m0 = (submask >> i) & 1u, m1 = (submask >> (i + 1)) & 1u;
+      const float2 o = kahan2x(make_float2(mine[i], mine[i + 1]), make_float2(c[i], c[i + 1]),
+                               make_float2(m0 ? -other[i] : other[i], m1 ? -other[i + 1] : other[i + 1]),
+                               make_float2(s[i], s[i + 1]));
+      const float2 pp = f2_mul(o, make_float2(y, y));
+      p[i] = pp.x;
+      p[i + 1] = pp.y;
+    }
+    if (!live) continue;
+    if constexpr (APPEND) {
+      if (h >= a.hq) {  // a K head goes to its slot (a V head is already there)
+        const int64_t place = h < a.hqk ? cache_place(a, slot, h - a.hq, l == 0) : -1;
+        if (place < 0) continue;
+        if (a.k_scale != nullptr) {
+          const float m = __frcp_rn(__ldg(a.k_scale));
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] *= m;
+          cache_store<(H > 1)>(a, a.k_cache, place, l, G, codes8(p), codes8(p + 8));
+        } else {
+          cache_store<(H > 1)>(a, a.k_cache, place, l, G, bf16x8(p), bf16x8(p + 8));
+        }
+        continue;
+      }
+    }
+    uint16_t *head = token + (int64_t)h * D;
+    [[maybe_unused]] const uint64_t bytes = VG_ROWS(a.T) * 2ull * (uint64_t)a.row;
+    if (VG_ACCESS_OK(g_rope_status, head + l * kElemsPerChunk, 16, a.qkv, bytes))
+      st_stream(head + l * kElemsPerChunk, bf16x8(p));
+    if (VG_ACCESS_OK(g_rope_status, head + (l + G) * kElemsPerChunk, 16, a.qkv, bytes))
+      st_stream(head + (l + G) * kElemsPerChunk, bf16x8(p + 8));
+  }
 }
 
 // One token per CTA: up to 16 warps of heads; blockIdx.y covers the rest.
-template <int G, bool AXES, bool APPEND>
-cudaError_t launch_form(const QkArgs &a, bool neox, cudaStream_t s) {
-  const int heads_per_warp = 32 / G;
+template <int G, bool AXES, bool APPEND, int H>
+cudaError_t launch_heads(const QkArgs &a, bool neox, cudaStream_t s) {
+  constexpr int heads_per_warp = 32 / G * H;
   // up to 16 warps a CTA; more of them are dealt out evenly
   const int all = (a.nh + heads_per_warp - 1) / heads_per_warp;
   const int parts = (all + 15) / 16;
   const int warps = (all + parts - 1) / parts;
   const dim3 grid((unsigned)a.T, (unsigned)((a.nh + warps * heads_per_warp - 1) / (warps * heads_per_warp)));
-  return neox ? launch_pdl(qk_norm_rope_kernel<G, true, AXES, APPEND>, grid, dim3(warps * 32), 0, s, a)
-              : launch_pdl(qk_norm_rope_kernel<G, false, AXES, APPEND>, grid, dim3(warps * 32), 0, s, a);
+  return neox ? launch_pdl(qk_norm_rope_kernel<G, true, AXES, APPEND, H>, grid, dim3(warps * 32), 0, s, a)
+              : launch_pdl(qk_norm_rope_kernel<G, false, AXES, APPEND, H>, grid, dim3(warps * 32), 0, s, a);
+}
+
+// Many tokens: from four per SM on (pf_ctas is two per SM).
+template <int G, bool AXES, bool APPEND>
+cudaError_t launch_form(const QkArgs &a, bool neox, cudaStream_t s) {
+  if (a.T >= 2LL * a.pf_ctas) return launch_heads<G, AXES, APPEND, kManyHeads>(a, neox, s);
+  return launch_heads<G, AXES, APPEND, 1>(a, neox, s);
 }
 
 template <int G>
@@ -316,7 +333,7 @@ cudaError_t launch_g(const QkArgs &a, bool neox, cudaStream_t s) {
   // form turns by its one axis
   const bool weights = (a.hq == 0 || a.qw) && (a.hqk == a.hq || a.kw);
   return a.axes > 1 || !weights ? launch_form<G, true, false>(a, neox, s)
-                                : launch_form<G, false, false>(a, neox, s);
+                                : launch_heads<G, false, false, 1>(a, neox, s);
 }
 
 }  // namespace

@@ -347,6 +347,7 @@ vg_status set_axes(QkArgs &a, const int32_t *sections, int32_t axes, int32_t D, 
   if (axes < 1 || axes > 4 || (axes > 1 && !sections)) return VG_ERR_BAD_SHAPE;
   const int half = D / 2;
   a.axes = axes;
+  if (a.max_pos > INT32_MAX / D) return VG_ERR_BAD_SHAPE;  // 32-bit table offsets
   if (!sections) return VG_OK;
   int64_t sum = 0;
   for (int x = 0; x < axes; ++x) {

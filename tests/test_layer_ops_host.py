@@ -83,6 +83,7 @@ def test_mrope_refusals(lib):
     assert mrope(lib, hq=0, hkv=0) == SHAPE
     assert mrope(lib, hq=4000, hkv=100) == SHAPE
     assert mrope(lib, maxp=0) == SHAPE
+    assert mrope(lib, maxp=2 ** 31 // 128) == SHAPE           # table offsets past 31 bits
     assert mrope(lib, T=-1) == SHAPE
     for axes, sec in ((0, ()), (5, (24, 10, 10, 10, 10)), (3, None), (3, (24, 20, 19)),
                       (3, (65, 0, -1)), (2, (70, -6)), (1, (63,))):
