@@ -87,7 +87,8 @@ __device__ __forceinline__ float group_scale(float amax, bool ue8m0) {
 // ------------------------------------------------------------- tile kernel
 
 constexpr int kTileT = 128, kTileW = 256, kHalfW = 128;
-constexpr int kTileStages = 5, kScaleSlots = 8;
+constexpr int kTileStages = 5;
+constexpr int kScaleSlots = 8;  // scale blocks staged ahead (stream kernel); a group of the tile kernel's two
 constexpr int kTileStageBytes = (kTileT + kHalfW) * kBlockK;  // of either CTA
 constexpr int kSumWarps = 16, kTileThreads = 128 + 32 * kSumWarps;
 constexpr int kPart = kHalfW * 4 / kSumWarps;  // columns of either half that a thread sums
@@ -99,11 +100,11 @@ template <bool GATED>
 struct TileSmem {
   uint8_t stage[kTileStages][kTileStageBytes];
   uint8_t out[kSumWarps][32 * kPart * (GATED ? 1 : 2)];  // a box of 32 rows
-  float sa[kScaleSlots][kTileT];
-  float sw[kScaleSlots][2];
+  float sa[2][kScaleSlots][kTileT];
+  float sw[2][kScaleSlots][2];
   float amax[GATED ? 2 : 1][GATED ? kSumWarps / 4 : 1][GATED ? kTileT : 1];
   uint64_t full[kTileStages], empty[kTileStages];
-  uint64_t acc_full[2], acc_empty[2], scale_full[kScaleSlots], scale_empty[kScaleSlots], drain;
+  uint64_t acc_full[2], acc_empty[2], scale_full[2], scale_empty[2], drain;
   uint32_t tmem;
   uint32_t failed;
 };
@@ -154,8 +155,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.acc_full[i], 1);
       mbar_init(&sm.acc_empty[i], 2 * kSumWarps);  // of both CTAs (the first CTA's counts)
-    }
-    for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(&sm.scale_full[i], 32);
       mbar_init(&sm.scale_empty[i], kSumWarps);
     }
@@ -235,27 +234,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       (void)mbar_wait_bounded(&sm.drain, 0);
     } else if (warp == 2) {
-      // Scales go straight to shared memory, eight blocks ahead (measured with
-      // two blocks of them prefetched in registers: their L2 latency, not the
-      // products, set the pace, 1980 instead of 2800 TFLOP/s).
-      uint32_t it = 0, s = 0, lap = 0;
+      // Scales go straight to shared memory, in groups of eight blocks of a
+      // tile (measured with two blocks prefetched in registers: their L2
+      // latency, not the products, set the pace, 1980 instead of 2800 TFLOP/s;
+      // a group takes one wait and one release of the summing warps, not
+      // eight).
+      uint32_t g = 0;  // groups so far
       bool ok = true;
       for (uint32_t i = first; i < tiles && ok; i += pairs) {
         const Tile t = tile_at(i, num_t, num_n);
         const int r = half_row<GATED>(a, t.n, lane & 1), row = t.t0 + my_t + lane;
         const bool w_live = r < (GATED ? 2 : 1) * a.N;
         const float *pw = a.w_scale + (w_live ? (int64_t)(r / kBlockK) * num_k : 0);
-        for (int kb = 0; kb < num_k; ++kb, ++it) {
-          if (lap > 0 && !(ok = warp_wait_phase(&sm.scale_empty[s], (lap - 1) & 1, &sm.failed))) break;
+        for (int kb = 0; kb < num_k; kb += kScaleSlots, ++g) {
+          if (g >= 2 && !(ok = warp_wait_phase(&sm.scale_empty[g & 1], (g / 2 - 1) & 1, &sm.failed))) break;
+          const int n = min(kScaleSlots, num_k - kb);
+          for (int x = 0; x < n; ++x) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bool live = row + 32 * j < a.T;
-            copy_async4(&sm.sa[s][lane + 32 * j],
-                        a.a_scale + (live ? (row + 32 * j) * a.a_ts + kb * a.a_bs : 0), live);
+            for (int j = 0; j < 4; ++j) {
+              const bool live = row + 32 * j < a.T;
+              copy_async4(&sm.sa[g & 1][x][lane + 32 * j],
+                          a.a_scale + (live ? (row + 32 * j) * a.a_ts + (kb + x) * a.a_bs : 0), live);
+            }
+            if (lane < 2) copy_async4(&sm.sw[g & 1][x][lane], pw + (w_live ? kb + x : 0), w_live);
           }
-          if (lane < 2) copy_async4(&sm.sw[s][lane], pw + (w_live ? kb : 0), w_live);
-          copy_async_arrive(&sm.scale_full[s]);
-          if (++s == kScaleSlots) s = 0, ++lap;
+          copy_async_arrive(&sm.scale_full[g & 1]);
         }
       }
       copy_async_wait_all();
@@ -265,7 +268,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int quarter = warp & 3, part = (warp - 4) >> 2;  // lanes, columns of each half
     const int row = quarter * 32 + lane;
     uint8_t *box = sm.out[warp - 4];
-    uint32_t it = 0;
+    const uint32_t release = cluster_addr(&sm.acc_empty[0], 0);
+    uint32_t it = 0, g = 0;
     int turn = 0;
     bool ok = true;
     for (uint32_t i = first; i < tiles; i += pairs, turn ^= 1) {
@@ -275,29 +279,30 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int j = 0; j < kPart / 2; ++j) acc[h][j] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < num_k; ++kb, ++it) {
-        const uint32_t b = it & 1, ss = it % kScaleSlots;
-        const bool odd = lane & 1;  // half of the lanes wait for either barrier
-        if (!(ok = warp_wait_phase(odd ? &sm.scale_full[ss] : &sm.acc_full[b],
-                                   (odd ? it / kScaleSlots : it / 2) & 1, &sm.failed)))
-          break;
+        const uint32_t b = it & 1, x = (uint32_t)kb % kScaleSlots;
+        if (x == 0 && !(ok = warp_wait_phase(&sm.scale_full[g & 1], (g >> 1) & 1, &sm.failed))) break;
+        const float s = sm.sa[g & 1][x][row];
+        const float2 w = *reinterpret_cast<const float2 *>(sm.sw[g & 1][x]);
+        if (x == kScaleSlots - 1 || kb == num_k - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.scale_empty[g & 1]);
+          ++g;
+        }
+        if (!(ok = warp_wait_phase(&sm.acc_full[b], (it >> 1) & 1, &sm.failed))) break;
         tcgen05_fence_after();
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * kTileW + part * kPart;
         uint32_t v[kPart];
         tmem_load32(base, v);
-        const float s = sm.sa[ss][row];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h > 0) tmem_load32(base + kHalfW, v);
-          const float sh = s * sm.sw[ss][h];
+          const float sh = s * (h ? w.y : w.x);
           const float2 sc = make_float2(sh, sh);
           tmem_load_wait(v);
           if (h > 0) {  // all read: the products of the block after next may start
             tcgen05_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_cluster(cluster_addr(&sm.acc_empty[b], 0));
-              mbar_arrive(&sm.scale_empty[ss]);
-            }
+            if (lane == 0) mbar_arrive_cluster(release + 8 * b);
           }
 #pragma unroll
           for (int j = 0; j < kPart / 2; ++j)
