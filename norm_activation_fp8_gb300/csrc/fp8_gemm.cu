@@ -39,6 +39,7 @@ __device__ uint32_t g_gemm_status;
 namespace {
 
 constexpr int kBlockK = 128;  // codes of K per scale block (and per stage)
+constexpr int kHalfW = 128;   // weight rows of a tile's half (tile kernel), of a tile (stream kernel)
 
 // Waits for a barrier phase; a wait that gives up is recorded for the CTA,
 // which reports it when it ends.
@@ -84,9 +85,33 @@ __device__ __forceinline__ float group_scale(float amax, bool ue8m0) {
   return rows == 0 ? 0 : 4 * ((rows - 1) * (uint64_t)a.s_ts + (uint64_t)(a.N / kBlockK - 1) * a.s_gs + 1);
 }
 
+// Four columns of a token's output row, from n on (N is a multiple of 8).
+__device__ __forceinline__ void store_out4(const GemmArgs &a, int64_t t, int n, const float4 &c) {
+  uint16_t *o = a.out + t * a.N + n;
+  if (n < a.N && VG_ACCESS_OK(g_gemm_status, o, 8, a.out, VG_ROWS(a.T) * 2ull * (uint64_t)a.N))
+    *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2_rn(c.x, c.y), pack_bf16x2_rn(c.z, c.w));
+}
+
+// Activation and codes of a token's group of 128 columns, a warp: lane has
+// gate and up of columns 4 lane ..
+__device__ __forceinline__ void store_gated4(const GemmArgs &a, int64_t t, int group, int lane,
+                                             const float4 &g, const float4 &u) {
+  const float y0 = silu_mul(g.x, u.x), y1 = silu_mul(g.y, u.y);
+  const float y2 = silu_mul(g.z, u.z), y3 = silu_mul(g.w, u.w);
+  const float m = warp_max(fmax3(fmax3(fabsf(y0), fabsf(y1), fabsf(y2)), fabsf(y3), 0.f));
+  const float s = group_scale(m, a.ue8m0 != 0), r = __frcp_rn(s);
+  uint8_t *o = a.q + t * a.N + (int64_t)group * kHalfW + 4 * lane;
+  if (VG_ACCESS_OK(g_gemm_status, o, 4, a.q, VG_ROWS(a.T) * (uint64_t)a.N))
+    *reinterpret_cast<uint32_t *>(o) = cvt_e4m3x2(y0 * r, y1 * r) | (cvt_e4m3x2(y2 * r, y3 * r) << 16);
+  if (lane == 0) {
+    float *p = a.scale + t * a.s_ts + (int64_t)group * a.s_gs;
+    if (VG_ACCESS_OK(g_gemm_status, p, 4, a.scale, gemm_scale_extent(a))) *p = s;
+  }
+}
+
 // ------------------------------------------------------------- tile kernel
 
-constexpr int kTileT = 128, kTileW = 256, kHalfW = 128;
+constexpr int kTileT = 128, kTileW = 256;
 constexpr int kTileStages = 5;
 constexpr int kScaleSlots = 8;  // scale blocks staged ahead (stream kernel); a group of the tile kernel's two
 constexpr int kTileStageBytes = (kTileT + kHalfW) * kBlockK;  // of either CTA
@@ -98,7 +123,10 @@ constexpr int kTileGroup = 16;  // token tiles of a pair that share a sweep over
 // Dynamic shared memory (1024-byte aligned).
 template <bool GATED>
 struct TileSmem {
-  uint8_t stage[kTileStages][kTileStageBytes];
+  union {
+    uint8_t stage[kTileStages][kTileStageBytes];
+    float4 part[kTileT][kTileW / 4];  // split K: partial sums, once the products are done
+  };
   uint8_t out[kSumWarps][32 * kPart * (GATED ? 1 : 2)];  // a box of 32 rows
   float sa[2][kScaleSlots][kTileT];
   float sw[2][kScaleSlots][2];
@@ -132,15 +160,22 @@ struct GemmMaps {
   CUtensorMap a, w, out;
 };
 
-template <bool GATED>
+template <bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    fp8_gemm_tile_kernel(const GemmArgs a, const __grid_constant__ GemmMaps maps, int num_t, int num_n) {
+    fp8_gemm_tile_kernel(const GemmArgs a, const __grid_constant__ GemmMaps maps, int num_t, int num_n,
+                         int splits) {
   extern __shared__ __align__(1024) uint8_t raw[];
   TileSmem<GATED> &sm = *reinterpret_cast<TileSmem<GATED> *>(raw);
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-  const int num_k = a.K / kBlockK;
+  const int all_k = a.K / kBlockK;
   const uint32_t tiles = (uint32_t)num_t * (uint32_t)num_n;  // at most 2^29
-  const uint32_t rank = cluster_rank(), first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // rank in the pair, the pair's first rank in the cluster; the tiles of the
+  // pair (SPLIT: one, shared by the cluster's pairs) and its scale blocks
+  const uint32_t rank = cluster_rank() & 1u, base = SPLIT ? cluster_rank() & ~1u : 0u;
+  const uint32_t first = SPLIT ? blockIdx.x / (2u * (uint32_t)splits) : blockIdx.x >> 1;
+  const uint32_t pairs = SPLIT ? tiles : gridDim.x >> 1;
+  const int k_lo = SPLIT ? all_k * (int)(base >> 1) / splits : 0;
+  const int num_k = (SPLIT ? all_k * (int)((base >> 1) + 1) / splits : all_k) - k_lo;
   const int my_t = (int)rank * kTileT;  // this CTA's tokens within the pair's
   VG_NEVER_BARRIER;
 
@@ -164,6 +199,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     sm.failed = 0;
   }
   if (warp == 1) tmem_alloc<true>(&sm.tmem, 512);
+  // Launched with programmatic dependent launch: nothing but L2 prefetches of
+  // the first weight stages before the previous grid has finished.
+  if (warp == 3 && lane < kTileStages && lane < num_k) {
+    const Tile t = tile_at(first, num_t, num_n);
+    tma_prefetch_2d(&maps.w, (k_lo + lane) * kBlockK, half_row<GATED>(a, t.n, (int)rank));
+  }
   tcgen05_fence_before();
   __syncthreads();
   cluster_sync();  // the pair's barriers are initialised
@@ -186,9 +227,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (elect_lane()) {
             if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kTileStageBytes);
             uint8_t *p = sm.stage[s];
-            const uint32_t bar = cluster_addr(&sm.full[s], 0);
-            tma_load_2d_pair(p, &maps.a, kb * kBlockK, t.t0 + my_t, bar);
-            tma_load_2d_pair(p + kTileT * kBlockK, &maps.w, kb * kBlockK, r0, bar);
+            const uint32_t bar = cluster_addr(&sm.full[s], base);
+            tma_load_2d_pair(p, &maps.a, (k_lo + kb) * kBlockK, t.t0 + my_t, bar);
+            tma_load_2d_pair(p + kTileT * kBlockK, &maps.w, (k_lo + kb) * kBlockK, r0, bar);
           }
           __syncwarp();
           ++issued;
@@ -223,8 +264,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int k = 0; k < kBlockK / 32; ++k)
               mma_e4m3<true>(tmem + b * kTileW, da + 2 * k, dw + 2 * k, desc, k > 0);
-            mma_commit_pair(&sm.acc_full[b]);
-            mma_commit_pair(&sm.empty[s]);
+            mma_commit_pair(&sm.acc_full[b], base);
+            mma_commit_pair(&sm.empty[s], base);
           }
           __syncwarp();
           if (++s == kTileStages) s = 0, ++lap;
@@ -245,7 +286,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const Tile t = tile_at(i, num_t, num_n);
         const int r = half_row<GATED>(a, t.n, lane & 1), row = t.t0 + my_t + lane;
         const bool w_live = r < (GATED ? 2 : 1) * a.N;
-        const float *pw = a.w_scale + (w_live ? (int64_t)(r / kBlockK) * num_k : 0);
+        const float *pw = a.w_scale + (w_live ? (int64_t)(r / kBlockK) * all_k + k_lo : 0);
+        const float *pa = a.a_scale + k_lo * a.a_bs;
         for (int kb = 0; kb < num_k; kb += kScaleSlots, ++g) {
           if (g >= 2 && !(ok = warp_wait_phase(&sm.scale_empty[g & 1], (g / 2 - 1) & 1, &sm.failed))) break;
           const int n = min(kScaleSlots, num_k - kb);
@@ -254,7 +296,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int j = 0; j < 4; ++j) {
               const bool live = row + 32 * j < a.T;
               copy_async4(&sm.sa[g & 1][x][lane + 32 * j],
-                          a.a_scale + (live ? (row + 32 * j) * a.a_ts + (kb + x) * a.a_bs : 0), live);
+                          pa + (live ? (row + 32 * j) * a.a_ts + (kb + x) * a.a_bs : 0), live);
             }
             if (lane < 2) copy_async4(&sm.sw[g & 1][x][lane], pw + (w_live ? kb + x : 0), w_live);
           }
@@ -268,7 +310,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int quarter = warp & 3, part = (warp - 4) >> 2;  // lanes, columns of each half
     const int row = quarter * 32 + lane;
     uint8_t *box = sm.out[warp - 4];
-    const uint32_t release = cluster_addr(&sm.acc_empty[0], 0);
+    const uint32_t release = cluster_addr(&sm.acc_empty[0], base);
     uint32_t it = 0, g = 0;
     int turn = 0;
     bool ok = true;
@@ -310,7 +352,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                sc, acc[h][j]);
         }
       }
-      if (!GATED && !ok) break;
+      if (!(GATED && !SPLIT) && !ok) break;
+      if constexpr (SPLIT) {
+        // Partial sums to shared memory (the last products are done, so nothing
+        // reads the stages), 16-byte chunks swizzled by the row.
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < kPart / 4; ++q) {
+            const float2 x = acc[h][2 * q], y = acc[h][2 * q + 1];
+            const int c = h * (kHalfW / 4) + part * (kPart / 4) + q;
+            sm.part[row][c ^ (row & 7)] = make_float4(x.x, x.y, y.x, y.y);
+          }
+        break;
+      }
 
       const Tile t = tile_at(i, num_t, num_n);
       const int t0 = t.t0 + my_t + quarter * 32;  // this warp's first token
@@ -386,9 +441,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // copies that the other CTA issued ahead of this one's count: a millisecond
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   }
-  cluster_sync();  // neither CTA's memory is in use by the other any more
+  cluster_sync();  // SPLIT: all partial sums are in place; otherwise the pair is done
   __syncwarp();
   if (warp == 1) tmem_dealloc<true>(tmem, 512);
+  if constexpr (SPLIT) {
+    // Each pair of the cluster adds some of the tile's rows, in a fixed order:
+    // a warp a token row, a lane four columns of either half.
+    const Tile t = tile_at(first, num_t, num_n);
+    for (int row = (int)(base >> 1) + warp * splits; row < kTileT; row += kTileThreads / 32 * splits) {
+      const int64_t token = t.t0 + my_t + row;
+      if (token >= a.T) break;
+      float4 c[2] = {};
+      for (int x = 0; x < splits; ++x)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 p = ld_cluster4(cluster_addr(&sm.part[row][(h * (kHalfW / 4) + lane) ^ (row & 7)],
+                                                    2u * (uint32_t)x + rank));
+          c[h] = make_float4(c[h].x + p.x, c[h].y + p.y, c[h].z + p.z, c[h].w + p.w);
+        }
+      if constexpr (!GATED) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) store_out4(a, token, half_row<false>(a, t.n, h) + 4 * lane, c[h]);
+      } else {
+        store_gated4(a, token, t.n, lane, c[0], c[1]);
+      }
+    }
+    cluster_sync();  // nobody reads this CTA's sums any more
+  }
 }
 
 // ----------------------------------------------------------- stream kernel
@@ -429,7 +508,8 @@ struct StreamSmem {
 
 template <bool GATED, int TN>
 __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
-    fp8_gemm_stream_kernel(const GemmArgs a, const __grid_constant__ GemmMaps maps, int splits) {
+    fp8_gemm_stream_kernel(const GemmArgs a, const __grid_constant__ GemmMaps maps, int splits,
+                           bool w_once) {
   extern __shared__ __align__(1024) uint8_t raw[];
   using Smem = StreamSmem<TN>;
   Smem &sm = *reinterpret_cast<Smem *>(raw);
@@ -477,18 +557,23 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
   tcgen05_fence_after();
   const uint32_t tmem = sm.tmem;
   pdl_wait();
-  pdl_launch_dependents();
   int issued = 0;  // stages filled (warp 0)
 
   if (warp == 0) {
     int s = 0, lap = 0;
+    const uint64_t policy = l2_evict_first();
     for (int kb = k0; kb < k1; ++kb) {
       if (lap > 0 && !warp_wait_phase(&sm.empty[s], (lap - 1) & 1, &sm.failed)) break;
       if (elect_lane()) {
         mbar_arrive_expect_tx(&sm.full[s], Smem::kStageBytes);
         uint8_t *p = sm.stage[s];
-        tma_load_2d(p, &maps.w, kb * kBlockK, r0, &sm.full[s]);
-        tma_load_2d(p + kHalfW / 2 * kBlockK, &maps.w, kb * kBlockK, r1, &sm.full[s]);
+        if (w_once) {
+          tma_load_2d_hint(p, &maps.w, kb * kBlockK, r0, &sm.full[s], policy);
+          tma_load_2d_hint(p + kHalfW / 2 * kBlockK, &maps.w, kb * kBlockK, r1, &sm.full[s], policy);
+        } else {
+          tma_load_2d(p, &maps.w, kb * kBlockK, r0, &sm.full[s]);
+          tma_load_2d(p + kHalfW / 2 * kBlockK, &maps.w, kb * kBlockK, r1, &sm.full[s]);
+        }
         tma_load_2d(p + kHalfW * kBlockK, &maps.a, kb * kBlockK, t0, &sm.full[s]);
       }
       __syncwarp();
@@ -601,6 +686,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
   }
 
   __syncthreads();
+  pdl_launch_dependents();  // the loads are done
   if (sm.failed && warp == 0 && lane == 0) {  // copies in flight end here
     atomicOr(&g_gemm_status, kErrWaitTimeout);
     for (int it = issued < kStages ? 0 : issued - kStages; it < issued; ++it)
@@ -619,10 +705,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
         const float4 p = ld_cluster4(cluster_addr(&sm.part[j][4 * lane], (uint32_t)x));
         c = make_float4(c.x + p.x, c.y + p.y, c.z + p.z, c.w + p.w);
       }
-      const int n = r0 + 4 * lane;
-      uint16_t *o = a.out + t * a.N + n;
-      if (n < a.N && VG_ACCESS_OK(g_gemm_status, o, 8, a.out, VG_ROWS(a.T) * 2ull * (uint64_t)a.N))
-        *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2_rn(c.x, c.y), pack_bf16x2_rn(c.z, c.w));
+      store_out4(a, t, r0 + 4 * lane, c);
     } else {
       // lane: columns 4 lane .. of the group, from the half that has them
       float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
@@ -634,17 +717,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
         g = make_float4(g.x + p.x, g.y + p.y, g.z + p.z, g.w + p.w);
         u = make_float4(u.x + q.x, u.y + q.y, u.z + q.z, u.w + q.w);
       }
-      const float y0 = silu_mul(g.x, u.x), y1 = silu_mul(g.y, u.y);
-      const float y2 = silu_mul(g.z, u.z), y3 = silu_mul(g.w, u.w);
-      const float m = warp_max(fmax3(fmax3(fabsf(y0), fabsf(y1), fabsf(y2)), fabsf(y3), 0.f));
-      const float s = group_scale(m, a.ue8m0 != 0), r = __frcp_rn(s);
-      uint8_t *o = a.q + t * a.N + (int64_t)tile * kHalfW + 4 * lane;
-      if (VG_ACCESS_OK(g_gemm_status, o, 4, a.q, VG_ROWS(a.T) * (uint64_t)a.N))
-        *reinterpret_cast<uint32_t *>(o) = cvt_e4m3x2(y0 * r, y1 * r) | (cvt_e4m3x2(y2 * r, y3 * r) << 16);
-      if (lane == 0) {
-        float *p = a.scale + t * a.s_ts + (int64_t)tile * a.s_gs;
-        if (VG_ACCESS_OK(g_gemm_status, p, 4, a.scale, gemm_scale_extent(a))) *p = s;
-      }
+      store_gated4(a, t, tile, lane, g, u);
     }
   }
   cluster_sync();  // nobody reads this CTA's sums any more
@@ -717,10 +790,10 @@ cudaError_t opt_in_once(std::atomic<uint64_t> &opted_in, const void *kern) {
   return e;
 }
 
-template <bool GATED>
-cudaError_t launch_tile(const GemmArgs &a, int sms, cudaStream_t s) {
+template <bool GATED, bool SPLIT>
+cudaError_t launch_tile(const GemmArgs &a, int splits, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> opted_in{0};
-  const cudaError_t e = opt_in_once(opted_in, (const void *)fp8_gemm_tile_kernel<GATED>);
+  const cudaError_t e = opt_in_once(opted_in, (const void *)fp8_gemm_tile_kernel<GATED, SPLIT>);
   if (e != cudaSuccess) return e;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   GemmMaps maps;
@@ -734,9 +807,10 @@ cudaError_t launch_tile(const GemmArgs &a, int sms, cudaStream_t s) {
   const int num_t = (a.T + 2 * kTileT - 1) / (2 * kTileT);
   const int num_n = GATED ? a.N / kHalfW : (a.N + kTileW - 1) / kTileW;
   const int64_t tiles = (int64_t)num_t * num_n;
-  const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  return launch_pdl_cluster(fp8_gemm_tile_kernel<GATED>, dim3(2 * pairs), 2, dim3(kTileThreads),
-                            sizeof(TileSmem<GATED>), s, a, maps, num_t, num_n);
+  const int64_t pairs = SPLIT ? tiles * splits : (tiles < sms / 2 ? tiles : sms / 2);
+  return launch_pdl_cluster(fp8_gemm_tile_kernel<GATED, SPLIT>, dim3((unsigned)(2 * pairs)),
+                            SPLIT ? 2 * splits : 2, dim3(kTileThreads), sizeof(TileSmem<GATED>), s, a, maps,
+                            num_t, num_n, splits);
 }
 
 template <bool GATED, int TN>
@@ -752,9 +826,13 @@ cudaError_t launch_stream(const GemmArgs &a, int splits, cudaStream_t s) {
     return cudaErrorInvalidValue;
   maps.out = maps.a;  // not used: the sums are stored by threads
   const int ctas = GATED ? 2 * splits : splits;
+  // A weight that one token tile reads once and that would fill more than a
+  // quarter of L2 passes it by (117 MB, one token: 21.2 -> 19.7 us; 67 MB: 12.9
+  // -> 11.8; 25 MB, which stays in L2 from call to call: 6.4 -> 6.8).
+  const bool w_once = a.T <= TN && (GATED ? 2 : 1) * (int64_t)a.N * a.K > 32 << 20;
   const dim3 grid((unsigned)((a.N + kHalfW - 1) / kHalfW * ctas), (unsigned)((a.T + TN - 1) / TN));
   return launch_pdl_cluster(fp8_gemm_stream_kernel<GATED, TN>, grid, ctas, dim3(kStreamThreads),
-                            sizeof(StreamSmem<TN>), s, a, maps, splits);
+                            sizeof(StreamSmem<TN>), s, a, maps, splits, w_once);
 }
 
 template <bool GATED>
@@ -764,47 +842,70 @@ cudaError_t launch_form(const GemmArgs &a, const GemmPlan &p, int sms, cudaStrea
     case 32: return launch_stream<GATED, 32>(a, p.splits, s);
     case 64: return launch_stream<GATED, 64>(a, p.splits, s);
     case 128: return launch_stream<GATED, 128>(a, p.splits, s);
-    default: return launch_tile<GATED>(a, sms, s);
+    default:
+      return p.splits > 1 ? launch_tile<GATED, true>(a, p.splits, sms, s)
+                          : launch_tile<GATED, false>(a, 1, sms, s);
   }
 }
 
 }  // namespace
 
 // Which kernel, and its split, by an estimate of either one's time, in
-// microseconds (measured on GB300 over T = 1..1024, N = 1024..57344, K =
-// 4096..28672):
-//   tile kernel    a wave of pairs: 3 + 0.52 per scale block of K
+// microseconds (fitted on GB300 to T = 1..1024, N = 1024..57344, K =
+// 4096..28672; over those the choice is within 10 % of the best one):
+//   tile kernel    a wave of pairs: 0.42 per scale block of its share of K, and
+//                  4.4 (one share) .. 9.5 (four) for start, end and the sum of
+//                  the shares
 //   stream kernel  a wave of CTAs: 3.5, and 0.27 (16 tokens) .. 0.48 (128) per
-//                  block of its split or the weight's bytes at 6 TB/s (a second
-//                  token tile reads it from L2, at about three times that),
-//                  whichever is longer, with a fifth of the other
-// A wave of stream CTAs is taken as 85 % of the slots: clusters do not fill
-// every SM, and a second wave costs as much as the first (6144 x 4096, one
-// token: five ways, 240 CTAs, 6.5 us; six ways, 288 of 304 slots, 10.3 us).
-// Splits are powers of two: others pack worse (64 x 4096 x 4096: four ways
-// 7.5 us, five 9.4).
+//                  block of its split or the weight's bytes at 6.3 TB/s (two
+//                  thirds of that again for every further token tile, which
+//                  reads the weight from L2), whichever is longer, with a
+//                  fifth of the other
+// Clusters do not fill every SM, and a second wave costs as much as the first
+// (6144 x 4096, one token: five ways, 240 CTAs, 6.5 us; six ways, 288 of 304
+// slots, 10.3 us; 256 x 4096 x 14336 in tiles: three shares, 96 CTAs, 24.9 us,
+// four, 128, 40.7), so a wave is taken as the part of the slots that clusters
+// of that size were seen to fill.  Stream splits are powers of two: others
+// pack worse (64 x 4096 x 4096: four ways 7.5 us, five 9.4).
 GemmPlan plan_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
   GemmPlan p;
   const int64_t blocks = K / kBlockK, rows = (N + kHalfW - 1) / kHalfW * (gated ? 2 : 1);
+  const auto waves_of = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
+  const auto part = [](int64_t slots, int64_t percent) { return slots < 8 ? slots : slots * percent / 100; };
   const int64_t pairs =
       (T + 2 * kTileT - 1) / (2 * kTileT) * (gated ? N / kHalfW : (N + kTileW - 1) / kTileW);
   const int64_t pair_slots = sms < 2 ? 1 : sms / 2;
-  double best = (double)((pairs + pair_slots - 1) / pair_slots) * (3.0 + 0.52 * (double)blocks);
-  const int tn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
-  const int64_t token_tiles = (T + tn - 1) / tn, tiles = rows * token_tiles;
-  if (token_tiles > 65535) return p;
-  const int64_t slots = (int64_t)sms * (tn <= 64 ? 2 : 1), wave = slots < 8 ? slots : slots * 85 / 100;
-  const double per_block = tn <= 32 ? 0.27 : (tn == 64 ? 0.36 : 0.48);
-  const double bytes = (double)rows * kHalfW * (double)K * (1.0 + (double)(token_tiles - 1) / 3.0);
-  for (int s = 1; s <= (gated ? kMaxSplit / 2 : kMaxSplit) && s <= blocks; s *= 2) {
-    const double waves = (double)((tiles * s + wave - 1) / wave);
-    const double chain = (double)((blocks + s - 1) / s) * per_block;
-    const double traffic = bytes / waves / 6.0e6;  // 6.0 TB/s
-    const double cost = waves * (3.5 + (chain > traffic ? chain + 0.2 * traffic : traffic + 0.2 * chain));
+  static const double kFixed[4] = {4.4, 7.0, 9.0, 9.5};
+  static const int kFill[4] = {100, 90, 64, 64};
+  double best = 1e30;
+  for (int s = 1; s <= 4 && s <= blocks; ++s) {
+    const double waves = waves_of(pairs * s, part(pair_slots, kFill[s - 1]));
+    if (s > 1 && waves > 1) break;
+    const double cost = waves * (kFixed[s - 1] + 0.42 * (double)((blocks + s - 1) / s));
     if (cost < best) {
       best = cost;
-      p.tn = tn;
       p.splits = s;
+    }
+  }
+  // one token tile, or for more than 64 tokens tiles of 64 or 128
+  const int smallest = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
+  for (int tn = smallest; tn <= (T <= 64 ? smallest : 128); tn *= 2) {
+    const int64_t token_tiles = (T + tn - 1) / tn, tiles = rows * token_tiles;
+    if (token_tiles > 65535) continue;
+    const int64_t slots = (int64_t)sms * (tn <= 64 ? 2 : 1);
+    const double per_block = tn <= 32 ? 0.27 : (tn == 64 ? 0.36 : 0.48);
+    const double bytes = (double)rows * kHalfW * (double)K * (1.0 + (double)(token_tiles - 1) * 2.0 / 3.0);
+    for (int s = 1; s <= (gated ? kMaxSplit / 2 : kMaxSplit) && s <= blocks; s *= 2) {
+      const bool big = tn == 128 && s * (gated ? 2 : 1) == 8;  // eight SMs a cluster
+      const double waves = waves_of(tiles * s, part(slots, big ? 64 : 85));
+      const double chain = (double)((blocks + s - 1) / s) * per_block;
+      const double traffic = bytes / waves / 6.3e6;
+      const double cost = waves * (3.5 + (chain > traffic ? chain + 0.2 * traffic : traffic + 0.2 * chain));
+      if (cost < best) {
+        best = cost;
+        p.tn = tn;
+        p.splits = s;
+      }
     }
   }
   return p;

@@ -55,6 +55,21 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *m, int
       : "memory");
 }
 
+// The same with an L2 policy (l2_evict_first()): data that is read once.
+__device__ __forceinline__ uint64_t l2_evict_first() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_2d_hint(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
+                                                 uint64_t *bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // Asks for one box to be brought into L2.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *m, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x), "r"(y)
@@ -254,13 +269,13 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
                 : "memory");
 }
 
-// Arrives on `bar` of both CTAs of the pair (or of this one alone) once this
-// thread's earlier products have finished.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+// Arrives on `bar` of both CTAs of the pair whose first cluster rank is `base`
+// (or of this one alone) once this thread's earlier products have finished.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar, uint32_t base) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)(3u << base))
       : "memory");
 }
 template <bool PAIR>
