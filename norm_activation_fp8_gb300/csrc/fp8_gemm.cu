@@ -41,6 +41,19 @@ namespace {
 constexpr int kBlockK = 128;  // codes of K per scale block (and per stage)
 constexpr int kHalfW = 128;   // weight rows of a tile's half (tile kernel), of a tile (stream kernel)
 
+// Test-only builds (VG_TEST_FORCE_WAIT_TIMEOUT): a barrier that nothing
+// arrives on, in the kernels' own shared memory (a static variable would move
+// their 1024-byte aligned base).
+#ifdef VG_TEST_FORCE_WAIT_TIMEOUT
+#define VG_GEMM_NEVER uint64_t never;
+#define VG_GEMM_NEVER_INIT(sm) mbar_init(&(sm).never, 1)
+#define VG_GEMM_FORCED_TIMEOUT(sm, first) ((first) && !mbar_wait_bounded(&(sm).never, 0))
+#else
+#define VG_GEMM_NEVER
+#define VG_GEMM_NEVER_INIT(sm)
+#define VG_GEMM_FORCED_TIMEOUT(sm, first) false
+#endif
+
 // Waits for a barrier phase; a wait that gives up is recorded for the CTA,
 // which reports it when it ends.
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile uint32_t *failed) {
@@ -135,6 +148,7 @@ struct TileSmem {
   uint64_t acc_full[2], acc_empty[2], scale_full[2], scale_empty[2], drain;
   uint32_t tmem;
   uint32_t failed;
+  VG_GEMM_NEVER
 };
 
 // The i-th tile: token tiles run fastest within groups of
@@ -177,7 +191,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int k_lo = SPLIT ? all_k * (int)(base >> 1) / splits : 0;
   const int num_k = (SPLIT ? all_k * (int)((base >> 1) + 1) / splits : all_k) - k_lo;
   const int my_t = (int)rank * kTileT;  // this CTA's tokens within the pair's
-  VG_NEVER_BARRIER;
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&maps.a);
@@ -194,7 +207,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(&sm.scale_empty[i], kSumWarps);
     }
     mbar_init(&sm.drain, 1);
-    VG_NEVER_BARRIER_INIT();
+    VG_GEMM_NEVER_INIT(sm);
     fence_mbar_init();
     sm.failed = 0;
   }
@@ -252,7 +265,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                                  wait_phase(odd ? &sm.acc_empty[b] : &sm.full[s],
                                                             odd ? (it / 2 - 1) & 1 : lap & 1, &sm.failed))))
             break;
-          if (VG_FORCED_TIMEOUT(it == 0)) {
+          if (VG_GEMM_FORCED_TIMEOUT(sm, it == 0)) {
             sm.failed = 1;
             ok = false;
             break;
@@ -504,6 +517,7 @@ struct StreamSmem {
   uint64_t acc_full[kBufs], acc_empty[kBufs], scale_full[kScaleSlots], scale_empty[kScaleSlots], drain;
   uint32_t tmem;
   uint32_t failed;
+  VG_GEMM_NEVER
 };
 
 template <bool GATED, int TN>
@@ -523,7 +537,6 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
   const int r1 = GATED ? a.N + r0 : r0 + kHalfW / 2;
   const int t0 = (int)blockIdx.y * TN;
   const int k0 = num_k * split / splits, k1 = num_k * (split + 1) / splits;
-  VG_NEVER_BARRIER;
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&maps.a);
@@ -541,7 +554,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
       mbar_init(&sm.scale_empty[i], 4);
     }
     mbar_init(&sm.drain, 1);
-    VG_NEVER_BARRIER_INIT();
+    VG_GEMM_NEVER_INIT(sm);
     fence_mbar_init();
     sm.failed = 0;
   }
@@ -590,7 +603,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
                                        wait_phase(odd ? &sm.acc_empty[b] : &sm.full[s],
                                                   odd ? (it / kBufs - 1) & 1 : lap & 1, &sm.failed)))
         break;
-      if (VG_FORCED_TIMEOUT(it == 0)) {
+      if (VG_GEMM_FORCED_TIMEOUT(sm, it == 0)) {
         sm.failed = 1;
         break;
       }

@@ -72,7 +72,18 @@ PLAIN = [  # T, N, K
     (65, 640, 256), (100, 264, 32768), (127, 136, 512), (128, 256, 128), (129, 384, 1024),
     (200, 4096, 4096), (256, 4096, 2048), (257, 248, 384), (300, 6144, 1024), (513, 1032, 512),
     (1000, 2056, 896), (2049, 4096, 640), (4100, 264, 256),
+    # the plans that the sizes above do not take
+    (384, 4096, 4096), (196, 3704, 6912), (1465, 504, 29056), (20, 96, 128), (23, 744, 256),
+    (24, 72, 13312), (69, 28872, 128), (70, 3800, 6912),
 ]
+
+
+def test_sizes_take_every_plan():
+    """On 152 SMs the sizes above run every kernel with every split that some
+    size takes."""
+    import test_layer_ops_host as host
+    for sizes, gated in ((PLAIN, False), (GATED, True)):
+        assert {host.plan(*x, gated, 152) for x in sizes} >= host.reachable(gated)
 
 
 @pytest.mark.parametrize("T,N,K", PLAIN)
@@ -99,6 +110,8 @@ GATED = [  # T, I, K
     (17, 128, 128), (33, 1024, 640), (57, 2048, 2048), (64, 384, 32768), (65, 256, 512), (127, 640, 256),
     (128, 128, 384), (129, 1152, 512), (200, 14336, 256), (256, 2048, 1024), (300, 128, 896),
     (513, 1024, 512), (1000, 896, 640), (2049, 2048, 256), (4100, 128, 128),
+    (1738, 384, 18048), (609, 640, 11904), (812, 384, 25728), (22, 1152, 256), (25, 896, 512),
+    (83, 23936, 256),
 ]
 
 
@@ -135,6 +148,25 @@ def test_gated(T, I, K):
         assert bool(((got - grp(y)).abs() <= tol).all())
         assert intact(qbuf) and intact(sbuf)
     assert vg.vg_device_status() == 0
+
+
+@pytest.mark.parametrize("T,N,K", [(70001, 32768, 128), (70001, 32768, 256)])
+def test_outputs_past_32_bit_offsets(T, N, K):
+    """Outputs of more than 2^31 elements: rows sampled over all of them."""
+    import torch
+    a, s, w, sw, A, W = operands(T, N, K, 5, exact=True)
+    rows = torch.tensor([0, 127, 128, 40000, 65535, 65536, 65537, 69999, 70000], device="cuda")
+    out = vg.fp8_block_gemm(a, s, w, sw)
+    assert torch.equal(out[rows], (A[rows] @ W.t()).to(torch.bfloat16))
+    del out
+    if K == 128:
+        w2 = torch.cat([w.view(torch.uint8), w.view(torch.uint8)]).view(torch.float8_e4m3fn)
+        q, sc = vg.fp8_block_gemm_silu_mul_fp8(a, s, w2, torch.cat([sw, sw]))
+        few = vg.fp8_block_gemm_silu_mul_fp8(a.view(torch.uint8)[rows].view(torch.float8_e4m3fn), s[rows],
+                                             w2, torch.cat([sw, sw]))
+        # the sums are exact in either kernel, and the same steps follow
+        assert torch.equal(q.view(torch.uint8)[rows], few[0].view(torch.uint8))
+        assert torch.equal(sc[rows], few[1])
 
 
 def test_gated_zero_rows_and_saturated_gates():

@@ -59,6 +59,56 @@ def test_gemm_refusals(lib):
     assert gated(lib, q=None, s=None, a=None, sa=None, w=None, sw=None, T=0) == OK
 
 
+class GemmPlan(ctypes.Structure):
+    _fields_ = [("tn", ctypes.c_int), ("splits", ctypes.c_int)]
+
+
+def plan(T, N, K, gated, sms):
+    """The library's own plan: (tokens a tile of the stream kernel or 0 for the
+    tile kernel, ways that K is split)."""
+    f = vg.load()._ZN2vg9plan_gemmElllbi
+    f.restype, f.argtypes = GemmPlan, [ctypes.c_int64] * 3 + [ctypes.c_bool, ctypes.c_int]
+    p = f(T, N, K, gated, sms)
+    return p.tn, p.splits
+
+
+def _sizes(gated, n, seed):
+    import random
+    r = random.Random(seed)
+    unit = 128 if gated else 8
+    for _ in range(n):
+        yield (max(1, int(2 ** (13 * r.random()))), unit * int(2 ** ((8 if gated else 13) * r.random())),
+               128 * int(2 ** (8 * r.random())))
+
+
+def reachable(gated):
+    return {plan(*x, gated, 152) for x in _sizes(gated, 20000, 1)}
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_every_plan_can_be_launched(lib, gated):
+    """A split never exceeds the scale blocks or its cluster the eight CTAs
+    that may form one, the grid stays within its limits, and few tokens take
+    one token tile."""
+    sizes = list(_sizes(gated, 5000, 2)) + [(2 ** 24, 2 ** 15, 128), (2 ** 24, 128, 32768), (1, 128, 128)]
+    if not gated:
+        sizes += [(1, 2 ** 20, 32768), (2 ** 24, 8, 128), (128, 2 ** 20, 128), (1, 8, 32768)]
+    for sms in (152, 148, 132, 16, 2, 1):
+        for T, N, K in sizes:
+            tn, splits = plan(T, N, K, gated, sms)
+            assert 1 <= splits <= K // 128
+            if tn == 0:
+                assert splits <= 4
+                tiles = (T + 255) // 256 * (N // 128 if gated else (N + 255) // 256)
+                assert splits == 1 or 2 * splits * tiles < 2 ** 31
+                assert tiles < 2 ** 32
+            else:
+                assert tn in (16, 32, 64, 128) and splits * (2 if gated else 1) in (1, 2, 4, 8)
+                assert (T + tn - 1) // tn <= 65535
+                assert T > 64 or tn >= T
+    assert {tn for tn, _ in reachable(gated)} == {0, 16, 32, 64, 128}
+
+
 def _sec(sections):
     return None if sections is None else (ctypes.c_int32 * len(sections))(*sections)
 
