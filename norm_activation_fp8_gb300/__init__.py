@@ -351,7 +351,7 @@ def vg_silu_mul_nvfp4(q4, block_scale, gate_up, global_scale, stream=None,
 def _arg(t, dtypes, name, dev, contiguous=True):
     """Device pointer of a tensor on the current device (or None): one pass of
     cheap checks, the reasons only when one fails."""
-    if t is None:
+    if t is None:  # the library refuses a missing one
         return None
     if t.dtype in dtypes and t.get_device() == dev and (not contiguous or t.is_contiguous()):
         return t.data_ptr()
@@ -412,11 +412,13 @@ def _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_
         raise ValueError("cos_sin_cache: expected head_dim columns")
     if q_weight is not None:
         _shape(q_weight, (head_dim,), "q_weight")
+        q_weight = _arg(q_weight, bf16, "q_weight", dev)
     if k_weight is not None:
         _shape(k_weight, (head_dim,), "k_weight")
-    return (_arg(qkv, bf16, "qkv", dev), _arg(q_weight, bf16, "q_weight", dev),
-            _arg(k_weight, bf16, "k_weight", dev), _arg(cos_sin_cache, f32, "cos_sin_cache", dev),
-            _arg(positions, i64, "positions", dev), sec, axes, T, max_pos)
+        k_weight = _arg(k_weight, bf16, "k_weight", dev)
+    return (_arg(qkv, bf16, "qkv", dev), q_weight, k_weight,
+            _arg(cos_sin_cache, f32, "cos_sin_cache", dev), _arg(positions, i64, "positions", dev),
+            sec, axes, T, max_pos)
 
 
 def vg_fused_qk_norm_mrope(qkv, q_weight, k_weight, cos_sin_cache, positions, sections,
@@ -432,9 +434,11 @@ def vg_fused_qk_norm_mrope(qkv, q_weight, k_weight, cos_sin_cache, positions, se
     q, qw, kw, table, pos, sec, axes, T, max_pos = _rope_args(
         qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_q_heads, num_kv_heads,
         head_dim, dev)
-    _check((_lib or load()).vg_fused_qk_norm_mrope(
+    st = (_lib or load()).vg_fused_qk_norm_mrope(
         q, qw, kw, table, pos, sec, axes, T, num_q_heads, num_kv_heads, head_dim, max_pos, eps,
-        1 if is_neox else 0, 1 if interleaved else 0, raw))
+        is_neox, interleaved, raw)
+    if st:
+        _check(st)
 
 
 def vg_fused_qk_norm_rope_append(qkv, k_cache, v_cache, q_weight, k_weight, cos_sin_cache,
@@ -463,15 +467,20 @@ def vg_fused_qk_norm_rope_append(qkv, k_cache, v_cache, q_weight, k_weight, cos_
     if shape != v_cache.shape or strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must have the same shape and strides")
     _shape(slots, (T,), "slots")
-    if k_scale is not None and k_scale.numel() != 1 or v_scale is not None and v_scale.numel() != 1:
-        raise ValueError("k_scale and v_scale: expected one fp32 value on the device")
-    kinds = bf16 if k_scale is None and v_scale is None else fp8
-    _check((_lib or load()).vg_fused_qk_norm_rope_append(
+    kinds = bf16
+    if k_scale is not None or v_scale is not None:
+        kinds = fp8
+        for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if x is not None and x.numel() != 1:
+                raise ValueError(f"{name}: expected one fp32 value on the device")
+        k_scale, v_scale = _arg(k_scale, f32, "k_scale", dev), _arg(v_scale, f32, "v_scale", dev)
+    st = (_lib or load()).vg_fused_qk_norm_rope_append(
         q, _arg(k_cache, kinds, "k_cache", dev, False), _arg(v_cache, kinds, "v_cache", dev, False),
-        qw, kw, table, pos, _arg(slots, i64, "slots", dev), _arg(k_scale, f32, "k_scale", dev),
-        _arg(v_scale, f32, "v_scale", dev), sec, axes, T, num_q_heads, num_kv_heads, head_dim,
-        max_pos, shape[0], shape[1], strides[0], strides[1], strides[2], eps, 1 if is_neox else 0,
-        1 if interleaved else 0, raw))
+        qw, kw, table, pos, _arg(slots, i64, "slots", dev), k_scale, v_scale, sec, axes, T,
+        num_q_heads, num_kv_heads, head_dim, max_pos, shape[0], shape[1], strides[0], strides[1],
+        strides[2], eps, is_neox, interleaved, raw)
+    if st:
+        _check(st)
 
 
 def _block_gemm_args(a, a_scale, w, w_scale, a_options, dev):
@@ -482,13 +491,10 @@ def _block_gemm_args(a, a_scale, w, w_scale, a_options, dev):
     if K2 != K:
         raise ValueError("a and w must have the same number of columns")
     kb = K // BLOCK
-    want = (kb, (T + 3) // 4 * 4) if a_options & COLUMN_MAJOR else (T, kb)
-    if a_scale.shape != want:
-        _shape(a_scale, want, "a_scale")
-    if w_scale.shape != ((N + BLOCK - 1) // BLOCK, kb):
-        _shape(w_scale, ((N + BLOCK - 1) // BLOCK, kb), "w_scale")
+    _shape(a_scale, (kb, (T + 3) // 4 * 4) if a_options & COLUMN_MAJOR else (T, kb), "a_scale")
+    _shape(w_scale, ((N + BLOCK - 1) // BLOCK, kb), "w_scale")
     return (_arg(a, fp8, "a", dev), _arg(a_scale, f32, "a_scale", dev), _arg(w, fp8, "w", dev),
-            _arg(w_scale, f32, "w_scale", dev)), T, N, K
+            _arg(w_scale, f32, "w_scale", dev), T, N, K)
 
 
 def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=None):
@@ -497,12 +503,21 @@ def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=No
 
     a [T,K] fp8 with a_scale fp32 [T,K/128] (or, with COLUMN_MAJOR in
     a_options, [K/128,T4] as the per-group ops write it); w [N,K] fp8 with
-    w_scale fp32 [ceil(N/128),K/128].  UE8M0 scales need no option."""
+    w_scale fp32 [ceil(N/128),K/128].  UE8M0 scales need no option.
+    ``out`` None allocates it; returns out."""
+    bf16 = _kinds()[0]
     dev, raw = _here(a, stream)
-    ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
-    _shape(out, (T, N), "out")
-    _check((_lib or load()).vg_fp8_block_gemm(_arg(out, _kinds()[0], "out", dev), *ptrs, T, N, K,
-                                              a_options, raw))
+    pa, psa, pw, psw, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
+    if out is None:  # after the checks: an allocation right behind a launch is slower
+        out = a.new_empty((T, N), dtype=bf16[0])
+        po = out.data_ptr()
+    else:
+        _shape(out, (T, N), "out")
+        po = _arg(out, bf16, "out", dev)
+    st = (_lib or load()).vg_fp8_block_gemm(po, pa, psa, pw, psw, T, N, K, a_options, raw)
+    if st:
+        _check(st)
+    return out
 
 
 def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: int = 0,
@@ -513,19 +528,27 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     a and a_scale as for vg_fp8_block_gemm; w [2I,K] fp8 (gate rows [0,I), up
     rows [I,2I)) with w_scale [2I/128,K/128]; q [T,I] fp8, scale fp32
     [T,I/128], or with COLUMN_MAJOR in out_options [I/128,T4]; UE8M0 in
-    out_options: power-of-two scales."""
+    out_options: power-of-two scales.  ``q`` and ``scale`` both None
+    allocate them; returns (q, scale)."""
     _, fp8, f32, _, _ = _kinds()
     dev, raw = _here(a, stream)
-    ptrs, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
+    pa, psa, pw, psw, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
     if N % 2:
         raise ValueError("w must have an even number of rows (gate, then up)")
     inter = N // 2
-    _shape(q, (T, inter), "q")
-    _shape(scale, (inter // BLOCK, (T + 3) // 4 * 4) if out_options & COLUMN_MAJOR
-           else (T, inter // BLOCK), "scale")
-    _check((_lib or load()).vg_fp8_block_gemm_silu_mul_fp8(
-        _arg(q, fp8, "q", dev), _arg(scale, f32, "scale", dev), *ptrs, T, inter, K, a_options,
-        out_options, raw))
+    shape = (inter // BLOCK, (T + 3) // 4 * 4) if out_options & COLUMN_MAJOR else (T, inter // BLOCK)
+    if q is None and scale is None:
+        q, scale = a.new_empty((T, inter), dtype=fp8[0]), a.new_empty(shape, dtype=f32[0])
+        pq, ps = q.data_ptr(), scale.data_ptr()
+    else:
+        _shape(q, (T, inter), "q")
+        _shape(scale, shape, "scale")
+        pq, ps = _arg(q, fp8, "q", dev), _arg(scale, f32, "scale", dev)
+    st = (_lib or load()).vg_fp8_block_gemm_silu_mul_fp8(pq, ps, pa, psa, pw, psw, T, inter, K,
+                                                         a_options, out_options, raw)
+    if st:
+        _check(st)
+    return q, scale
 
 
 def vg_device_status(reset: bool = False) -> int:
@@ -636,17 +659,11 @@ def silu_mul_nvfp4(gate_up, global_scale, stream=None):
 
 def fp8_block_gemm(a, a_scale, w, w_scale, a_options: int = 0, stream=None):
     """Returns out bf16 [T,N]."""
-    out = a.new_empty((a.shape[0], w.shape[0]), dtype=_kinds()[0][0])
-    vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options, stream)
-    return out
+    return vg_fp8_block_gemm(None, a, a_scale, w, w_scale, a_options, stream)
 
 
 def fp8_block_gemm_silu_mul_fp8(a, a_scale, w, w_scale, a_options: int = 0, out_options: int = 0,
                                 stream=None):
     """Returns (q float8_e4m3fn [T,I], scale)."""
-    T, inter = a.shape[0], w.shape[0] // 2
-    q = a.new_empty((T, inter), dtype=_kinds()[1][0])
-    s = a.new_empty((inter // BLOCK, (T + 3) // 4 * 4) if out_options & COLUMN_MAJOR
-                    else (T, inter // BLOCK), dtype=_kinds()[2][0])
-    vg_fp8_block_gemm_silu_mul_fp8(q, s, a, a_scale, w, w_scale, a_options, out_options, stream)
-    return q, s
+    return vg_fp8_block_gemm_silu_mul_fp8(None, None, a, a_scale, w, w_scale, a_options, out_options,
+                                          stream)
