@@ -7,23 +7,38 @@
 //           rounded to bf16), s = max(amax |y| over 128 columns, 1e-10) / 448
 //           (or the power of two above it), q = e4m3(y / s)
 //
-// Tile kernel.  Persistent pairs of CTAs, one CTA per SM, compute tiles of 256
-// tokens x 256 weight rows (gated: 128 gate rows and the same 128 up rows), one
-// scale block (128 of K) at a time.  A CTA of the pair stages its 128 tokens
-// and one half of the weight rows by TMA in six 32 KB stages; one thread of
-// the pair issues four M256 N256 K32 products, which read the weight halves
-// of both (a CTA alone would stage and read all 256 weight rows: 96 KB of
-// shared memory traffic a block for 512 cycles of products, more than the
-// 128 bytes a cycle that there are; a pair needs 64 KB).  They go to one of
-// two 256-column accumulators, and in either CTA sixteen warps take the block's sum out of tensor memory and
-// add it, times its two scales, to an fp32 sum in registers (the block scales
-// are arbitrary fp32 numbers, so the tensor cores cannot apply them).  The
-// two accumulators let the products of the next block run meanwhile.  A
-// thread holds 32 columns of either half of a token's row: for the gated form
-// gate and up of the same columns, so that the activation needs no exchange
-// and a group's amax one float from each of the three warps beside it.
+// Tile kernel.  Pairs of CTAs, one CTA per SM, compute tiles of 256 tokens x
+// 256 weight rows (gated: 128 gate rows and the same 128 up rows), one scale
+// block (128 of K) at a time.  A CTA of the pair stages its 128 tokens and one
+// half of the weight rows by TMA in five 32 KB stages; one thread of the pair
+// issues four M256 N256 K32 products, which read the weight halves of both (a
+// CTA alone would stage and read all 256 weight rows: 96 KB of shared memory
+// traffic a block for 512 cycles of products, more than the 128 bytes a cycle
+// that there are; a pair needs 64 KB).  They go to one of two 256-column
+// accumulators, and in either CTA sixteen warps take the block's sum out of
+// tensor memory and add it, times its two scales, to an fp32 sum in registers
+// (the block scales are arbitrary fp32 numbers, so the tensor cores cannot
+// apply them).  The two accumulators let the products of the next block run
+// meanwhile.  A thread holds 32 columns of either half of a token's row: for
+// the gated form gate and up of the same columns, so that the activation needs
+// no exchange and a group's amax one float from each of the three warps beside
+// it.
 //   warp 0: TMA   warp 1: products   warp 2: scales (global -> shared)
 //   warps 4-19: sums and epilogue (warp w: tensor memory lanes 32 (w mod 4))
+// Many tiles: persistent pairs.  Few tiles and a long K (SPLIT): up to four
+// pairs of a cluster share a tile's scale blocks and add their fp32 sums
+// through distributed shared memory in a fixed order.
+//
+// What bounds it, at 4096 x 8192 x 28672 (684 us, 2810 TFLOP/s; the measured
+// bf16 rate is 1946 in a burst, so e4m3 at most about 3890): a block takes 840
+// cycles.  Its products are 512; the way round an accumulator (products
+// issued, finished, seen by the summing warps, read, given back to the issuing
+// warp) costs 940 cycles without any work in it, and with two accumulators half
+// of that and of the work shows.  Without the sums it runs at 3230, without
+// sums and tensor memory loads at 3470 TFLOP/s.  Shorter accumulators (four of
+// 128 columns) add a wait and a release a block and were slower (2100), a CTA
+// alone 1980, eight summing warps 1760.  Long runs meet the power limit first.
+
 #include <atomic>
 
 #include "common.cuh"
@@ -497,6 +512,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // Up to 64 tokens two CTAs share an SM (each asks for more than a third of its
 // shared memory and for at most half of its tensor memory, so no allocation
 // ever waits).
+//
+// Bound by the weight's bytes: 57344 x 8192, one token, 71 us (0.97 of the copy
+// rate); gated 14336 x 4096, one token, 19.3 us (0.90); 57 tokens x 28672 x
+// 8192 gated 86 us (0.80: 448 CTAs are a wave and a half).  Small products are
+// bound by a call's fixed 3.5 us (6144 x 4096, one token: 6.5 us, 0.57).
 
 constexpr int kStreamThreads = 256;
 constexpr int kMaxSplit = 8;
