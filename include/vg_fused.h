@@ -352,7 +352,8 @@ vg_status vg_fused_qk_norm_mrope(uint16_t *qkv, const uint16_t *q_weight, const 
  *   page_stride, token_stride, head_stride  in elements, multiples of 8, no
  *                  two places overlapping (a stride over an extent of one is
  *                  ignored); offsets may pass 32 bits
- * The caches must be 16-byte aligned and overlap no other tensor.
+ * The caches must be 16-byte aligned and overlap neither each other (the same
+ * pointer for both is VG_ERR_BAD_SHAPE) nor another tensor.
  */
 vg_status vg_fused_qk_norm_rope_append(
     uint16_t *qkv, void *k_cache, void *v_cache, const uint16_t *q_weight,

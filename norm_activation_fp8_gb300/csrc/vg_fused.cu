@@ -711,6 +711,7 @@ vg_status vg_fused_qk_norm_rope_append(
   if (!qkv || !k_cache || !v_cache || !cos_sin_cache || !positions || !slots ||
       vg::half_weighted(a) || ((k_scale == nullptr) != (v_scale == nullptr)))
     return VG_ERR_NULL_PTR;
+  if (k_cache == v_cache) return VG_ERR_BAD_SHAPE;
   if (vg::misaligned(k_cache, 16) || vg::misaligned(v_cache, 16) || vg::misaligned(slots, 8) ||
       vg::misaligned(k_scale, 4) || vg::misaligned(v_scale, 4))
     return VG_ERR_MISALIGNED;

@@ -162,6 +162,98 @@ def test_arguments_on_the_gpu():
         vg.vg_fused_qk_norm_rope_append(qkv, k, k.clone(), None, None, table, pos, slots[:3], 2, 1, 64, 1e-6)
 
 
+def test_no_tokens():
+    """Every call with zero tokens returns and writes nothing."""
+    import torch
+    f8 = torch.float8_e4m3fn
+    w, sw = torch.zeros((256, 256), dtype=f8, device="cuda"), torch.ones((2, 2), device="cuda")
+    for col in (0, COL):
+        a = torch.zeros((0, 256), dtype=f8, device="cuda")
+        sa = torch.zeros((2, 0) if col else (0, 2), device="cuda")
+        assert vg.fp8_block_gemm(a, sa, w, sw, col).shape == (0, 256)
+        q, s = vg.fp8_block_gemm_silu_mul_fp8(a, sa, w, sw, col, col)
+        assert q.shape == (0, 128) and s.shape == ((1, 0) if col else (0, 1))
+    qkv = torch.zeros((0, 4 * 64), device="cuda").bfloat16()
+    table, none = torch.zeros((16, 64), device="cuda"), torch.zeros(0, dtype=torch.int64, device="cuda")
+    k, v = (torch.ones((2, 16, 1, 64), device="cuda").bfloat16() for _ in range(2))
+    vg.vg_fused_qk_norm_mrope(qkv, None, None, table, none.view(2, 0), (16, 16), 2, 1, 64, 1e-6)
+    vg.vg_fused_qk_norm_rope_append(qkv, k, v, None, None, table, none, none, 2, 1, 64, 1e-6)
+    torch.cuda.synchronize()
+    assert bool((k == 1).all()) and bool((v == 1).all())
+
+
+def test_a_tensor_of_another_device_is_refused():
+    import torch
+    x = torch.zeros(4, device="cuda")
+    other = torch.cuda.current_device() + 1
+    for contiguous in (True, False):
+        with pytest.raises(ValueError, match="current device"):
+            vg._arg(x, (torch.float32,), "x", other, contiguous)
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import torch
+import norm_activation_fp8_gb300 as vg
+from test_fp8_gemm_gpu import operands
+from test_rope_append_gpu import inputs, cuda
+sets = [operands(T, N, K, 1, exact=True) for T, N, K in ((1, 1024, 512), (50, 640, 512), (196, 3704, 6912), (600, 8192, 512))]
+d = inputs(20, 4, 2, 128, seed=1)
+args = [cuda(d[n]) for n in ("q_weight", "k_weight", "cos_sin_cache", "positions")]
+qkv, k, v = cuda(d["qkv"]).clone(), *(torch.zeros((2, 16, 2, 128), dtype=torch.int16, device="cuda") for _ in range(2))
+slots = torch.arange(20, device="cuda")
+outs = [torch.zeros((s[0].shape[0], s[2].shape[0]), dtype=torch.bfloat16, device="cuda") for s in sets]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for o, s in zip(outs, sets):
+        vg.vg_fp8_block_gemm(o, *s[:4])
+    vg.vg_fused_qk_norm_rope_append(qkv, k, v, *args, slots, 4, 2, 128, 1e-6)
+g.replay()
+torch.cuda.synchronize()
+for o, s in zip(outs, sets):
+    assert torch.equal(o, (s[4] @ s[5].t()).to(torch.bfloat16))
+assert (v.view(-1, 256)[:20] == cuda(d["qkv"])[:, 768:]).all()
+print("captured first calls ok")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root)], capture_output=True, text=True,
+                       cwd=root, timeout=300)
+    assert p.returncode == 0 and "captured first calls ok" in p.stdout, p.stdout + p.stderr
+
+
+def test_calls_from_several_threads():
+    """Host threads that call at once, each on its own stream."""
+    import threading
+    import torch
+    from test_fp8_gemm_gpu import operands
+    sets = [operands(T, 1024, 1024, T, exact=True) for T in (1, 20, 60, 300, 700, 3)]
+    want = [(x[4] @ x[5].t()).to(torch.bfloat16) for x in sets]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()) as _:
+            outs = [vg.fp8_block_gemm(*sets[i][:4]) for _ in range(50)]
+            torch.cuda.current_stream().synchronize()
+        if not all(torch.equal(o, want[i]) for o in outs):
+            bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def _gemm(T, N, K):
     import torch
     from test_fp8_gemm_gpu import operands

@@ -119,7 +119,7 @@ def mrope(lib, qkv=A, qw=A, kw=A, cache=A, pos=A, sec=(24, 20, 20), axes=3, T=4,
                                       1e-6, 1, inter, None)
 
 
-def append(lib, qkv=A, kc=A, vc=A, qw=A, kw=A, cache=A, pos=A, slots=A, ks=None, vs=None, sec=None,
+def append(lib, qkv=A, kc=A, vc=A + 0x100000, qw=A, kw=A, cache=A, pos=A, slots=A, ks=None, vs=None, sec=None,
            axes=1, T=4, hq=32, hkv=8, D=128, maxp=4096, pages=64, page=16, ps=16 * 1024, ts=1024,
            hs=128, inter=0):
     return lib.vg_fused_qk_norm_rope_append(qkv, kc, vc, qw, kw, cache, pos, slots, ks, vs,
@@ -167,6 +167,7 @@ def test_append_refusals(lib):
     assert append(lib, ps=8 * 1024) == SHAPE                # pages overlap
     assert append(lib, ps=-16 * 1024) == SHAPE
     assert append(lib, ps=2 ** 62) == SHAPE                 # an offset past 64 bits
+    assert append(lib, vc=A) == SHAPE                       # one cache for K and V
     # heads outside tokens, an extent of one with any stride, gaps
     assert append(lib, hs=16 * 128, ts=128, T=0) == OK
     assert append(lib, pages=1, ps=3, T=0) == OK
@@ -177,7 +178,7 @@ def test_append_refusals(lib):
     assert append(lib, qw=None) == NULL and append(lib, kw=None) == NULL
     assert append(lib, ks=A) == NULL and append(lib, vs=A) == NULL
     for k in ("qkv", "kc", "vc", "qw", "kw", "cache"):
-        assert append(lib, **{k: A + 8}) == ALIGN, k
+        assert append(lib, **{k: 2 * A + 8}) == ALIGN, k
     assert append(lib, pos=A + 4) == ALIGN and append(lib, slots=A + 4) == ALIGN
     assert append(lib, ks=A + 2, vs=A) == ALIGN
     assert append(lib, qkv=None, kc=None, vc=None, qw=None, kw=None, cache=None, pos=None,

@@ -79,6 +79,9 @@ SECTIONS = {64: (12, 10, 10), 128: (24, 20, 20), 256: (56, 36, 36)}
     (33, 5, 0, 128, None), (17, 0, 3, 64, None), (9, 150, 5, 64, None),
     (50, 4, 2, 128, (40, 24)), (50, 4, 2, 128, (28, 12, 12, 12)), (50, 4, 2, 128, (64,)),
     (50, 4, 2, 128, (64, 0, 0)), (50, 4, 2, 64, (11, 11, 10)),
+    # many tokens: three heads a lane group, the last groups with fewer or none
+    (640, 32, 8, 128, None), (611, 28, 4, 128, (28, 12, 12, 12)), (700, 1, 1, 64, None),
+    (613, 23, 2, 64, None), (609, 7, 1, 256, None), (650, 0, 5, 128, (64,)), (620, 70, 3, 256, None),
 ])
 def test_mrope(T, hq, hkv, D, sections, interleaved, neox):
     sections = sections or SECTIONS[D]
@@ -186,6 +189,10 @@ def check_append(d, got, slots, T, hq, hkv, D, fp8, norm, neox, page):
     (130, 5, 3, 64, 1, 1, True, False),
     (77, 0, 2, 128, 64, 1, True, True),
     (601, 64, 8, 128, 128, 1, False, True),
+    # many tokens: three heads a lane group, Q, K and V in one warp
+    (640, 32, 8, 128, 16, 1, True, True), (611, 5, 1, 64, 1, 3, True, False),
+    (700, 64, 8, 128, 64, 1, False, True), (609, 3, 2, 256, 96, 3, True, True),
+    (650, 0, 5, 128, 16, 1, False, True), (1201, 28, 4, 128, 128, 3, True, True),
 ])
 def test_append(T, hq, hkv, D, page, axes, norm, neox, fp8, layout):
     sections = SECTIONS[D] if axes == 3 else None
