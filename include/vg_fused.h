@@ -23,6 +23,12 @@
  *   NVFP4 entry points and the per-group scale options (UE8M0,
  *   column-major) below.
  *
+ * Beside them, for the layer around those operations (the pages describe no
+ * such kernels; their own comments define them): the FP8 products that read
+ * the per-group outputs (vg_fp8_block_gemm, vg_fp8_block_gemm_silu_mul_fp8),
+ * rotary positions with several axes (vg_fused_qk_norm_mrope) and the rotation
+ * on the way into a paged key/value cache (vg_fused_qk_norm_rope_append).
+ *
  * Numerics (the pages give no formulas; these are the readings the library
  * implements):
  *   r   = bf16(x + residual)                       (fp32 add, RNE to bf16)
@@ -49,15 +55,16 @@
  *     it reads or writes any memory -- it only asks its first input rows
  *     into L2 before the wait, which cannot return stale data, since L2
  *     also takes every write of the previous kernel -- and signals
- *     griddepcontrol.launch_dependents once its loads are issued, before
- *     q, scale and residual_out are written.  A consumer launched
- *     after it with programmatic dependent launch too must therefore wait
+ *     griddepcontrol.launch_dependents once its loads are issued (a large
+ *     product: at its start), before its outputs are written.  A consumer
+ *     launched after it with programmatic dependent launch too must therefore wait
  *     on the grid dependency (cudaGridDependencySynchronize() or
  *     griddepcontrol.wait) before it reads these outputs; an ordinary
  *     launch, a copy or an event needs nothing extra.
  *   - bf16 tensors are passed as uint16_t bit patterns, fp8 outputs as
  *     uint8_t E4M3 codes.  All tensors are dense and row-major, except the
- *     MLA dual norm's two inputs, which are read through a row stride.
+ *     MLA dual norm's two inputs, which are read through a row stride, and the
+ *     paged caches, which have three strides.
  *   - Every argument is validated on the host before any launch; a
  *     validation error returns its status and launches nothing.  A launch
  *     failure returns VG_ERR_CUDA.  num_tokens == 0 returns VG_OK without
@@ -118,7 +125,8 @@ typedef enum {
     VG_ERR_BAD_MODE = 4,           /* mode is not a vg_scale_mode (with valid
                                       per-group options)                          */
     VG_ERR_BAD_GROUP = 5,          /* per-group with group_size not 64 or 128, or
-                                      not dividing the row length                 */
+                                      not dividing the row length; a product
+                                      whose K (or inter) 128 does not divide      */
     VG_ERR_UNSUPPORTED_DEVICE = 6, /* current device is not compute capability 10.3 */
     VG_ERR_CUDA = 7                /* a CUDA runtime call or launch failed        */
 } vg_status;

@@ -809,7 +809,7 @@ const char *vg_status_string(vg_status s) {
     case VG_ERR_BAD_SHAPE: return "bad shape: num_tokens < 0 or row length not a multiple of 8 in [8, VG_MAX_ROW]";
     case VG_ERR_MISALIGNED: return "misaligned pointer: tensors need 16-byte, scale 4-byte alignment";
     case VG_ERR_BAD_MODE: return "unknown scale mode";
-    case VG_ERR_BAD_GROUP: return "per-group mode needs group_size 64 or 128 dividing the row length";
+    case VG_ERR_BAD_GROUP: return "per-group mode needs group_size 64 or 128 dividing the row length (products: 128 dividing K and inter)";
     case VG_ERR_UNSUPPORTED_DEVICE: return "current device is not compute capability 10.3 (GB300)";
     case VG_ERR_CUDA: return "CUDA runtime or launch error";
   }
