@@ -35,10 +35,9 @@
 // issued, finished, seen by the summing warps, read, given back to the issuing
 // warp) costs 940 cycles without any work in it, and with two accumulators half
 // of that and of the work shows.  Without the sums it runs at 3230, without
-// sums and tensor memory loads at 3470 TFLOP/s.  Shorter accumulators (four of
-// 128 columns) add a wait and a release a block and were slower (2100), a CTA
-// alone 1980, eight summing warps 1760.  Long runs meet the power limit first.
-
+// sums and tensor memory loads at 3470 TFLOP/s.  Products of 128 columns take as
+// long as those of 256, so four shorter accumulators, or one released by halves,
+// are slower (2120); a CTA alone reached 1980, eight summing warps 1760.  Long runs meet the power limit first.
 #include <atomic>
 
 #include "common.cuh"
@@ -141,12 +140,17 @@ __device__ __forceinline__ void store_gated4(const GemmArgs &a, int64_t t, int g
 
 constexpr int kTileT = 128, kTileW = 256;
 constexpr int kTileStages = 5;
-constexpr int kScaleSlots = 8;  // scale blocks staged ahead (stream kernel); a group of the tile kernel's two
+constexpr int kScaleSlots = 8;  // scale blocks staged ahead (stream kernel), a group (tile kernel)
 constexpr int kTileStageBytes = (kTileT + kHalfW) * kBlockK;  // of either CTA
+// Four warps of a scheduler hide each other's tensor memory loads (eight warps
+// of 128 columns a thread: 1760 instead of 1980 TFLOP/s, before the pairs).
 constexpr int kSumWarps = 16, kTileThreads = 128 + 32 * kSumWarps;
 constexpr int kPart = kHalfW * 4 / kSumWarps;  // columns of either half that a thread sums
-// The launch holds 640 x 96 registers; the split hands out 128 x 56 + 512 x 104.
-constexpr int kTileGroup = 16;  // token tiles of a pair that share a sweep over the weight
+// The launch holds 640 x 96 registers; setmaxnreg hands out 128 x 56 + 512 x
+// 104 of them.
+constexpr int kServiceRegs = 56, kSumRegs = 104;
+static_assert(128 * kServiceRegs + 32 * kSumWarps * kSumRegs <= kTileThreads * 96, "register split");
+constexpr int kTileGroup = 16;  // pairs' token tiles that share a sweep over the weight
 
 // Dynamic shared memory (1024-byte aligned).
 template <bool GATED>
@@ -166,9 +170,9 @@ struct TileSmem {
   VG_GEMM_NEVER
 };
 
-// The i-th tile: token tiles run fastest within groups of
-// kTileGroup, so that the tiles in flight share weight rows and the group's
-// activations stay in L2 while the weight streams by.
+// The i-th tile: token tiles run fastest within groups of kTileGroup, so that
+// the tiles in flight share weight rows and the group's activations stay in L2
+// while the weight streams by (groups of 4 and 8: within 5 %).
 struct Tile {
   int t0;  // first token of the pair
   int n;   // weight tile
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint32_t issued = 0;  // stages this CTA has filled (warp 0)
 
   if (warp < 4) {
-    regs_decrease<56>();
+    regs_decrease<kServiceRegs>();
     if (warp == 0) {
       uint32_t it = 0, s = 0, lap = 0;
       bool ok = true;
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint32_t b = it & 1;
           // Operands staged and accumulator free: half of the lanes wait for
           // either (one after the other would put both waits' latencies, some
-          // 200 cycles each even when nothing is left to wait for, before
+          // 130 cycles each even when nothing is left to wait for, before
           // every block's products).
           const bool odd = lane & 1;
           if (!(ok = __all_sync(0xFFFFFFFFu, (odd && it < 2) ||
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       copy_async_wait_all();
     }
   } else {
-    regs_increase<104>();
+    regs_increase<kSumRegs>();
     const int quarter = warp & 3, part = (warp - 4) >> 2;  // lanes, columns of each half
     const int row = quarter * 32 + lane;
     uint8_t *box = sm.out[warp - 4];
