@@ -893,11 +893,11 @@ cudaError_t launch_form(const GemmArgs &a, const GemmPlan &p, int sms, cudaStrea
 //   tile kernel    a wave of pairs: 0.42 per scale block of its share of K, and
 //                  4.4 (one share) .. 9.5 (four) for start, end and the sum of
 //                  the shares
-//   stream kernel  a wave of CTAs: 3.5, and 0.27 (16 tokens) .. 0.48 (128) per
-//                  block of its split or the weight's bytes at 6.3 TB/s (two
-//                  thirds of that again for every further token tile, which
-//                  reads the weight from L2), whichever is longer, with a
-//                  fifth of the other
+//   stream kernel  a wave of CTAs: 3.5 and 0.15 for each CTA of a cluster, and
+//                  0.27 (16 tokens) .. 0.48 (128) per block of its split or the
+//                  weight's bytes at 6.3 TB/s (two thirds of that again for
+//                  every further token tile, which reads the weight from L2),
+//                  whichever is longer, with a fifth of the other
 // Clusters do not fill every SM, and a second wave costs as much as the first
 // (6144 x 4096, one token: five ways, 240 CTAs, 6.5 us; six ways, 288 of 304
 // slots, 10.3 us; 256 x 4096 x 14336 in tiles: three shares, 96 CTAs, 24.9 us,
@@ -937,7 +937,8 @@ GemmPlan plan_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
       const double waves = waves_of(tiles * s, part(slots, big ? 64 : 85));
       const double chain = (double)((blocks + s - 1) / s) * per_block;
       const double traffic = bytes / waves / 6.3e6;
-      const double cost = waves * (3.5 + (chain > traffic ? chain + 0.2 * traffic : traffic + 0.2 * chain));
+      const double fixed = 3.5 + 0.15 * (double)(s * (gated ? 2 : 1));
+      const double cost = waves * (fixed + (chain > traffic ? chain + 0.2 * traffic : traffic + 0.2 * chain));
       if (cost < best) {
         best = cost;
         p.tn = tn;

@@ -110,7 +110,7 @@ GATED = [  # T, I, K
     (17, 128, 128), (33, 1024, 640), (57, 2048, 2048), (64, 384, 32768), (65, 256, 512), (127, 640, 256),
     (128, 128, 384), (129, 1152, 512), (200, 14336, 256), (256, 2048, 1024), (300, 128, 896),
     (513, 1024, 512), (1000, 896, 640), (2049, 2048, 256), (4100, 128, 128),
-    (1738, 384, 18048), (609, 640, 11904), (812, 384, 25728), (22, 1152, 256), (25, 896, 512),
+    (1738, 384, 18048), (609, 640, 11904), (812, 384, 25728), (22, 1152, 256), (25, 896, 512), (25, 256, 9472),
     (83, 23936, 256),
 ]
 
