@@ -348,29 +348,18 @@ def vg_silu_mul_nvfp4(q4, block_scale, gate_up, global_scale, stream=None,
         inter, _stream(stream)))
 
 
+# The calls below check all their tensors in one expression and look for the
+# reason only when it fails (_arg, _shape): on a decode step the host's time
+# for a call is longer than the kernel's.
+
 def _arg(t, dtypes, name, dev, contiguous=True):
-    """Device pointer of a tensor on the current device (or None): one pass of
-    cheap checks, the reasons only when one fails."""
-    if t is None:  # the library refuses a missing one
-        return None
-    if t.dtype in dtypes and t.get_device() == dev and (not contiguous or t.is_contiguous()):
-        return t.data_ptr()
-    if contiguous or t.dtype not in dtypes or not t.is_cuda:
-        _ptr(t if contiguous else t[:0], dtypes, name)
-    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}: call under "
-                     "torch.cuda.device(tensor.device)")
-
-
-def _here(t, stream):
-    """(current device, raw stream) of a call whose tensors should be where ``t`` is; for a CPU
-    tensor a device that no tensor is on."""
-    if t.get_device() < 0:
-        return -2, 0
-    torch = _kinds()[4]
-    dev = torch.cuda.current_device()
-    if stream is None:
-        return dev, torch._C._cuda_getCurrentRawStream(dev)
-    return dev, _stream(stream)
+    """Refuses a tensor that is not of these dtypes, on the device ``dev`` and contiguous."""
+    if not contiguous:
+        t = t[:0]
+    _ptr(t, dtypes, name)
+    if t is not None and t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}: call under "
+                         "torch.cuda.device(tensor.device)")
 
 
 def _shape(t, shape, name):
@@ -383,6 +372,18 @@ def _kinds():
     """(bf16, fp8, fp32, int64 dtypes, torch)"""
     import torch
     return *_dtypes(), (torch.int64,), torch
+
+
+def _here(t, stream):
+    """(current device, raw stream) of a call whose tensors should be where ``t`` is; for a CPU
+    tensor a device that no tensor is on."""
+    if t.get_device() < 0:
+        return -2, 0
+    torch = _kinds()[4]
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, _stream(stream)
 
 
 def _sections(sections, positions):
@@ -401,24 +402,36 @@ def _rope_args(qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_
                num_kv_heads, head_dim, dev):
     """Checked pointers and sizes that the multi-axis and cache forms share."""
     bf16, _, f32, i64, _ = _kinds()
-    T, row = _rows(qkv, "qkv")
-    max_pos, D = _rows(cos_sin_cache, "cos_sin_cache")
-    sec, axes, tokens = _sections(sections, positions)
-    if row != (num_q_heads + 2 * num_kv_heads) * head_dim:
-        raise ValueError("qkv: expected (num_q_heads + 2 num_kv_heads) * head_dim columns")
-    if tokens != T:
-        raise ValueError("positions and qkv must have the same number of tokens")
-    if D != head_dim:
-        raise ValueError("cos_sin_cache: expected head_dim columns")
+    sec, axes, T = _sections(sections, positions)
+    row = (num_q_heads + 2 * num_kv_heads) * head_dim
+    max_pos = cos_sin_cache.shape[0]
+    if (qkv.shape != (T, row) or cos_sin_cache.shape != (max_pos, head_dim)
+            or qkv.dtype not in bf16 or qkv.get_device() != dev or not qkv.is_contiguous()
+            or cos_sin_cache.dtype not in f32 or cos_sin_cache.get_device() != dev
+            or not cos_sin_cache.is_contiguous() or positions.dtype not in i64
+            or positions.get_device() != dev or not positions.is_contiguous()):
+        if _rows(qkv, "qkv")[1] != row:
+            raise ValueError("qkv: expected (num_q_heads + 2 num_kv_heads) * head_dim columns")
+        if qkv.shape[0] != T:
+            raise ValueError("positions and qkv must have the same number of tokens")
+        if _rows(cos_sin_cache, "cos_sin_cache")[1] != head_dim:
+            raise ValueError("cos_sin_cache: expected head_dim columns")
+        _arg(qkv, bf16, "qkv", dev)
+        _arg(cos_sin_cache, f32, "cos_sin_cache", dev)
+        _arg(positions, i64, "positions", dev)
+    qw = kw = None
     if q_weight is not None:
         _shape(q_weight, (head_dim,), "q_weight")
-        q_weight = _arg(q_weight, bf16, "q_weight", dev)
+        if q_weight.dtype not in bf16 or q_weight.get_device() != dev or not q_weight.is_contiguous():
+            _arg(q_weight, bf16, "q_weight", dev)
+        qw = q_weight.data_ptr()
     if k_weight is not None:
         _shape(k_weight, (head_dim,), "k_weight")
-        k_weight = _arg(k_weight, bf16, "k_weight", dev)
-    return (_arg(qkv, bf16, "qkv", dev), q_weight, k_weight,
-            _arg(cos_sin_cache, f32, "cos_sin_cache", dev), _arg(positions, i64, "positions", dev),
-            sec, axes, T, max_pos)
+        if k_weight.dtype not in bf16 or k_weight.get_device() != dev or not k_weight.is_contiguous():
+            _arg(k_weight, bf16, "k_weight", dev)
+        kw = k_weight.data_ptr()
+    return (qkv.data_ptr(), qw, kw, cos_sin_cache.data_ptr(), positions.data_ptr(), sec, axes, T,
+            max_pos)
 
 
 def vg_fused_qk_norm_mrope(qkv, q_weight, k_weight, cos_sin_cache, positions, sections,
@@ -460,41 +473,55 @@ def vg_fused_qk_norm_rope_append(qkv, k_cache, v_cache, q_weight, k_weight, cos_
     q, qw, kw, table, pos, sec, axes, T, max_pos = _rope_args(
         qkv, q_weight, k_weight, cos_sin_cache, positions, sections, num_q_heads, num_kv_heads,
         head_dim, dev)
+    kinds, ks, vs = bf16, None, None
+    if k_scale is not None or v_scale is not None:
+        kinds = fp8
+        for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if x is not None and x.numel() != 1:
+                raise ValueError(f"{name}: expected one fp32 value on the device")
+            _arg(x, f32, name, dev)
+        ks = None if k_scale is None else k_scale.data_ptr()
+        vs = None if v_scale is None else v_scale.data_ptr()
     shape, strides = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or shape[2] != num_kv_heads or shape[3] != head_dim or strides[3] != 1:
         raise ValueError("k_cache: expected [pages, page_size, num_kv_heads, head_dim] with "
                          "contiguous head rows")
     if shape != v_cache.shape or strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    _shape(slots, (T,), "slots")
-    kinds = bf16
-    if k_scale is not None or v_scale is not None:
-        kinds = fp8
-        for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if x is not None and x.numel() != 1:
-                raise ValueError(f"{name}: expected one fp32 value on the device")
-        k_scale, v_scale = _arg(k_scale, f32, "k_scale", dev), _arg(v_scale, f32, "v_scale", dev)
+    if (k_cache.dtype not in kinds or k_cache.get_device() != dev or v_cache.dtype not in kinds
+            or v_cache.get_device() != dev or slots.shape != (T,) or slots.dtype not in i64
+            or slots.get_device() != dev or not slots.is_contiguous()):
+        _arg(k_cache, kinds, "k_cache", dev, False)
+        _arg(v_cache, kinds, "v_cache", dev, False)
+        _shape(slots, (T,), "slots")
+        _arg(slots, i64, "slots", dev)
     st = (_lib or load()).vg_fused_qk_norm_rope_append(
-        q, _arg(k_cache, kinds, "k_cache", dev, False), _arg(v_cache, kinds, "v_cache", dev, False),
-        qw, kw, table, pos, _arg(slots, i64, "slots", dev), k_scale, v_scale, sec, axes, T,
-        num_q_heads, num_kv_heads, head_dim, max_pos, shape[0], shape[1], strides[0], strides[1],
-        strides[2], eps, is_neox, interleaved, raw)
+        q, k_cache.data_ptr(), v_cache.data_ptr(), qw, kw, table, pos, slots.data_ptr(), ks, vs, sec,
+        axes, T, num_q_heads, num_kv_heads, head_dim, max_pos, shape[0], shape[1], strides[0],
+        strides[1], strides[2], eps, is_neox, interleaved, raw)
     if st:
         _check(st)
 
 
-def _block_gemm_args(a, a_scale, w, w_scale, a_options, dev):
-    """Checked pointers and sizes of an FP8 product's operands."""
+def _block_gemm_sizes(a, a_scale, w, w_scale, a_options, dev):
+    """T, N and K of an FP8 product's checked operands."""
     _, fp8, f32, _, _ = _kinds()
-    T, K = _rows(a, "a")
-    N, K2 = _rows(w, "w")
-    if K2 != K:
-        raise ValueError("a and w must have the same number of columns")
-    kb = K // BLOCK
-    _shape(a_scale, (kb, (T + 3) // 4 * 4) if a_options & COLUMN_MAJOR else (T, kb), "a_scale")
-    _shape(w_scale, ((N + BLOCK - 1) // BLOCK, kb), "w_scale")
-    return (_arg(a, fp8, "a", dev), _arg(a_scale, f32, "a_scale", dev), _arg(w, fp8, "w", dev),
-            _arg(w_scale, f32, "w_scale", dev), T, N, K)
+    N, K = _rows(w, "w")
+    T, kb = a.shape[0], K // BLOCK
+    scales = (kb, (T + 3) // 4 * 4) if a_options & COLUMN_MAJOR else (T, kb)
+    if (a.shape != (T, K) or a_scale.shape != scales or w_scale.shape != ((N + BLOCK - 1) // BLOCK, kb)
+            or a.dtype not in fp8 or a.get_device() != dev or not a.is_contiguous()
+            or w.dtype not in fp8 or w.get_device() != dev or not w.is_contiguous()
+            or a_scale.dtype not in f32 or a_scale.get_device() != dev or not a_scale.is_contiguous()
+            or w_scale.dtype not in f32 or w_scale.get_device() != dev or not w_scale.is_contiguous()):
+        if _rows(a, "a")[1] != K:
+            raise ValueError("a and w must have the same number of columns")
+        _shape(a_scale, scales, "a_scale")
+        _shape(w_scale, ((N + BLOCK - 1) // BLOCK, kb), "w_scale")
+        for t, kinds, name in ((a, fp8, "a"), (a_scale, f32, "a_scale"), (w, fp8, "w"),
+                               (w_scale, f32, "w_scale")):
+            _arg(t, kinds, name, dev)
+    return T, N, K
 
 
 def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=None):
@@ -507,14 +534,15 @@ def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=No
     ``out`` None allocates it; returns out."""
     bf16 = _kinds()[0]
     dev, raw = _here(a, stream)
-    pa, psa, pw, psw, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
-    if out is None:  # after the checks: an allocation right behind a launch is slower
+    T, N, K = _block_gemm_sizes(a, a_scale, w, w_scale, a_options, dev)
+    if out is None:
         out = a.new_empty((T, N), dtype=bf16[0])
-        po = out.data_ptr()
-    else:
+    elif (out.shape != (T, N) or out.dtype not in bf16 or out.get_device() != dev
+          or not out.is_contiguous()):
         _shape(out, (T, N), "out")
-        po = _arg(out, bf16, "out", dev)
-    st = (_lib or load()).vg_fp8_block_gemm(po, pa, psa, pw, psw, T, N, K, a_options, raw)
+        _arg(out, bf16, "out", dev)
+    st = (_lib or load()).vg_fp8_block_gemm(out.data_ptr(), a.data_ptr(), a_scale.data_ptr(),
+                                            w.data_ptr(), w_scale.data_ptr(), T, N, K, a_options, raw)
     if st:
         _check(st)
     return out
@@ -532,20 +560,25 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     allocate them; returns (q, scale)."""
     _, fp8, f32, _, _ = _kinds()
     dev, raw = _here(a, stream)
-    pa, psa, pw, psw, T, N, K = _block_gemm_args(a, a_scale, w, w_scale, a_options, dev)
+    T, N, K = _block_gemm_sizes(a, a_scale, w, w_scale, a_options, dev)
     if N % 2:
         raise ValueError("w must have an even number of rows (gate, then up)")
     inter = N // 2
     shape = (inter // BLOCK, (T + 3) // 4 * 4) if out_options & COLUMN_MAJOR else (T, inter // BLOCK)
     if q is None and scale is None:
         q, scale = a.new_empty((T, inter), dtype=fp8[0]), a.new_empty(shape, dtype=f32[0])
-        pq, ps = q.data_ptr(), scale.data_ptr()
-    else:
+    elif (q is None or scale is None or q.shape != (T, inter) or q.dtype not in fp8
+          or q.get_device() != dev or not q.is_contiguous() or scale.shape != shape
+          or scale.dtype not in f32 or scale.get_device() != dev or not scale.is_contiguous()):
+        if q is None or scale is None:
+            raise ValueError("q and scale: give both or neither")
         _shape(q, (T, inter), "q")
+        _arg(q, fp8, "q", dev)
         _shape(scale, shape, "scale")
-        pq, ps = _arg(q, fp8, "q", dev), _arg(scale, f32, "scale", dev)
-    st = (_lib or load()).vg_fp8_block_gemm_silu_mul_fp8(pq, ps, pa, psa, pw, psw, T, inter, K,
-                                                         a_options, out_options, raw)
+        _arg(scale, f32, "scale", dev)
+    st = (_lib or load()).vg_fp8_block_gemm_silu_mul_fp8(
+        q.data_ptr(), scale.data_ptr(), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
+        w_scale.data_ptr(), T, inter, K, a_options, out_options, raw)
     if st:
         _check(st)
     return q, scale

@@ -134,6 +134,18 @@ def test_arguments_on_the_gpu():
         vg.fp8_block_gemm(a[:, :256], sa, w, sw)
     with pytest.raises(TypeError, match="w_scale"):
         vg.fp8_block_gemm(a[:, :256].contiguous(), sa, w, sw.double())
+    with pytest.raises(ValueError, match="both or neither"):
+        vg.vg_fp8_block_gemm_silu_mul_fp8(None, sa, a[:, :256].contiguous(), sa, w, sw)
+    with pytest.raises(ValueError, match="scale"):
+        vg.vg_fp8_block_gemm_silu_mul_fp8(torch.zeros((4, 128), dtype=f8, device="cuda"), sa,
+                                          a[:, :256].contiguous(), sa, torch.cat([w.view(torch.uint8)] * 2),
+                                          torch.cat([sw] * 2))
+    with pytest.raises(TypeError, match="out"):
+        vg.vg_fp8_block_gemm(torch.zeros((4, 128), device="cuda"), a[:, :256].contiguous(), sa, w, sw)
+    with pytest.raises(TypeError, match="a:"):
+        vg.fp8_block_gemm(a[:, :256].float(), sa, w, sw)
+    with pytest.raises(ValueError, match="2-D"):
+        vg.fp8_block_gemm(a[0, :256], sa, w, sw)
     with pytest.raises(ValueError, match="out"):
         vg.vg_fp8_block_gemm(torch.zeros((4, 64), device="cuda").bfloat16(), a[:, :256].contiguous(), sa, w, sw)
     with pytest.raises(ValueError, match="CUDA"):
