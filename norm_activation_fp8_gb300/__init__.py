@@ -532,11 +532,11 @@ def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=No
     a_options, [K/128,T4] as the per-group ops write it); w [N,K] fp8 with
     w_scale fp32 [ceil(N/128),K/128].  UE8M0 scales need no option.
     ``out`` None allocates it; returns out."""
-    bf16 = _kinds()[0]
+    bf16, _, _, _, torch = _kinds()
     dev, raw = _here(a, stream)
     T, N, K = _block_gemm_sizes(a, a_scale, w, w_scale, a_options, dev)
     if out is None:
-        out = a.new_empty((T, N), dtype=bf16[0])
+        out = torch.empty((T, N), dtype=bf16[0], device=a.device)
     elif (out.shape != (T, N) or out.dtype not in bf16 or out.get_device() != dev
           or not out.is_contiguous()):
         _shape(out, (T, N), "out")
@@ -558,7 +558,7 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     [T,I/128], or with COLUMN_MAJOR in out_options [I/128,T4]; UE8M0 in
     out_options: power-of-two scales.  ``q`` and ``scale`` both None
     allocate them; returns (q, scale)."""
-    _, fp8, f32, _, _ = _kinds()
+    _, fp8, f32, _, torch = _kinds()
     dev, raw = _here(a, stream)
     T, N, K = _block_gemm_sizes(a, a_scale, w, w_scale, a_options, dev)
     if N % 2:
@@ -566,7 +566,8 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     inter = N // 2
     shape = (inter // BLOCK, (T + 3) // 4 * 4) if out_options & COLUMN_MAJOR else (T, inter // BLOCK)
     if q is None and scale is None:
-        q, scale = a.new_empty((T, inter), dtype=fp8[0]), a.new_empty(shape, dtype=f32[0])
+        q = torch.empty((T, inter), dtype=fp8[0], device=a.device)
+        scale = torch.empty(shape, dtype=f32[0], device=a.device)
     elif (q is None or scale is None or q.shape != (T, inter) or q.dtype not in fp8
           or q.get_device() != dev or not q.is_contiguous() or scale.shape != shape
           or scale.dtype not in f32 or scale.get_device() != dev or not scale.is_contiguous()):
