@@ -169,6 +169,52 @@ def test_outputs_past_32_bit_offsets(T, N, K):
         assert torch.equal(sc[rows], few[1])
 
 
+def test_weights_and_activations_past_32_bit_offsets():
+    """A weight, then activations, of more than 2^32 codes; rows sampled."""
+    import torch
+    K = 32768
+    for T, N in ((3, 131080), (131080, 16)):
+        big = max(T, N)
+        g = torch.Generator(device="cuda").manual_seed(T)
+        base = torch.randint(-2, 3, (997, K), generator=g, device="cuda").to(torch.float8_e4m3fn)
+        many = base.view(torch.uint8).repeat(big // 997 + 1, 1)[:big].view(torch.float8_e4m3fn)
+        few = torch.randint(-2, 3, (min(T, N), K), generator=g, device="cuda").to(torch.float8_e4m3fn)
+        a, w = (few, many) if T < N else (many, few)
+        sa = 2.0 ** torch.randint(-1, 2, (T, K // BLOCK), generator=g, device="cuda").float()
+        sw = 2.0 ** torch.randint(-1, 2, ((N + 127) // 128, K // BLOCK), generator=g, device="cuda").float()
+        out = vg.fp8_block_gemm(a, sa, w, sw)
+        at = torch.tensor([0, 127, 65535, 65536, 65537, 131071, 131072, big - 1], device="cuda")
+        rows = torch.arange(T, device="cuda") if T < N else at
+        cols = at if T < N else torch.arange(N, device="cuda")
+        A = a.view(torch.uint8)[rows].view(torch.float8_e4m3fn).double() * sa[rows].double().repeat_interleave(BLOCK, 1)
+        W = w.view(torch.uint8)[cols].view(torch.float8_e4m3fn).double()
+        W = W * sw[cols // BLOCK].double().repeat_interleave(BLOCK, 1)
+        assert torch.equal(out[rows][:, cols], (A @ W.t()).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_infinite_scales_follow_ieee_arithmetic(T):
+    """An infinite token scale: its row is infinite or NaN where the products
+    say so; the others do not notice.  Gated: infinite activations give the
+    group an infinite scale and NaN codes there, zeros beside them."""
+    import torch
+    N, K = 256, 256
+    a, s, w, sw, A, W = operands(T, N, K, 8, exact=True)
+    t = T // 2
+    s2 = s.clone()
+    s2[t, 1] = float("inf")
+    out, ref = vg.fp8_block_gemm(a, s2, w, sw), vg.fp8_block_gemm(a, s, w, sw)
+    part = a[t, BLOCK:].double() @ w[:, BLOCK:].double().t()  # inf * part, then + finite
+    want = torch.where(part == 0, float("nan"), part.sign() * float("inf")).float()
+    assert torch.equal(out[t].float().nan_to_num(7.0, 8.0, 9.0), want.nan_to_num(7.0, 8.0, 9.0))
+    keep = torch.arange(T, device="cuda") != t
+    assert torch.equal(out[keep], ref[keep])
+    q, sc = vg.fp8_block_gemm_silu_mul_fp8(a, s2, w, sw)
+    q0, sc0 = vg.fp8_block_gemm_silu_mul_fp8(a, s, w, sw)
+    assert torch.equal(q.view(torch.uint8)[keep], q0.view(torch.uint8)[keep]) and torch.equal(sc[keep], sc0[keep])
+    assert not bool(torch.isfinite(sc[t]).all()) or bool((q[t].view(torch.uint8) & 0x7F == 0x7F).any())
+
+
 def test_gated_zero_rows_and_saturated_gates():
     """A zero token: zero codes under the floor scale.  Gates far on either
     side: silu(g) = g, or -0."""
