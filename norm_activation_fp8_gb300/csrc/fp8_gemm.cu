@@ -140,7 +140,7 @@ __device__ __forceinline__ void store_gated4(const GemmArgs &a, int64_t t, int g
 
 constexpr int kTileT = 128, kTileW = 256;
 constexpr int kTileStages = 5;
-constexpr int kScaleSlots = 8;  // scale blocks staged ahead (stream kernel), a group (tile kernel)
+constexpr int kScaleSlots = 8;  // scale blocks staged ahead
 constexpr int kTileStageBytes = (kTileT + kHalfW) * kBlockK;  // of either CTA
 // Four warps of a scheduler hide each other's tensor memory loads (eight warps
 // of 128 columns a thread: 1760 instead of 1980 TFLOP/s, before the pairs).
@@ -366,10 +366,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tcgen05_fence_after();
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + b * kTileW + part * kPart;
         uint32_t v[kPart];
-        tmem_load32(base, v);
+        tmem_load(base, v);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (h > 0) tmem_load32(base + kHalfW, v);
+          if (h > 0) tmem_load(base + kHalfW, v);
           const float sh = s * (h ? w.y : w.x);
           const float2 sc = make_float2(sh, sh);
           tmem_load_wait(v);
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // in shared memory and the cluster adds them in a fixed order, every CTA some
 // of the tokens, a warp a token: for the gated form the two CTAs of a scale
 // group (64 columns each) meet there too.
-//   warp 0: TMA   warp 1: products   warp 2: scales   warps 4-7: sums
+//   warp 0: TMA   warp 1: products   warp 2: scales   warps from 4 on: sums
 // Up to 64 tokens two CTAs share an SM (each asks for more than a third of its
 // shared memory and for at most half of its tensor memory, so no allocation
 // ever waits).
@@ -522,15 +522,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // 8192 gated 86 us (0.80: 448 CTAs are a wave and a half).  Small products are
 // bound by a call's fixed 3.5 us (6144 x 4096, one token: 6.5 us, 0.57).
 
-constexpr int kStreamThreads = 256;
 constexpr int kMaxSplit = 8;
+
+// Warps that sum: four, or for 128 tokens eight of 64 tokens each, over four
+// accumulators (four warps took longer for a block's sums than its products do:
+// 100 x 4096 x 14336 18.4 -> 17.5 us, 128 x 8192 x 8192 21.3 -> 20.0).
+template <int TN>
+constexpr int kStreamSums = TN <= 64 ? 4 : 8;
+template <int TN>
+constexpr int kStreamThreads = 128 + 32 * kStreamSums<TN>;
 
 template <int TN>
 struct StreamSmem {
   static constexpr int kStageBytes = (kHalfW + TN) * kBlockK;
   static constexpr int kStages = TN <= 32 ? 5 : (TN == 64 ? 4 : 6);
-  static constexpr int kBufs = TN <= 64 ? 4 : 2;  // accumulators
-  static constexpr int kColumns = kBufs * TN;     // of tensor memory
+  static constexpr int kBufs = 4;              // accumulators
+  static constexpr int kColumns = kBufs * TN;  // of tensor memory
   union {
     uint8_t stage[kStages][kStageBytes];
     float part[TN][kHalfW];  // partial sums, once the products are done
@@ -545,7 +552,7 @@ struct StreamSmem {
 };
 
 template <bool GATED, int TN>
-__global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(kStreamThreads<TN>, TN <= 64 ? 2 : 1)
     fp8_gemm_stream_kernel(const GemmArgs a, const __grid_constant__ GemmMaps maps, int splits,
                            bool w_once) {
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -571,11 +578,11 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&sm.acc_full[i], 1);
-      mbar_init(&sm.acc_empty[i], 4);
+      mbar_init(&sm.acc_empty[i], kStreamSums<TN>);
     }
     for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(&sm.scale_full[i], 32);
-      mbar_init(&sm.scale_empty[i], 4);
+      mbar_init(&sm.scale_empty[i], kStreamSums<TN>);
     }
     mbar_init(&sm.drain, 1);
     VG_GEMM_NEVER_INIT(sm);
@@ -667,57 +674,54 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
     }
     copy_async_wait_all();
   } else if (warp >= 4) {
-    const int quarter = warp & 3, row = quarter * 32 + lane;
-    float2 acc[TN / 2];
+    constexpr int kCols = TN * 4 / kStreamSums<TN>;  // tokens a thread sums
+    const int quarter = warp & 3, row = quarter * 32 + lane, col0 = (warp - 4) / 4 * kCols;
+    float2 acc[kCols / 2];
 #pragma unroll
-    for (int j = 0; j < TN / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+    for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
     for (int kb = k0; kb < k1; ++kb) {
-      const int it = kb - k0, b = it % kBufs, ss = it % kScaleSlots;
-      const bool odd = lane & 1;
-      if (!warp_wait_phase(odd ? &sm.scale_full[ss] : &sm.acc_full[b],
+      const int it = kb - k0, b = it % kBufs, x = it % kScaleSlots;
+      const bool odd = lane & 1;  // half of the lanes wait for either barrier
+      if (!warp_wait_phase(odd ? &sm.scale_full[x] : &sm.acc_full[b],
                            (odd ? it / kScaleSlots : it / kBufs) & 1, &sm.failed))
         break;
       tcgen05_fence_after();
-      const float w = sm.sw[ss][quarter >> 1];
-      const float2 w2 = make_float2(w, w);
-      constexpr int kLoad = TN < 32 ? TN : 32;
+      constexpr int kLoad = TN == 128 ? 32 : 16;  // (32 would spill at two CTAs an SM)
 #pragma unroll
-      for (int c = 0; c < TN / kLoad; ++c) {
+      for (int c = 0; c < kCols / kLoad; ++c) {
         uint32_t v[kLoad];
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + b * TN + c * kLoad;
-        if constexpr (kLoad == 16) {
-          tmem_load16(at, v);
-        } else {
-          tmem_load32(at, v);
-          tmem_load_wait(v);
-        }
-        float4 sa[kLoad / 4];
+        tmem_load(tmem + ((uint32_t)(quarter * 32) << 16) + b * TN + col0 + c * kLoad, v);
+        const float w = sm.sw[x][quarter >> 1];  // while the sums are on their way
+        const float2 w2 = make_float2(w, w);
+        float2 s[kLoad / 2];
 #pragma unroll
-        for (int j = 0; j < kLoad / 4; ++j)
-          sa[j] = *reinterpret_cast<const float4 *>(&sm.sa[ss][c * kLoad + 4 * j]);
-        if (c == TN / kLoad - 1) {  // all read
+        for (int j = 0; j < kLoad / 4; ++j) {
+          const float4 sa = *reinterpret_cast<const float4 *>(&sm.sa[x][col0 + c * kLoad + 4 * j]);
+          s[2 * j] = f2_mul(make_float2(sa.x, sa.y), w2);
+          s[2 * j + 1] = f2_mul(make_float2(sa.z, sa.w), w2);
+        }
+        tmem_load_wait(v);
+        if (c == kCols / kLoad - 1) {  // all read
           tcgen05_fence_before();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&sm.acc_empty[b]);
-            mbar_arrive(&sm.scale_empty[ss]);
+            mbar_arrive(&sm.scale_empty[x]);
           }
         }
 #pragma unroll
-        for (int j = 0; j < kLoad / 4; ++j) {
-          const float2 s0 = f2_mul(make_float2(sa[j].x, sa[j].y), w2), s1 = f2_mul(make_float2(sa[j].z, sa[j].w), w2);
-          float2 &x = acc[c * kLoad / 2 + 2 * j], &y = acc[c * kLoad / 2 + 2 * j + 1];
-          x = f2_fma(make_float2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), s0, x);
-          y = f2_fma(make_float2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), s1, y);
+        for (int j = 0; j < kLoad / 2; ++j) {
+          float2 &y = acc[c * kLoad / 2 + j];
+          y = f2_fma(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), s[j], y);
         }
       }
     }
     // The last block's products are done, so nothing reads the stages.
     if (!sm.failed) {
 #pragma unroll
-      for (int j = 0; j < TN / 2; ++j) {
-        sm.part[2 * j][row] = acc[j].x;
-        sm.part[2 * j + 1][row] = acc[j].y;
+      for (int j = 0; j < kCols / 2; ++j) {
+        sm.part[col0 + 2 * j][row] = acc[j].x;
+        sm.part[col0 + 2 * j + 1][row] = acc[j].y;
       }
     }
   }
@@ -734,7 +738,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
   if (warp == 1) tmem_dealloc<false>(tmem, Smem::kColumns);
 
   const int tokens = min(TN, a.T - t0);
-  for (int j = rank + warp * ctas; j < tokens; j += (kStreamThreads / 32) * ctas) {
+  for (int j = rank + warp * ctas; j < tokens; j += kStreamThreads<TN> / 32 * ctas) {
     const int64_t t = t0 + j;
     if constexpr (!GATED) {
       float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -868,7 +872,7 @@ cudaError_t launch_stream(const GemmArgs &a, int splits, cudaStream_t s) {
   // -> 11.8; 25 MB, which stays in L2 from call to call: 6.4 -> 6.8).
   const bool w_once = a.T <= TN && (GATED ? 2 : 1) * (int64_t)a.N * a.K > 32 << 20;
   const dim3 grid((unsigned)((a.N + kHalfW - 1) / kHalfW * ctas), (unsigned)((a.T + TN - 1) / TN));
-  return launch_pdl_cluster(fp8_gemm_stream_kernel<GATED, TN>, grid, ctas, dim3(kStreamThreads),
+  return launch_pdl_cluster(fp8_gemm_stream_kernel<GATED, TN>, grid, ctas, dim3(kStreamThreads<TN>),
                             sizeof(StreamSmem<TN>), s, a, maps, splits, w_once);
 }
 
@@ -894,7 +898,7 @@ cudaError_t launch_form(const GemmArgs &a, const GemmPlan &p, int sms, cudaStrea
 //                  4.4 (one share) .. 9.5 (four) for start, end and the sum of
 //                  the shares
 //   stream kernel  a wave of CTAs: 3.5 and 0.15 for each CTA of a cluster, and
-//                  0.27 (16 tokens) .. 0.48 (128) per block of its split or the
+//                  0.27 (16 tokens) .. 0.44 (128) per block of its split or the
 //                  weight's bytes at 6.3 TB/s (two thirds of that again for
 //                  every further token tile, which reads the weight from L2),
 //                  whichever is longer, with a fifth of the other
@@ -930,7 +934,7 @@ GemmPlan plan_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
     const int64_t token_tiles = (T + tn - 1) / tn, tiles = rows * token_tiles;
     if (token_tiles > 65535) continue;
     const int64_t slots = (int64_t)sms * (tn <= 64 ? 2 : 1);
-    const double per_block = tn <= 32 ? 0.27 : (tn == 64 ? 0.36 : 0.48);
+    const double per_block = tn <= 32 ? 0.27 : (tn == 64 ? 0.36 : 0.44);
     const double bytes = (double)rows * kHalfW * (double)K * (1.0 + (double)(token_tiles - 1) * 2.0 / 3.0);
     for (int s = 1; s <= (gated ? kMaxSplit / 2 : kMaxSplit) && s <= blocks; s *= 2) {
       const bool big = tn == 128 && s * (gated ? 2 : 1) == 8;  // eight SMs a cluster
