@@ -285,3 +285,104 @@ def test_append_captured_and_replayed():
         graph.replay()
         got = qkv.cpu().numpy().view(np.uint16), before, (k.cpu().numpy(), v.cpu().numpy())
         check_append(e, got, np.arange(T) + shift, T, hq, hkv, D, False, True, True, page)
+
+
+def with_infinities(d, hq, hkv, D, seed):
+    """d with infinities of either sign in Q, K and V heads, alone in a pair and
+    on both sides of it, some at position 0, whose sines are zero."""
+    rng = np.random.default_rng(seed)
+    T, heads = d["qkv"].shape[0], hq + 2 * hkv
+    x = d["qkv"].copy().reshape(T, heads, D)
+    for n in range(6 * heads):
+        t, h, i = rng.integers(T), n % heads, rng.integers(D // 2)
+        kind = n // heads % 3  # one side of a neox pair, of a gptj pair, both sides of both
+        at = ((i, i), (2 * i, 2 * i), (i, i + D // 2, i ^ 1))[kind]
+        x[t, h, list(at)] = np.where(rng.random(len(at)) < 0.5, 0x7F80, 0xFF80)
+    d["qkv"] = x.reshape(T, -1)
+    d["positions"][::3] = 0
+    d["token_table"] = d["cos_sin_cache"][d["positions"]]
+    return d
+
+
+def near_codes(codes, q):
+    """Every code is q's, or its neighbour where q lies within 2^-19 of their
+    midpoint: the rotation is off by at most 2 ulps (2^-22), the reciprocal and
+    the product by half an ulp each (2^-24).  No cap on the neighbours' number:
+    at position 0 K passes unchanged, and bf16 values as common as 0.5 lie at
+    0.5 / fp32(0.02) = 25 (1 + 2.2e-8), beside the midpoint of 24 and 26."""
+    want = oracle.e4m3_encode(q).reshape(q.shape)
+    at = codes != want
+    a, b, v = codes[at], want[at], np.abs(q[at])
+    assert ((a & 0x80) == (b & 0x80)).all() and (np.abs((a & 0x7F).astype(int) - (b & 0x7F)) == 1).all()
+    mid = (np.abs(oracle.e4m3_decode(a).astype(np.float64)) + np.abs(oracle.e4m3_decode(b))) / 2
+    assert (np.abs(v - mid) <= 2.0 ** -19 * mid).all()
+
+
+@pytest.mark.parametrize("neox", [True, False], ids=["neox", "gptj"])
+@pytest.mark.parametrize("T,hq,hkv,D", [(40, 4, 2, 128), (170, 3, 1, 64), (700, 5, 2, 128), (650, 2, 1, 256)])
+def test_infinities_without_a_norm_follow_the_formula(T, hq, hkv, D, neox):
+    """x = inf: a c - b s is that infinity, NaN only where IEEE arithmetic says
+    so (inf - inf, inf * 0), and an FP8 cache saturates it as it does V's."""
+    d = with_infinities(inputs(T, hq, hkv, D, seed=T), hq, hkv, D, T)
+    with np.errstate(invalid="ignore"):
+        out, o = turned(d, hq, hkv, D, neox, False)
+    assert np.isinf(o).any() and np.isnan(o).any()
+
+    def check(bits, want, exact, what):
+        v = oracle.bf16_decode(bits).astype(np.float64)
+        assert np.array_equal(np.isnan(v), np.isnan(exact)), what
+        inf = np.isinf(exact)
+        assert np.array_equal(v[inf], exact[inf]), what
+        ok = np.isfinite(exact)
+        parity.compare_bf16(bits[ok], want[ok], exact[ok], what)
+
+    qkv = cuda(d["qkv"]).clone()
+    vg.vg_fused_qk_norm_mrope(qkv, None, None, cuda(d["cos_sin_cache"]), cuda(d["positions"][None]), (D // 2,),
+                              hq, hkv, D, EPS, neox)
+    g = qkv.cpu().numpy().view(np.uint16)
+    n = (hq + hkv) * D
+    check(g[:, :n], out[:, :n], o, "in place")
+    assert np.array_equal(g[:, n:], d["qkv"][:, n:])
+    slots = np.arange(T, dtype=np.int64)
+    for fp8 in (False, True):
+        g, _, (k, v) = run_append(d, T, hq, hkv, D, fp8, False, neox, None, False, "heads", 16, slots, T // 16 + 1)
+        k, v = (x.reshape(-1, hkv * D)[:T] for x in (k, v))
+        check(g[:, :hq * D], out[:, :hq * D], o[:, :hq * D], "q heads")
+        ko, vbits = o[:, hq * D:], d["qkv"][:, n:]
+        if not fp8:
+            check(k.view(np.uint16), out[:, hq * D:n], ko, "k cache")
+            assert np.array_equal(v.view(np.uint16), vbits)
+            continue
+        for codes, value, s in ((k, ko, 0.02), (v, oracle.bf16_decode(vbits).astype(np.float64), 0.015)):
+            assert np.array_equal(codes & 0x7F == 0x7F, np.isnan(value))
+            assert (codes[value == np.inf] == 0x7E).all() and (codes[value == -np.inf] == 0xFE).all()
+            ok = np.isfinite(value)
+            near_codes(codes[ok], value[ok] / float(np.float32(s)))
+    assert vg.vg_device_status() == 0
+
+
+@pytest.mark.parametrize("neox", [True, False], ids=["neox", "gptj"])
+@pytest.mark.parametrize("T", [30, 640])
+def test_infinities_under_a_norm(T, neox):
+    """x = inf makes its head's mean square infinite and 1 / rms zero: NaN in
+    the pairs that hold it, zeros beside them, other heads as they are."""
+    hq, hkv, D = 4, 2, 128
+    clean = inputs(T, hq, hkv, D, seed=T)
+    d = with_infinities(inputs(T, hq, hkv, D, seed=T), hq, hkv, D, T)
+    x = oracle.bf16_decode(d["qkv"]).reshape(T, -1, D)[:, :hq + hkv]
+    inf = np.isinf(x)
+    pair = inf | (np.roll(inf, D // 2, -1) if neox else inf[..., np.arange(D) ^ 1])
+    hit = inf.any(-1)
+    clean["positions"] = d["positions"]
+    qkv, ref = cuda(d["qkv"]).clone(), cuda(clean["qkv"]).clone()
+    w = cuda(d["q_weight"]), cuda(d["k_weight"]), cuda(d["cos_sin_cache"])
+    for q in (qkv, ref):
+        vg.vg_fused_qk_norm_mrope(q, *w, cuda(d["positions"][None]), (D // 2,), hq, hkv, D, EPS, neox)
+    plain = cuda(d["qkv"]).clone()
+    vg.vg_fused_qk_norm_rope(plain, *w, cuda(d["positions"]), hq, hkv, D, EPS, neox)
+    for out in (qkv, plain):
+        v = oracle.bf16_decode(out.cpu().numpy().view(np.uint16)).reshape(T, -1, D)[:, :hq + hkv]
+        r = oracle.bf16_decode(ref.cpu().numpy().view(np.uint16)).reshape(T, -1, D)[:, :hq + hkv]
+        assert np.array_equal(np.isnan(v), pair)
+        assert (v[hit[..., None] & ~pair] == 0).all()
+        assert np.array_equal(v[~hit], r[~hit])
