@@ -23,7 +23,7 @@
 // the exact result, and its bf16 differs from the correctly rounded one only
 // where the exact value lies that close to a bf16 midpoint, by one ulp.
 //
-// Two further forms of the same kernel.  AXES: pair i turns by the position
+// Two further forms, in a kernel of their own.  AXES: pair i turns by the position
 // on its axis, positions[axis(i), t]; each lane takes its pairs' values from
 // the rows of their axes (measured against a row put together in shared
 // memory once per CTA: its barrier couples the warps, 16411 tokens of 32 + 8
@@ -48,6 +48,13 @@ __device__ uint32_t g_rope_status;
 
 namespace {
 
+__device__ __forceinline__ void load8f(const float *p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
 __device__ __forceinline__ void load4f(const float *p, float (&v)[8], int at) {
   const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
   v[at] = a.x; v[at + 1] = a.y; v[at + 2] = a.z; v[at + 3] = a.w;
@@ -65,6 +72,120 @@ __device__ __forceinline__ float2 kahan2x(float2 a, float2 c, float2 nb, float2 
   const float2 o = f2_add(f, e);
   return make_float2(e.x != 0.f && !(INF && isnan(o.x)) ? o.x : f.x,
                      e.y != 0.f && !(INF && isnan(o.y)) ? o.y : f.y);
+}
+
+// The plain form, in place: one head a lane group, weights and one axis.  A
+// kernel of its own: as an instance of the one below its gptj rotation took 3 %
+// longer (32768 tokens of 32 + 8 heads 108.2 us against 104.7; 4096 tokens 15.4
+// against 14.8; neox alike).
+template <int G, bool NEOX>
+__global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
+  constexpr int D = G * 16;
+  const int lane = threadIdx.x & 31;
+  const int l = lane & (G - 1);
+  const int64_t t = blockIdx.x;
+  const int h = ((int)blockIdx.y * (int)(blockDim.x >> 5) + (int)(threadIdx.x >> 5)) * (32 / G) + lane / G;
+  // Launched with programmatic dependent launch: nothing in global memory
+  // before the previous grid has finished, except that the CTA's heads are
+  // asked into L2 first; the next grid may be scheduled once the loads are out.
+  if (threadIdx.x == 0 && (int)blockIdx.x < a.pf_ctas) {
+    const int h0 = (int)blockIdx.y * (int)(blockDim.x >> 5) * (32 / G);
+    const int nh = a.nh - h0 < (int)(blockDim.x >> 5) * (32 / G) ? a.nh - h0 : (int)(blockDim.x >> 5) * (32 / G);
+    prefetch_l2(a.qkv + t * a.row + (int64_t)h0 * D, 2u * (uint32_t)(nh * D));
+  }
+  pdl_wait();
+  // The head's loads do not depend on the token's position, so they go out
+  // together with it (a head with a bad position is loaded but not stored);
+  // only the cos/sin row waits for the position.
+  const bool in_head = h < a.nh;
+  uint16_t *head = a.qkv + t * a.row + (in_head ? (int64_t)h * D : 0);
+  const uint16_t *w = h < a.hq ? a.qw : a.kw;
+  const int64_t pos = a.pos[t];
+  // chunk 0 of the lane: l (first half of the head), chunk 1: l + G
+  const uint4 xa = in_head ? ld_stream(head + l * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
+  const uint4 xb = in_head ? ld_stream(head + (l + G) * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
+  const uint4 wa = in_head ? ld_keep(w + l * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
+  const uint4 wb = in_head ? ld_keep(w + (l + G) * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
+  const bool live = in_head && pos >= 0 && pos < a.max_pos;  // same for the head's lanes
+  if (in_head && !live && l == 0) atomicOr(&g_rope_status, kErrBadPosition);
+  pdl_launch_dependents();
+  float2 ta[4], tb[4];
+  float cmax;
+  RowAcc acc;
+  pass1_chunk<false, false>(xa, xa, wa, ta, cmax, acc);
+  pass1_chunk<false, false>(xb, xb, wb, tb, cmax, acc);
+  float ss = acc.ss.x + acc.ss.y;
+#pragma unroll
+  for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+  const float y = rsqrtf(fmaf(ss, 1.0f / (float)D, a.eps));
+
+  // mine[0..7]: chunk 0, mine[8..15]: chunk 1; other: each element's pair
+  // partner; c, s: its pair's cos and sin; submask bit k: minus sign
+  float mine[16], other[16], c[16], s[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    mine[2 * i] = ta[i].x;
+    mine[2 * i + 1] = ta[i].y;
+    mine[8 + 2 * i] = tb[i].x;
+    mine[8 + 2 * i + 1] = tb[i].y;
+  }
+  const float *cs = a.cache + (live ? pos * D : 0);
+  uint32_t submask;
+  if (NEOX) {  // element k of chunk 0 pairs with element k of chunk 1: pair 8l + k
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      other[k] = mine[8 + k];
+      other[8 + k] = mine[k];
+    }
+    float c8[8] = {}, s8[8] = {};
+    if (live) {
+      load8f(cs + 8 * l, c8);
+      load8f(cs + D / 2 + 8 * l, s8);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      c[k] = c[8 + k] = c8[k];
+      s[k] = s[8 + k] = s8[k];
+    }
+    submask = 0x00FFu;
+  } else {  // pairs (2i, 2i + 1) inside each chunk: pair 4 chunk + k / 2
+#pragma unroll
+    for (int k = 0; k < 16; ++k) other[k] = mine[k ^ 1];
+    float c4[8] = {}, s4[8] = {};
+    if (live) {
+      load4f(cs + 4 * l, c4, 0);
+      load4f(cs + 4 * (l + G), c4, 4);
+      load4f(cs + D / 2 + 4 * l, s4, 0);
+      load4f(cs + D / 2 + 4 * (l + G), s4, 4);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      c[k] = c4[k >> 1];
+      s[k] = s4[k >> 1];
+    }
+    submask = 0x5555u;
+  }
+
+  float p[16];
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) {
+    const bool m0 = (submask >> k) & 1u, m1 = (submask >> (k + 1)) & 1u;
+    const float2 o = kahan2x<false>(make_float2(mine[k], mine[k + 1]), make_float2(c[k], c[k + 1]),
+                             make_float2(m0 ? -other[k] : other[k], m1 ? -other[k + 1] : other[k + 1]),
+                             make_float2(s[k], s[k + 1]));
+    const float2 pp = f2_mul(o, make_float2(y, y));
+    p[k] = pp.x;
+    p[k + 1] = pp.y;
+  }
+  const uint4 oa = make_uint4(pack_bf16x2_rn(p[0], p[1]), pack_bf16x2_rn(p[2], p[3]),
+                              pack_bf16x2_rn(p[4], p[5]), pack_bf16x2_rn(p[6], p[7]));
+  const uint4 ob = make_uint4(pack_bf16x2_rn(p[8], p[9]), pack_bf16x2_rn(p[10], p[11]),
+                              pack_bf16x2_rn(p[12], p[13]), pack_bf16x2_rn(p[14], p[15]));
+  [[maybe_unused]] const uint64_t bytes = VG_ROWS(a.T) * 2ull * (uint64_t)a.row;
+  if (live && VG_ACCESS_OK(g_rope_status, head + l * kElemsPerChunk, 16, a.qkv, bytes))
+    st_stream(head + l * kElemsPerChunk, oa);
+  if (live && VG_ACCESS_OK(g_rope_status, head + (l + G) * kElemsPerChunk, 16, a.qkv, bytes))
+    st_stream(head + (l + G) * kElemsPerChunk, ob);
 }
 
 // Eight fp32 values (in registers: every index is a constant) as bf16, as
@@ -129,19 +250,19 @@ __device__ __forceinline__ void cache_store(const QkArgs &a, void *cache, int64_
   cache_put<MANY>(a, cache, o + 8 * (l + g), cb);
 }
 
-// H: heads that a lane group takes, one after the other; their loads go out
-// together and they share the token's position, slot and cos/sin values.  The
-// plain form takes one.  The two further forms, whose per-token work is larger,
-// take one for few tokens (the shortest chain: a token 1.8 us against 2.5) and
-// three for many (16411 tokens of 32 + 8 heads with three axes: 80, 57, 55, 55
-// us with one to four; 32768 tokens into a bf16 cache: 171, 140, 122, 124 us,
-// the copy rate; 8191 tokens of 64 + 8 heads into an FP8 cache: 66, 59, 56, 54).
+// The multi-axis and cache forms.  H: heads that a lane group takes, one after
+// the other; their loads go out together and they share the token's position,
+// slot and cos/sin values.  One for few tokens (the shortest chain: a token 1.8
+// us against 2.5) and three for many (16411 tokens of 32 + 8 heads with three
+// axes: 80, 57, 55, 55 us with one to four; 32768 tokens into a bf16 cache: 171,
+// 140, 122, 124 us, the copy rate; 8191 tokens of 64 + 8 heads into an FP8
+// cache: 66, 59, 56, 54; gptj with one to three: 80, 58, 56; 170, 133, 121; 66,
+// 55, 52).
 constexpr int kManyHeads = 3;
 
 template <int G, bool NEOX, bool AXES, bool APPEND, int H>
-__global__ void __launch_bounds__(512, AXES || APPEND ? 2 : 3) qk_norm_rope_kernel(const QkArgs a) {
+__global__ void __launch_bounds__(512, 2) qk_norm_rope_form_kernel(const QkArgs a) {
   constexpr int D = G * 16, kPerWarp = 32 / G;
-  constexpr bool kPlain = !AXES && !APPEND;  // every head has a norm
   const int lane = threadIdx.x & 31;
   const int l = lane & (G - 1);
   const int64_t t = blockIdx.x;
@@ -163,7 +284,7 @@ __global__ void __launch_bounds__(512, AXES || APPEND ? 2 : 3) qk_norm_rope_kern
   const int64_t pos = AXES ? 0 : a.pos[t];
   const int64_t slot = APPEND ? a.slots[t] : 0;
   // chunk 0 of the lane: l (first half of the head), chunk 1: l + G
-  uint4 xa[H], xb[H], wa[H], wb[H];
+  uint4 xa[H], xb[H];
 #pragma unroll
   for (int k = 0; k < H; ++k) {
     const int h = h0 + lane / G + k * kPerWarp;
@@ -171,11 +292,6 @@ __global__ void __launch_bounds__(512, AXES || APPEND ? 2 : 3) qk_norm_rope_kern
     const uint16_t *head = token + (in_head ? (int64_t)h * D : 0);
     xa[k] = in_head ? ld_stream(head + l * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
     xb[k] = in_head ? ld_stream(head + (l + G) * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
-    if constexpr (kPlain) {
-      const uint16_t *w = h < a.hq ? a.qw : a.kw;
-      wa[k] = in_head ? ld_keep(w + l * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
-      wb[k] = in_head ? ld_keep(w + (l + G) * kElemsPerChunk) : make_uint4(0, 0, 0, 0);
-    }
   }
   bool pos_ok = true;                       // the same for the whole CTA
   [[maybe_unused]] uint32_t at[4] = {};     // first element of each axis's table row
@@ -240,21 +356,18 @@ __global__ void __launch_bounds__(512, AXES || APPEND ? 2 : 3) qk_norm_rope_kern
         }
       }
     }
-    if (!kPlain && first >= (APPEND ? a.hqk : a.nh)) continue;  // the whole warp
-    bool norm = true;
-    if constexpr (!kPlain) {
-      const uint16_t *w = h < a.hq ? a.qw : a.kw;
-      norm = w != nullptr && h < a.hqk;
-      constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones: a rotation without a norm
-      const uint4 ones = make_uint4(kOnes, kOnes, kOnes, kOnes);
-      wa[k] = norm ? ld_keep(w + l * kElemsPerChunk) : ones;
-      wb[k] = norm ? ld_keep(w + (l + G) * kElemsPerChunk) : ones;
-    }
+    if (first >= (APPEND ? a.hqk : a.nh)) continue;  // the whole warp
+    const uint16_t *w = h < a.hq ? a.qw : a.kw;
+    const bool norm = w != nullptr && h < a.hqk;
+    constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones: a rotation without a norm
+    const uint4 ones = make_uint4(kOnes, kOnes, kOnes, kOnes);
+    const uint4 wa = norm ? ld_keep(w + l * kElemsPerChunk) : ones;
+    const uint4 wb = norm ? ld_keep(w + (l + G) * kElemsPerChunk) : ones;
     float2 ta[4], tb[4];
     float cmax;
     RowAcc acc;
-    pass1_chunk<false, false>(xa[k], xa[k], wa[k], ta, cmax, acc);
-    pass1_chunk<false, false>(xb[k], xb[k], wb[k], tb, cmax, acc);
+    pass1_chunk<false, false>(xa[k], xa[k], wa, ta, cmax, acc);
+    pass1_chunk<false, false>(xb[k], xb[k], wb, tb, cmax, acc);
     float ss = acc.ss.x + acc.ss.y;
 #pragma unroll
     for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
@@ -294,9 +407,10 @@ __global__ void __launch_bounds__(512, AXES || APPEND ? 2 : 3) qk_norm_rope_kern
     };
     // A head whose squares' sum is not finite may hold an infinity.  Without a
     // norm it keeps it (with one, y = 0 makes it NaN either way).  Only such
-    // heads take the rotation with the test: in every head's it cost 1-2 %
-    // (16411 tokens, three axes, 55.1 -> 56.3 us; plain form 106.9 -> 110.3).
-    if (!kPlain && !norm && !(ss <= FLT_MAX))
+    // heads take the rotation with the test (16411 tokens, three axes: 56.5 us
+    // neox, 55.0 gptj; with the test in every head 56.5 and 57.1, without any
+    // 55.5 and 55.9).
+    if (!norm && !(ss <= FLT_MAX))
       turn(std::true_type{});
     else
       turn(std::false_type{});
@@ -325,24 +439,27 @@ __global__ void __launch_bounds__(512, AXES || APPEND ? 2 : 3) qk_norm_rope_kern
   }
 }
 
-// One token per CTA: up to 16 warps of heads; blockIdx.y covers the rest.
-template <int G, bool AXES, bool APPEND, int H>
-cudaError_t launch_heads(const QkArgs &a, bool neox, cudaStream_t s) {
+// One token per CTA: up to 16 warps of heads, more of them dealt out evenly over
+// blockIdx.y.  H: heads a lane group takes.
+template <int G, int H>
+cudaError_t launch_heads(void (*kern)(QkArgs), const QkArgs &a, cudaStream_t s) {
   constexpr int heads_per_warp = 32 / G * H;
-  // up to 16 warps a CTA; more of them are dealt out evenly
   const int all = (a.nh + heads_per_warp - 1) / heads_per_warp;
   const int parts = (all + 15) / 16;
   const int warps = (all + parts - 1) / parts;
   const dim3 grid((unsigned)a.T, (unsigned)((a.nh + warps * heads_per_warp - 1) / (warps * heads_per_warp)));
-  return neox ? launch_pdl(qk_norm_rope_kernel<G, true, AXES, APPEND, H>, grid, dim3(warps * 32), 0, s, a)
-              : launch_pdl(qk_norm_rope_kernel<G, false, AXES, APPEND, H>, grid, dim3(warps * 32), 0, s, a);
+  return launch_pdl(kern, grid, dim3(warps * 32), 0, s, a);
 }
 
 // Many tokens: from four per SM on (pf_ctas is two per SM).
 template <int G, bool AXES, bool APPEND>
 cudaError_t launch_form(const QkArgs &a, bool neox, cudaStream_t s) {
-  if (a.T >= 2LL * a.pf_ctas) return launch_heads<G, AXES, APPEND, kManyHeads>(a, neox, s);
-  return launch_heads<G, AXES, APPEND, 1>(a, neox, s);
+  constexpr int H = kManyHeads;
+  if (a.T >= 2LL * a.pf_ctas)
+    return launch_heads<G, H>(neox ? qk_norm_rope_form_kernel<G, true, AXES, APPEND, H>
+                                   : qk_norm_rope_form_kernel<G, false, AXES, APPEND, H>, a, s);
+  return launch_heads<G, 1>(neox ? qk_norm_rope_form_kernel<G, true, AXES, APPEND, 1>
+                                 : qk_norm_rope_form_kernel<G, false, AXES, APPEND, 1>, a, s);
 }
 
 template <int G>
@@ -352,8 +469,8 @@ cudaError_t launch_g(const QkArgs &a, bool neox, cudaStream_t s) {
   // the plain form has weights and one axis; without weights the multi-axis
   // form turns by its one axis
   const bool weights = (a.hq == 0 || a.qw) && (a.hqk == a.hq || a.kw);
-  return a.axes > 1 || !weights ? launch_form<G, true, false>(a, neox, s)
-                                : launch_heads<G, false, false, 1>(a, neox, s);
+  if (a.axes > 1 || !weights) return launch_form<G, true, false>(a, neox, s);
+  return launch_heads<G, 1>(neox ? qk_norm_rope_kernel<G, true> : qk_norm_rope_kernel<G, false>, a, s);
 }
 
 }  // namespace
