@@ -111,3 +111,68 @@ def test_nvfp4_wrappers():
     assert tuple(q4.shape) == (T, I // 2) and tuple(sf.shape) == (T, I // 16)
     o = parity.oracle_nvfp4_silu(ds["gate_up"], 168.0)
     parity.check_nvfp4({"q4": q4.cpu().numpy(), "sf": sf.view(torch.uint8).cpu().numpy()}, o)
+
+
+def _calls(torch):
+    """Every allocating call: (name, function of a stream that returns its outputs)."""
+    T, H = 300, 1024
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, res = (torch.randn((T, H), generator=g, device="cuda").bfloat16() for _ in range(2))
+    gu = torch.randn((T, 2 * H), generator=g, device="cuda").bfloat16()
+    w, gs = torch.ones(H, device="cuda").bfloat16(), torch.ones(1, device="cuda")
+    a = torch.randint(-2, 3, (T, H), generator=g, device="cuda").to(torch.float8_e4m3fn)
+    b = torch.randint(-2, 3, (H, H), generator=g, device="cuda").to(torch.float8_e4m3fn)
+    sa, sb = torch.ones((T, H // 128), device="cuda"), torch.ones((H // 128, H // 128), device="cuda")
+    return {
+        "norm": lambda s: vg.fused_add_rms_norm_fp8(x, res, w, 1e-5, vg.PER_GROUP, inplace=False, stream=s),
+        "silu": lambda s: vg.silu_mul_fp8(gu, vg.PER_GROUP | OPT, stream=s),
+        "mla": lambda s: vg.mla_dual_rms_norm(x, w, res, w, 1e-5, 1e-5, stream=s),
+        "mla_fp8": lambda s: vg.mla_dual_rms_norm(x, w, res, w, 1e-5, 1e-5, True, stream=s),
+        "pad": lambda s: vg.fused_add_rms_norm_pad(x, res, w, 1e-5, H + 256, inplace=False, stream=s),
+        "norm_nvfp4": lambda s: vg.fused_add_rms_norm_nvfp4(x, res, w, 1e-5, gs, inplace=False, stream=s),
+        "silu_nvfp4": lambda s: vg.silu_mul_nvfp4(gu, gs, stream=s),
+        "gemm": lambda s: (vg.fp8_block_gemm(a, sa, b, sb, stream=s),),
+        "gated": lambda s: vg.fp8_block_gemm_silu_mul_fp8(a, sa, b, sb, stream=s),
+    }
+
+
+def _pool_stream(torch, t):
+    """The stream whose pool a tensor's memory belongs to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's memory")
+
+
+@pytest.mark.parametrize("name", ["norm", "silu", "mla", "mla_fp8", "pad", "norm_nvfp4", "silu_nvfp4", "gemm",
+                                  "gated"])
+def test_outputs_of_a_call_on_another_stream_are_that_streams_memory(name):
+    """The call's stream does not wait for the current one, so its outputs must
+    not reuse a block that work queued there still writes."""
+    import torch
+    call = _calls(torch)[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    big = torch.randn((8192, 8192), device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        # blocks of the outputs' sizes, written late on the current stream, then freed
+        old = [torch.empty_like(t) for t in want]
+        for _ in range(20):
+            big @ big
+        for t in old:
+            t.view(torch.uint8).fill_(0xAB)
+        del old, t
+        got = call(stream)
+        assert all(_pool_stream(torch, t) == side.cuda_stream for t in got)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    with torch.cuda.stream(side):  # the current stream, given by name
+        got = call(side)
+    assert all(_pool_stream(torch, t) == side.cuda_stream for t in got)
+    for stream in (0, torch.cuda.default_stream()):
+        assert all(_pool_stream(torch, t) == 0 for t in call(stream))
+        with torch.cuda.stream(side):
+            assert all(_pool_stream(torch, t) == 0 for t in call(stream))
+    torch.cuda.synchronize()
