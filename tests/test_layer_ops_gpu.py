@@ -266,6 +266,82 @@ def test_calls_from_several_threads():
     assert not bad
 
 
+@pytest.mark.parametrize("first", ["gemm", "gated", "append", "mrope", "norm"])
+def test_first_call_of_a_thread(first):
+    """A host thread whose first use of CUDA is a call of this library, into
+    outputs that are there already."""
+    import threading
+    import torch
+    from test_fp8_gemm_gpu import operands
+    from test_rope_append_gpu import cuda, inputs
+    sets = [operands(T, 512, 512, T, exact=True) for T in (1, 40, 300)]
+    outs = [torch.zeros((x[0].shape[0], 512), dtype=torch.bfloat16, device="cuda") for x in sets]
+    qs = [torch.zeros((x[0].shape[0], 256), dtype=torch.float8_e4m3fn, device="cuda") for x in sets]
+    scs = [torch.zeros((x[0].shape[0], 2), device="cuda") for x in sets]
+    d = inputs(20, 4, 2, 128, seed=1)
+    args = [cuda(d[n]) for n in ("q_weight", "k_weight", "cos_sin_cache")]
+    pos, qkv = cuda(d["positions"]), cuda(d["qkv"]).clone()
+    k, v = (torch.zeros((2, 16, 2, 128), dtype=torch.int16, device="cuda") for _ in range(2))
+    slots, w = torch.arange(20, device="cuda"), torch.ones(512, device="cuda").bfloat16()
+    stream = torch.cuda.current_stream().cuda_stream
+    calls = {
+        "gemm": lambda i: vg.vg_fp8_block_gemm(outs[i], *sets[i][:4], stream=stream),
+        "gated": lambda i: vg.vg_fp8_block_gemm_silu_mul_fp8(qs[i], scs[i], *sets[i][:4], stream=stream),
+        "append": lambda i: vg.vg_fused_qk_norm_rope_append(qkv, k, v, *args, pos, slots, 4, 2, 128, 1e-6,
+                                                            stream=stream),
+        "mrope": lambda i: vg.vg_fused_qk_norm_mrope(qkv, *args, pos.view(1, 20), (64,), 4, 2, 128, 1e-6,
+                                                     stream=stream),
+        "norm": lambda i: vg.vg_fused_add_rms_norm_fp8(qs[i].view(-1, 256), None, scs[i], outs[i][:, :256].contiguous(),
+                                                       None, w[:256], 1e-5, vg.PER_GROUP, stream=stream),
+    }
+    torch.cuda.synchronize()
+    raised = []
+
+    def work(i):
+        try:
+            calls[first](i)
+        except Exception as e:  # noqa: BLE001
+            raised.append(e)
+
+    for i in range(3):
+        t = threading.Thread(target=work, args=(i,))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert not raised
+    if first == "gemm":
+        for o, x in zip(outs, sets):
+            assert torch.equal(o, (x[4] @ x[5].t()).to(torch.bfloat16))
+
+
+def test_threads_that_call_at_once_raise_nothing():
+    """As above, many threads at once, each allocating on a stream of its own."""
+    import threading
+    import torch
+    from test_fp8_gemm_gpu import operands
+    sets = [operands(T, 1024, 1024, T, exact=True) for T in (1, 20, 60, 300, 700, 3)]
+    want = [(x[4] @ x[5].t()).to(torch.bfloat16) for x in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    done = []
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            outs = [vg.fp8_block_gemm(*sets[i][:4]) for _ in range(50)]
+            gated = [vg.fp8_block_gemm_silu_mul_fp8(*sets[i][:4]) for _ in range(10)]
+            streams[i].synchronize()
+        if all(torch.equal(o, want[i]) for o in outs) and all(torch.equal(s, gated[0][1]) for _, s in gated):
+            done.append(i)
+
+    for _ in range(5):
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    assert sorted(done) == sorted(list(range(len(sets))) * 5)
+
+
 def _gemm(T, N, K):
     import torch
     from test_fp8_gemm_gpu import operands
