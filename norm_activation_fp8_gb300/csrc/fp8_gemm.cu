@@ -268,6 +268,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (++s == kTileStages) s = 0, ++lap;
         }
       }
+      // The last stages are released in both CTAs by products that the first
+      // one issued: neither CTA may end before these arrivals have landed.
+      for (uint32_t i = it < kTileStages ? 0 : it - kTileStages; i < it && ok; ++i)
+        ok = warp_wait_phase(&sm.empty[i % kTileStages], (i / kTileStages) & 1, &sm.failed);
     } else if (warp == 1 && rank == 0) {
       constexpr uint32_t desc = product_desc(2 * kTileT, kTileW);
       uint32_t it = 0, s = 0, lap = 0;
