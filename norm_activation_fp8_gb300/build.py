@@ -93,8 +93,8 @@ def build_wait_test(force: bool = False) -> str:
     return build(force, extra_flags=WAIT_TEST_FLAGS, out=WAIT_TEST_LIB)
 
 
-# Test-only copies with device bounds checks: every store and bulk-copy
-# source is checked against its tensor's extent; an access outside it is
+# Test-only copies with device bounds checks: every store, bulk-copy source and
+# scale copy is checked against its tensor's extent; an access outside it is
 # skipped and reported as VG_DEVICE_OUT_OF_BOUNDS.  The "shrunk" copy
 # reports every tensor one row short, so that the checks must fire.
 DEBUG_LIB = os.path.join(BUILD, "libvg_fused_debug_checks.so")

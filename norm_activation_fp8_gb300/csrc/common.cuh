@@ -111,12 +111,14 @@ __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
 // -------------------------------------------------------- debug checks
 //
 // Debug builds (-DVG_DEBUG_CHECKS, a test-only copy of the library): every
-// global store, and the source of every bulk copy, is first checked against
-// the extent of the tensor it touches.  An access outside it is skipped and
+// global store, and the source of every bulk copy and of the products' scale
+// copies, is first checked against the extent of the tensor it touches (copies
+// through a tensor map are clipped by the map instead).  An access outside it
+// is skipped (a scale reads as zero) and
 // sets kErrBounds in the translation unit's status word, so an indexing
 // mistake shows up as a status flag, not as a fault or as overwritten
 // memory.  Product builds compile each check to `true`.
-// VG_DEBUG_SHRINK_EXTENT (tests only) reports every tensor one row short,
+// VG_DEBUG_SHRINK_EXTENT (tests only) reports every tensor of tokens one row short,
 // so that the checks of a row's last accesses fire.
 constexpr uint32_t kErrBounds = 4u;
 #ifdef VG_DEBUG_SHRINK_EXTENT

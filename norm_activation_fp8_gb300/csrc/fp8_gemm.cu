@@ -112,6 +112,17 @@ __device__ __forceinline__ float group_scale(float amax, bool ue8m0) {
   return rows == 0 ? 0 : 4 * ((rows - 1) * (uint64_t)a.s_ts + (uint64_t)(a.N / kBlockK - 1) * a.s_gs + 1);
 }
 
+// Extents in bytes of the operands' scale tensors (debug checks; the operands
+// themselves and the tile kernel's outputs are clipped by their tensor maps).
+[[maybe_unused]] __device__ __forceinline__ uint64_t a_scale_extent(const GemmArgs &a) {
+  const uint64_t rows = VG_ROWS(a.T);
+  return rows == 0 ? 0 : 4 * ((rows - 1) * (uint64_t)a.a_ts + (uint64_t)(a.K / kBlockK - 1) * a.a_bs + 1);
+}
+template <bool GATED>
+[[maybe_unused]] __device__ __forceinline__ uint64_t w_scale_extent(const GemmArgs &a) {
+  return 4ull * (((GATED ? 2 : 1) * (uint64_t)a.N + kBlockK - 1) / kBlockK) * (uint64_t)(a.K / kBlockK);
+}
+
 // Four columns of a token's output row, from n on (N is a multiple of 8).
 __device__ __forceinline__ void store_out4(const GemmArgs &a, int64_t t, int n, const float4 &c) {
   uint16_t *o = a.out + t * a.N + n;
@@ -331,10 +342,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const bool live = row + 32 * j < a.T;
-              copy_async4(&sm.sa[g & 1][x][lane + 32 * j],
-                          pa + (live ? (row + 32 * j) * a.a_ts + (kb + x) * a.a_bs : 0), live);
+              const float *p = pa + (live ? (row + 32 * j) * a.a_ts + (kb + x) * a.a_bs : 0);
+              copy_async4(&sm.sa[g & 1][x][lane + 32 * j], p,
+                          live && VG_ACCESS_OK(g_gemm_status, p, 4, a.a_scale, a_scale_extent(a)));
             }
-            if (lane < 2) copy_async4(&sm.sw[g & 1][x][lane], pw + (w_live ? kb + x : 0), w_live);
+            if (lane < 2) {
+              const float *p = pw + (w_live ? kb + x : 0);
+              copy_async4(&sm.sw[g & 1][x][lane], p,
+                          w_live && VG_ACCESS_OK(g_gemm_status, p, 4, a.w_scale, w_scale_extent<GATED>(a)));
+            }
           }
           copy_async_arrive(&sm.scale_full[g & 1]);
         }
@@ -668,11 +684,17 @@ __global__ void __launch_bounds__(kStreamThreads<TN>, TN <= 64 ? 2 : 1)
 #pragma unroll
       for (int j = 0; j < (TN + 31) / 32; ++j) {
         const int t = lane + 32 * j;
-        const bool live = t0 + t < a.T;
+        const bool live = t0 + t < a.T && t < TN;
+        const float *p = a.a_scale + (live ? (t0 + t) * a.a_ts + kb * a.a_bs : 0);
         if (t < TN)
-          copy_async4(&sm.sa[s][t], a.a_scale + (live ? (t0 + t) * a.a_ts + kb * a.a_bs : 0), live);
+          copy_async4(&sm.sa[s][t], p,
+                      live && VG_ACCESS_OK(g_gemm_status, p, 4, a.a_scale, a_scale_extent(a)));
       }
-      if (lane < 2) copy_async4(&sm.sw[s][lane], pw + (w_live ? kb : 0), w_live);
+      if (lane < 2) {
+        const float *p = pw + (w_live ? kb : 0);
+        copy_async4(&sm.sw[s][lane], p,
+                    w_live && VG_ACCESS_OK(g_gemm_status, p, 4, a.w_scale, w_scale_extent<GATED>(a)));
+      }
       copy_async_arrive(&sm.scale_full[s]);
       if (++s == kScaleSlots) s = 0, ++lap;
     }
