@@ -378,8 +378,9 @@ vg_status vg_fused_qk_norm_rope_append(
  * what the per-group-128 ops above write.  With b = k / 128,
  *   out[t, n] = bf16( sum_b a_scale[t, b] w_scale[n / 128, b]
  *                     sum_{k in block b} a[t, k] w[n, k] )
- * The products of a block and the scaled sum over blocks are held in fp32;
- * the result is rounded once, to nearest even bf16.
+ * The products of a block and the scaled sum over blocks are held in fp32: the
+ * sum is off by at most 2^-23 (K / 128 + 130) times the sum of the scaled
+ * products' magnitudes; it is rounded once, to nearest even bf16.
  *
  *   out       out uint16 [T, N] bf16
  *   a         in  uint8 [T, K]  E4M3 codes

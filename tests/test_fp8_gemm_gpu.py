@@ -303,3 +303,37 @@ def test_captured_calls_and_two_streams(T):
     torch.cuda.synchronize()
     for k in range(2):
         assert all(torch.equal(x, want[k]) for x in got[k])
+
+
+@pytest.mark.parametrize("big,step", [(256.0, 2.0 ** -4), (448.0, 2.0 ** -3)])
+@pytest.mark.parametrize("T,N,K", [
+    (1, 8, 128), (1, 6144, 4096), (20, 96, 128), (31, 384, 896), (50, 2056, 512), (69, 28872, 128),
+    (70, 3800, 6912), (196, 3704, 6912), (1000, 2056, 896), (2049, 4096, 640)])
+def test_block_sums_are_held_in_fp32(T, N, K, big, step):
+    """Blocks with +big^2 and -big^2, in one product of 32 codes or in two,
+    beside products that are multiples of 2^-3 step: their sum has to come out
+    exact.  Every partial sum, in whatever order, is a multiple of 2^-3 step
+    (2^-7, 2^-6) below big^2 + 126 * 2^-1 step < 2^17 (2^18), so it has at most
+    24 bits; an accumulator of fewer, or products aligned to fewer, loses some."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    kb = K // BLOCK
+    for apart in (False, True):
+        a = torch.randint(-2, 3, (T, K), generator=g, device="cuda") * 2.0 ** -3
+        w = torch.randint(-2, 3, (N, K), generator=g, device="cuda") * step
+        st = torch.randint(0, 2, (T, 1), generator=g, device="cuda") * 2.0 - 1
+        sn = torch.randint(0, 2, (N, 1), generator=g, device="cuda") * 2.0 - 1
+        for b in range(kb):
+            p = int(torch.randint(0, 128, (1,), generator=g, device="cuda"))
+            q = (p + 32 + 32 * (b % 3)) % 128 if apart else p ^ (1 + b % 31)
+            p, q = b * BLOCK + p, b * BLOCK + q
+            a[:, [p, q]] = big * st
+            w[:, [p]], w[:, [q]] = big * sn, -big * sn
+        f8 = torch.float8_e4m3fn
+        assert bool((a.to(f8).float() == a).all()) and bool((w.to(f8).float() == w).all())
+        want = a.double() @ w.double().t()
+        assert float(want.abs().max()) < 4 * kb and (K == 128 or float(want.abs().max()) > 0)
+        sa = torch.ones((T, kb), device="cuda")
+        sw = torch.ones(((N + BLOCK - 1) // BLOCK, kb), device="cuda")
+        out = vg.fp8_block_gemm(a.to(f8), sa, w.to(f8), sw)
+        assert torch.equal(out, want.to(torch.bfloat16))
