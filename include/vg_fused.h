@@ -416,8 +416,16 @@ vg_status vg_fp8_block_gemm(uint16_t *out, const uint8_t *a, const float *a_scal
  *   w         in  uint8 [2I, K]: gate rows [0, I), up rows [I, 2I)
  *   w_scale   in  fp32 [2I / 128, K / 128]
  *   inter I: a multiple of 128 (else VG_ERR_BAD_GROUP), at most VG_MAX_ROW
- * y is fp32: with VG_SCALE_UE8M0 a group whose amax lies within fp32 rounding
- * of a power-of-two boundary may get the neighbouring power.
+ * y is fp32: besides what the errors of g and u make of it, off by at most
+ * (5 + 1.2 |g|) 2^-23 |y| (the exponential's error grows with its argument;
+ * below g = -87 it may be 0, where |y| < 2^-119 |u|); s is within 2^-23 of its
+ * own, codes are those of a quotient within 2^-22 of y / s.  With
+ * VG_SCALE_UE8M0 a group whose amax lies that near a power-of-two boundary may
+ * get the neighbouring power.
+ * Not finite (as vg_silu_mul_fp8): a NaN never wins the amax and its code is
+ * 0x7F; silu(-inf) is NaN; an infinite y gives its group the scale +inf, itself
+ * the code 0x7F and its finite neighbours signed zeros, or with VG_SCALE_UE8M0
+ * the scale 2^120 (the largest that a finite amax takes) and itself +-448.
  */
 vg_status vg_fp8_block_gemm_silu_mul_fp8(uint8_t *q, float *scale, const uint8_t *a,
                                          const float *a_scale, const uint8_t *w,
