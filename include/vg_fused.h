@@ -333,8 +333,8 @@ vg_status vg_fused_qk_norm_mrope(uint16_t *qkv, const uint16_t *q_weight, const 
  * vg_fused_qk_norm_rope, and V's own bits.  FP8 caches hold e4m3(o / k_scale)
  * and e4m3(v / v_scale) (RNE, saturating, infinities too, from the fp32 value;
  * the kernel multiplies by the rounded 1 / scale).  Without a norm an infinite
- * element gives what IEEE arithmetic makes of a c - b s.  The K and V heads of
- * qkv itself are left as they are.
+ * element gives what IEEE arithmetic makes of a c - b s (cosines and sines of
+ * at most 1).  The K and V heads of qkv itself are left as they are.
  *
  *   qkv            in/out uint16 [T, (Hq + 2 Hkv) * D] bf16 (Q heads written)
  *   k_cache, v_cache  out uint16 bf16, or uint8 E4M3 codes; element (page,

@@ -33,9 +33,6 @@
 // written once.  A rotation without a norm takes weights of one and y = 1, and
 // keeps infinities (NaN only where IEEE arithmetic gives it); FP8 caches
 // saturate them.
-#include <cfloat>
-#include <type_traits>
-
 #include "common.cuh"
 #include "launch.h"
 #include "row_norm.cuh"
@@ -61,17 +58,14 @@ __device__ __forceinline__ void load4f(const float *p, float (&v)[8], int at) {
 }
 
 // Two elements of a*c -/+ b*s (Kahan), packed; a zero keeps the plain
-// expression's sign.  nb = -b for the minus form.  INF: elements may be
-// infinite; an infinite product makes the error term NaN, and there the plain
-// expression stands.
-template <bool INF>
+// expression's sign, and so does an infinite b, whose error term is NaN (the
+// comparison is false for it).  nb = -b for the minus form.
 __device__ __forceinline__ float2 kahan2x(float2 a, float2 c, float2 nb, float2 s) {
   const float2 q = f2_mul(nb, s);
   const float2 e = f2_fma(nb, s, make_float2(-q.x, -q.y));
   const float2 f = f2_fma(a, c, q);
   const float2 o = f2_add(f, e);
-  return make_float2(e.x != 0.f && !(INF && isnan(o.x)) ? o.x : f.x,
-                     e.y != 0.f && !(INF && isnan(o.y)) ? o.y : f.y);
+  return make_float2(fabsf(e.x) > 0.f ? o.x : f.x, fabsf(e.y) > 0.f ? o.y : f.y);
 }
 
 // The plain form, in place: one head a lane group, weights and one axis.  A
@@ -170,7 +164,7 @@ __global__ void __launch_bounds__(512) qk_norm_rope_kernel(const QkArgs a) {
 #pragma unroll
   for (int k = 0; k < 16; k += 2) {
     const bool m0 = (submask >> k) & 1u, m1 = (submask >> (k + 1)) & 1u;
-    const float2 o = kahan2x<false>(make_float2(mine[k], mine[k + 1]), make_float2(c[k], c[k + 1]),
+    const float2 o = kahan2x(make_float2(mine[k], mine[k + 1]), make_float2(c[k], c[k + 1]),
                              make_float2(m0 ? -other[k] : other[k], m1 ? -other[k + 1] : other[k + 1]),
                              make_float2(s[k], s[k + 1]));
     const float2 pp = f2_mul(o, make_float2(y, y));
@@ -257,7 +251,7 @@ __device__ __forceinline__ void cache_store(const QkArgs &a, void *cache, int64_
 // axes: 80, 57, 55, 55 us with one to four; 32768 tokens into a bf16 cache: 171,
 // 140, 122, 124 us, the copy rate; 8191 tokens of 64 + 8 heads into an FP8
 // cache: 66, 59, 56, 54; gptj with one to three: 80, 58, 56; 170, 133, 121; 66,
-// 55, 52).
+// 55, 52, although three spill 16 to 20 bytes).
 constexpr int kManyHeads = 3;
 
 template <int G, bool NEOX, bool AXES, bool APPEND, int H>
@@ -392,28 +386,16 @@ __global__ void __launch_bounds__(512, 2) qk_norm_rope_form_kernel(const QkArgs 
     constexpr uint32_t submask = NEOX ? 0x00FFu : 0x5555u;
 
     float p[16];
-    const auto turn = [&](auto inf) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const bool m0 = (submask >> i) & 1u, m1 = (submask >> (i + 1)) & 1u;
-        const float2 o = kahan2x<decltype(inf)::value>(
-            make_float2(mine[i], mine[i + 1]), make_float2(c[i], c[i + 1]),
-            make_float2(m0 ? -other[i] : other[i], m1 ? -other[i + 1] : other[i + 1]),
-            make_float2(s[i], s[i + 1]));
-        const float2 pp = f2_mul(o, make_float2(y, y));
-        p[i] = pp.x;
-        p[i + 1] = pp.y;
-      }
-    };
-    // A head whose squares' sum is not finite may hold an infinity.  Without a
-    // norm it keeps it (with one, y = 0 makes it NaN either way).  Only such
-    // heads take the rotation with the test (16411 tokens, three axes: 56.5 us
-    // neox, 55.0 gptj; with the test in every head 56.5 and 57.1, without any
-    // 55.5 and 55.9).
-    if (!norm && !(ss <= FLT_MAX))
-      turn(std::true_type{});
-    else
-      turn(std::false_type{});
+    for (int i = 0; i < 16; i += 2) {
+      const bool m0 = (submask >> i) & 1u, m1 = (submask >> (i + 1)) & 1u;
+      const float2 o = kahan2x(make_float2(mine[i], mine[i + 1]), make_float2(c[i], c[i + 1]),
+                               make_float2(m0 ? -other[i] : other[i], m1 ? -other[i + 1] : other[i + 1]),
+                               make_float2(s[i], s[i + 1]));
+      const float2 pp = f2_mul(o, make_float2(y, y));
+      p[i] = pp.x;
+      p[i + 1] = pp.y;
+    }
     if (!live) continue;
     if constexpr (APPEND) {
       if (h >= a.hq) {  // a K head goes to its slot (a V head is already there)
