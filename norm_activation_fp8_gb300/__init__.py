@@ -178,20 +178,29 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+_AS_IT_IS = contextlib.nullcontext()
+
+
 def _allocating(stream):
     """Context for the outputs a call allocates: they belong to the stream it
     runs on.  Memory of the current stream may still be in use there by work
     queued before, which another stream does not wait for."""
-    import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _AS_IT_IS
+    import torch
     raw = _stream(stream)
     if raw == torch.cuda.current_stream().cuda_stream:
-        return contextlib.nullcontext()
+        return _AS_IT_IS
     if not isinstance(stream, torch.cuda.Stream):
         # 0 and 1 (cudaStreamLegacy) are the default stream
         stream = torch.cuda.ExternalStream(raw) if raw > 1 else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
+
+
+def _empty_on(stream, shape, dtype, device):
+    import torch
+    with _allocating(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _dtypes():
@@ -554,8 +563,8 @@ def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=No
     dev, raw = _here(a, stream)
     T, N, K = _block_gemm_sizes(a, a_scale, w, w_scale, a_options, dev)
     if out is None:
-        with _allocating(stream):
-            out = torch.empty((T, N), dtype=bf16[0], device=a.device)
+        out = (torch.empty((T, N), dtype=bf16[0], device=a.device) if stream is None
+               else _empty_on(stream, (T, N), bf16[0], a.device))
     elif (out.shape != (T, N) or out.dtype not in bf16 or out.get_device() != dev
           or not out.is_contiguous()):
         _shape(out, (T, N), "out")
@@ -585,9 +594,12 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     inter = N // 2
     shape = (inter // BLOCK, (T + 3) // 4 * 4) if out_options & COLUMN_MAJOR else (T, inter // BLOCK)
     if q is None and scale is None:
-        with _allocating(stream):
+        if stream is None:
             q = torch.empty((T, inter), dtype=fp8[0], device=a.device)
             scale = torch.empty(shape, dtype=f32[0], device=a.device)
+        else:
+            q = _empty_on(stream, (T, inter), fp8[0], a.device)
+            scale = _empty_on(stream, shape, f32[0], a.device)
     elif (q is None or scale is None or q.shape != (T, inter) or q.dtype not in fp8
           or q.get_device() != dev or not q.is_contiguous() or scale.shape != shape
           or scale.dtype not in f32 or scale.get_device() != dev or not scale.is_contiguous()):
