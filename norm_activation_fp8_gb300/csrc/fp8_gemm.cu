@@ -35,9 +35,14 @@
 // issued, finished, seen by the summing warps, read, given back to the issuing
 // warp) costs 940 cycles without any work in it, and with two accumulators half
 // of that and of the work shows.  Without the sums it runs at 3230, without
-// sums and tensor memory loads at 3470 TFLOP/s.  Products of 128 columns take as
-// long as those of 256, so four shorter accumulators, or one released by halves,
-// are slower (2120); a CTA alone reached 1980, eight summing warps 1760.  Long runs meet the power limit first.
+// sums and tensor memory loads at 3470 TFLOP/s.  A block's products take two
+// cycles a column (back to back, a pair: 259, 323, 387, 451, 515 cycles for 128,
+// 160, 192, 224, 256 columns; 64 columns take 175), so narrower accumulators
+// lose nothing there; but four of 128 columns, or one released by halves, have
+// twice the waits and arrivals for the same work and were slower (2120).  Three
+// of 160 columns have not been built.  A CTA alone reached 1980, eight summing
+// warps 1760.  The persistent forms spill 20 bytes.  Long runs meet the power
+// limit first.
 #include <atomic>
 
 #include "common.cuh"
@@ -925,7 +930,9 @@ cudaError_t launch_form(const GemmArgs &a, const GemmPlan &p, int sms, cudaStrea
 
 // Which kernel, and its split, by an estimate of either one's time, in
 // microseconds (fitted on GB300 to T = 1..1024, N = 1024..57344, K =
-// 4096..28672; over those the choice is within 10 % of the best one):
+// 4096..28672; over those the choice was within 10 % of the best one at all
+// sizes but one: 700 x 1024 x 4096 takes 64-token tiles, 14.0 us, where
+// 128-token tiles take 12.4):
 //   tile kernel    a wave of pairs: 0.42 per scale block of its share of K, and
 //                  4.4 (one share) .. 9.5 (four) for start, end and the sum of
 //                  the shares
