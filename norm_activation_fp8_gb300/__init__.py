@@ -47,7 +47,6 @@ stream they run on):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -178,29 +177,24 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-_AS_IT_IS = contextlib.nullcontext()
-
-
-def _allocating(stream):
-    """Context for the outputs a call allocates: they belong to the stream it
-    runs on.  Memory of the current stream may still be in use there by work
-    queued before, which another stream does not wait for."""
-    if stream is None:
-        return _AS_IT_IS
+def _allocator(stream):
+    """torch.empty for the outputs of a call: memory of the stream it runs on.
+    Memory of the current stream may still be in use there by work queued
+    before, which another stream does not wait for."""
     import torch
+    if stream is None:
+        return torch.empty
     raw = _stream(stream)
     if raw == torch.cuda.current_stream().cuda_stream:
-        return _AS_IT_IS
+        return torch.empty
     if not isinstance(stream, torch.cuda.Stream):
         # 0 and 1 (cudaStreamLegacy) are the default stream
         stream = torch.cuda.ExternalStream(raw) if raw > 1 else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
 
-
-def _empty_on(stream, shape, dtype, device):
-    import torch
-    with _allocating(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+    def empty(shape, dtype, device):
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    return empty
 
 
 def _dtypes():
@@ -563,8 +557,7 @@ def vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options: int = 0, stream=No
     dev, raw = _here(a, stream)
     T, N, K = _block_gemm_sizes(a, a_scale, w, w_scale, a_options, dev)
     if out is None:
-        out = (torch.empty((T, N), dtype=bf16[0], device=a.device) if stream is None
-               else _empty_on(stream, (T, N), bf16[0], a.device))
+        out = _allocator(stream)((T, N), dtype=bf16[0], device=a.device)
     elif (out.shape != (T, N) or out.dtype not in bf16 or out.get_device() != dev
           or not out.is_contiguous()):
         _shape(out, (T, N), "out")
@@ -594,12 +587,9 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     inter = N // 2
     shape = (inter // BLOCK, (T + 3) // 4 * 4) if out_options & COLUMN_MAJOR else (T, inter // BLOCK)
     if q is None and scale is None:
-        if stream is None:
-            q = torch.empty((T, inter), dtype=fp8[0], device=a.device)
-            scale = torch.empty(shape, dtype=f32[0], device=a.device)
-        else:
-            q = _empty_on(stream, (T, inter), fp8[0], a.device)
-            scale = _empty_on(stream, shape, f32[0], a.device)
+        empty = _allocator(stream)
+        q = empty((T, inter), dtype=fp8[0], device=a.device)
+        scale = empty(shape, dtype=f32[0], device=a.device)
     elif (q is None or scale is None or q.shape != (T, inter) or q.dtype not in fp8
           or q.get_device() != dev or not q.is_contiguous() or scale.shape != shape
           or scale.dtype not in f32 or scale.get_device() != dev or not scale.is_contiguous()):
@@ -628,18 +618,18 @@ def vg_device_status(reset: bool = False) -> int:
 
 # ------------------------------------------------- allocating wrappers
 
-def _scale_out(mode, T, n, group_size, scale, device):
+def _scale_out(empty, mode, T, n, group_size, scale, device):
     import torch
     if mode & COLUMN_MAJOR:
-        return torch.empty((n // group_size, (T + 3) // 4 * 4), dtype=torch.float32, device=device)
+        return empty((n // group_size, (T + 3) // 4 * 4), dtype=torch.float32, device=device)
     mode &= 0xFF
     if mode == STATIC:
         if scale is None:
             raise ValueError("static mode needs a scale tensor")
         return scale
     if mode == PER_TOKEN:
-        return torch.empty((T,), dtype=torch.float32, device=device)
-    return torch.empty((T, n // group_size), dtype=torch.float32, device=device)
+        return empty((T,), dtype=torch.float32, device=device)
+    return empty((T, n // group_size), dtype=torch.float32, device=device)
 
 
 def fused_add_rms_norm_fp8(x, residual, weight, eps: float, mode: int, group_size: int = 128,
@@ -648,12 +638,12 @@ def fused_add_rms_norm_fp8(x, residual, weight, eps: float, mode: int, group_siz
     ``inplace`` the residual is updated in place, as the fused op does."""
     import torch
     T, H = x.shape
-    with _allocating(stream):
-        q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
-        s = _scale_out(mode, T, H, group_size, scale, x.device)
-        r_out = None
-        if residual is not None:
-            r_out = residual if inplace else torch.empty_like(residual)
+    empty = _allocator(stream)
+    q = empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
+    s = _scale_out(empty, mode, T, H, group_size, scale, x.device)
+    r_out = None
+    if residual is not None:
+        r_out = residual if inplace else empty(residual.shape, dtype=residual.dtype, device=residual.device)
     vg_fused_add_rms_norm_fp8(q, r_out, s, x, residual, weight, eps, mode, group_size, stream)
     return q, s, r_out
 
@@ -662,9 +652,9 @@ def silu_mul_fp8(gate_up, mode: int, group_size: int = 128, scale=None, stream=N
     """Returns (q float8_e4m3fn [T,I], scale)."""
     import torch
     T, two_i = gate_up.shape
-    with _allocating(stream):
-        q = torch.empty((T, two_i // 2), dtype=torch.float8_e4m3fn, device=gate_up.device)
-        s = _scale_out(mode, T, two_i // 2, group_size, scale, gate_up.device)
+    empty = _allocator(stream)
+    q = empty((T, two_i // 2), dtype=torch.float8_e4m3fn, device=gate_up.device)
+    s = _scale_out(empty, mode, T, two_i // 2, group_size, scale, gate_up.device)
     vg_silu_mul_fp8(q, s, gate_up, mode, group_size, stream)
     return q, s
 
@@ -675,10 +665,10 @@ def mla_dual_rms_norm(q_c, q_weight, kv_c, kv_weight, eps_q: float, eps_kv: floa
     ``q_fp8`` (q float8_e4m3fn [T,q_dim], q_scale fp32 [T], kv_normed)."""
     import torch
     T, q_dim = q_c.shape
-    with _allocating(stream):
-        kv = torch.empty((T, kv_c.shape[1]), dtype=kv_c.dtype, device=kv_c.device)
-        q = torch.empty((T, q_dim), dtype=torch.float8_e4m3fn if q_fp8 else q_c.dtype, device=q_c.device)
-        s = torch.empty((T,), dtype=torch.float32, device=q_c.device) if q_fp8 else None
+    empty = _allocator(stream)
+    kv = empty((T, kv_c.shape[1]), dtype=kv_c.dtype, device=kv_c.device)
+    q = empty((T, q_dim), dtype=torch.float8_e4m3fn if q_fp8 else q_c.dtype, device=q_c.device)
+    s = empty((T,), dtype=torch.float32, device=q_c.device) if q_fp8 else None
     if q_fp8:
         vg_fused_mla_dual_rms_norm_per_token_quant(q, s, kv, q_c, q_weight, kv_c, kv_weight,
                                                    eps_q, eps_kv, stream)
@@ -692,11 +682,11 @@ def fused_add_rms_norm_pad(x, residual, weight, eps: float, padded_hidden: int,
     """Returns (out bf16 [T, padded_hidden], residual_out)."""
     import torch
     T, H = x.shape
-    with _allocating(stream):
-        out = torch.empty((T, padded_hidden), dtype=x.dtype, device=x.device)
-        r_out = None
-        if residual is not None:
-            r_out = residual if inplace else torch.empty_like(residual)
+    empty = _allocator(stream)
+    out = empty((T, padded_hidden), dtype=x.dtype, device=x.device)
+    r_out = None
+    if residual is not None:
+        r_out = residual if inplace else empty(residual.shape, dtype=residual.dtype, device=residual.device)
     vg_fused_add_rms_norm_pad(out, r_out, x, residual, weight, eps, stream)
     return out, r_out
 
@@ -707,12 +697,12 @@ def fused_add_rms_norm_nvfp4(x, residual, weight, eps: float, global_scale, inpl
     residual_out); global_scale is an fp32 [1] device tensor."""
     import torch
     T, H = x.shape
-    with _allocating(stream):
-        q4 = torch.empty((T, H // 2), dtype=torch.uint8, device=x.device)
-        sf = torch.empty((T, H // 16), dtype=torch.float8_e4m3fn, device=x.device)
-        r_out = None
-        if residual is not None:
-            r_out = residual if inplace else torch.empty_like(residual)
+    empty = _allocator(stream)
+    q4 = empty((T, H // 2), dtype=torch.uint8, device=x.device)
+    sf = empty((T, H // 16), dtype=torch.float8_e4m3fn, device=x.device)
+    r_out = None
+    if residual is not None:
+        r_out = residual if inplace else empty(residual.shape, dtype=residual.dtype, device=residual.device)
     vg_fused_add_rms_norm_nvfp4(q4, sf, r_out, x, residual, weight, global_scale, eps, stream)
     return q4, sf, r_out
 
@@ -721,9 +711,9 @@ def silu_mul_nvfp4(gate_up, global_scale, stream=None):
     """Returns (q4 uint8 [T,I/2], block_scale float8_e4m3fn [T,I/16])."""
     import torch
     T, two_i = gate_up.shape
-    with _allocating(stream):
-        q4 = torch.empty((T, two_i // 4), dtype=torch.uint8, device=gate_up.device)
-        sf = torch.empty((T, two_i // 32), dtype=torch.float8_e4m3fn, device=gate_up.device)
+    empty = _allocator(stream)
+    q4 = empty((T, two_i // 4), dtype=torch.uint8, device=gate_up.device)
+    sf = empty((T, two_i // 32), dtype=torch.float8_e4m3fn, device=gate_up.device)
     vg_silu_mul_nvfp4(q4, sf, gate_up, global_scale, stream)
     return q4, sf
 
