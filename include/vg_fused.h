@@ -26,6 +26,9 @@
  * Beside them, for the layer around those operations (the pages describe no
  * such kernels; their own comments define them): the FP8 products that read
  * the per-group outputs (vg_fp8_block_gemm, vg_fp8_block_gemm_silu_mul_fp8),
+ * the NVFP4 products that read the NVFP4 outputs (vg_nvfp4_gemm,
+ * vg_nvfp4_gemm_silu_mul_nvfp4) with a quantiser for other rows and the way
+ * back (vg_nvfp4_quantize, vg_nvfp4_dequantize),
  * rotary positions with several axes (vg_fused_qk_norm_mrope) and the rotation
  * on the way into a paged key/value cache (vg_fused_qk_norm_rope_append).
  *
@@ -63,8 +66,8 @@
  *     launch, a copy or an event needs nothing extra.
  *   - bf16 tensors are passed as uint16_t bit patterns, fp8 outputs as
  *     uint8_t E4M3 codes.  All tensors are dense and row-major, except the
- *     MLA dual norm's two inputs, which are read through a row stride, and the
- *     paged caches, which have three strides.
+ *     MLA dual norm's two inputs and the NVFP4 quantiser's one, which are read
+ *     through a row stride, and the paged caches, which have three strides.
  *   - Every argument is validated on the host before any launch; a
  *     validation error returns its status and launches nothing.  A launch
  *     failure returns VG_ERR_CUDA.  num_tokens == 0 returns VG_OK without
@@ -432,6 +435,81 @@ vg_status vg_fp8_block_gemm_silu_mul_fp8(uint8_t *q, float *scale, const uint8_t
                                          const float *w_scale, int64_t num_tokens, int64_t inter,
                                          int64_t k, int32_t a_options, int32_t out_options,
                                          vg_stream_t stream);
+
+/*
+ * Rows of bf16 to NVFP4 (the format above), for what no fused op writes: an
+ * attention's output, a weight.
+ *   sf = e4m3(gs * amax / 6),  q = e2m1(x * gs / decode(sf)),  +0 where sf is 0
+ * Every code, scale's and element's, is the one that the exact value rounds to.
+ *
+ *   q4            out uint8 [T, n/2], block_scale out uint8 [T, n/16]: as above
+ *   x             in  uint16 bf16; row t is x[t * x_stride + j], j < n
+ *   x_stride      elements between rows: >= n, a multiple of 8
+ *   global_scale  in  fp32 [1], device, > 0 and finite (a usual one: 6 * 448
+ *                 over the tensor's largest magnitude)
+ *   num_tokens T >= 0; n: a multiple of 16 in [16, VG_MAX_ROW]; T * n < 2^41
+ * A NaN never wins the amax and its code is a saturated one; a block with an
+ * infinity gets the scale 448, and the infinity +-6.
+ */
+vg_status vg_nvfp4_quantize(uint8_t *q4, uint8_t *block_scale, const uint16_t *x, int64_t x_stride,
+                            const float *global_scale, int64_t num_tokens, int64_t n,
+                            vg_stream_t stream);
+
+/*
+ * NVFP4 back to bf16:
+ *   out = bf16(value(q) * fp32(decode(sf) / gs))
+ * (fp32 until the one rounding to nearest even bf16: 2^-23 of the value before
+ * it).  A NaN scale code gives NaN.
+ *
+ *   out           out uint16 [T, n] bf16
+ *   q4, block_scale, global_scale, num_tokens, n  as for vg_nvfp4_quantize
+ */
+vg_status vg_nvfp4_dequantize(uint16_t *out, const uint8_t *q4, const uint8_t *block_scale,
+                              const float *global_scale, int64_t num_tokens, int64_t n,
+                              vg_stream_t stream);
+
+/*
+ * NVFP4 matrix product, which reads what the NVFP4 ops write:
+ *   out[t, n] = bf16( alpha sum_k a[t, k] sa[t, k / 16] w[n, k] sw[n, k / 16] )
+ * The tensor cores apply the block scales and hold the sum over K in fp32: it
+ * is off by at most 2^-23 (K / 64 + 66) times the sum of the scaled products'
+ * magnitudes; alpha times it is rounded once, to nearest even bf16.
+ *
+ *   out       out uint16 [T, N] bf16
+ *   a         in  uint8 [T, K / 2]   E2M1 codes, a_scale in uint8 [T, K / 16]
+ *   w         in  uint8 [N, K / 2]   E2M1 codes, w_scale in uint8 [N, K / 16]:
+ *                 E4M3 codes of non-negative scales (0x00..0x7E)
+ *   alpha     in  fp32 [1], device: 1 / (gs of a * gs of w), as a rule
+ *   num_tokens T in [0, VG_MAX_GEMM_TOKENS]; n N: a multiple of 8 in
+ *             [8, VG_MAX_GEMM_COLUMNS]; k K: a multiple of 64 in
+ *             [64, VG_MAX_ROW] (else VG_ERR_BAD_SHAPE)
+ * All tensors 16-byte aligned, the scales too; alpha 4-byte.  No workspace.
+ */
+vg_status vg_nvfp4_gemm(uint16_t *out, const uint8_t *a, const uint8_t *a_scale, const uint8_t *w,
+                        const uint8_t *w_scale, const float *alpha, int64_t num_tokens, int64_t n,
+                        int64_t k, vg_stream_t stream);
+
+/*
+ * Gated feed-forward projection in NVFP4: the gate and up products, SiLU(gate)
+ * * up and its NVFP4 codes in one kernel:
+ *   g = row n, u = row I + n of w in the product above (fp32, not rounded)
+ *   y = g / (1 + exp(-g)) * u,  sf and q as for vg_silu_mul_nvfp4
+ *
+ *   q4, block_scale  out uint8 [T, I / 2] and [T, I / 16]
+ *   a, a_scale, alpha, k  as for vg_nvfp4_gemm
+ *   w         in  uint8 [2I, K / 2]: gate rows [0, I), up rows [I, 2I);
+ *                 w_scale [2I, K / 16] (one global scale, in alpha)
+ *   global_scale  in fp32 [1], device, > 0 and finite: the output's
+ *   inter I: a multiple of 64 in [64, VG_MAX_ROW] (else VG_ERR_BAD_SHAPE)
+ * Besides what the errors of g and u make of it, y is off by at most 2^-21 |y|
+ * (below g = -87 it may be 0), and gs amax / 6 and y gs / sf by 2^-21 of
+ * theirs: codes are those of values that near.
+ */
+vg_status vg_nvfp4_gemm_silu_mul_nvfp4(uint8_t *q4, uint8_t *block_scale, const uint8_t *a,
+                                       const uint8_t *a_scale, const uint8_t *w,
+                                       const uint8_t *w_scale, const float *alpha,
+                                       const float *global_scale, int64_t num_tokens, int64_t inter,
+                                       int64_t k, vg_stream_t stream);
 
 /*
  * Device-side status of the library's kernels on the current device (no

@@ -1,6 +1,6 @@
 """Fused residual-add + RMSNorm -> FP8 and SiLU-and-mul -> FP8 on GB300, the
-block-scaled FP8 products that read them, and QK norm + rotation with a paged
-K/V cache.
+block-scaled FP8 products that read them, NVFP4 quantisation and products, and
+QK norm + rotation with a paged K/V cache.
 
 Thin Python binding over the C ABI of ``libvg_fused.so`` (declared in
 ``include/vg_fused.h``).  Every step of both ops runs in the library's CUDA
@@ -34,6 +34,11 @@ Entry points (same names and argument order as the C ABI):
   vg_fp8_block_gemm(out, a, a_scale, w, w_scale, a_options=0, stream=None)
   vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options=0,
                          out_options=0, stream=None)
+  vg_nvfp4_quantize(q4, block_scale, x, global_scale, stream=None)
+  vg_nvfp4_dequantize(out, q4, block_scale, global_scale, stream=None)
+  vg_nvfp4_gemm(out, a, a_scale, w, w_scale, alpha, stream=None)
+  vg_nvfp4_gemm_silu_mul_nvfp4(q4, block_scale, a, a_scale, w, w_scale, alpha,
+                         global_scale, stream=None)
 Convenience wrappers that allocate the outputs with torch (as memory of the
 stream they run on):
   fused_add_rms_norm_fp8(x, residual, weight, eps, mode, ...)
@@ -44,6 +49,10 @@ stream they run on):
   silu_mul_nvfp4(gate_up, global_scale, ...)
   fp8_block_gemm(a, a_scale, w, w_scale, a_options=0)
   fp8_block_gemm_silu_mul_fp8(a, a_scale, w, w_scale, a_options=0, out_options=0)
+  nvfp4_quantize(x, global_scale)
+  nvfp4_dequantize(q4, block_scale, global_scale)
+  nvfp4_gemm(a, a_scale, w, w_scale, alpha)
+  nvfp4_gemm_silu_mul_nvfp4(a, a_scale, w, w_scale, alpha, global_scale)
 """
 from __future__ import annotations
 
@@ -67,7 +76,9 @@ EXPORTED_SYMBOLS = ("vg_fused_add_rms_norm_fp8", "vg_silu_mul_fp8", "vg_fused_ad
                     "vg_fused_mla_dual_rms_norm", "vg_fused_qk_norm_rope",
                     "vg_fused_mla_dual_rms_norm_per_token_quant", "vg_fused_add_rms_norm_nvfp4",
                     "vg_silu_mul_nvfp4", "vg_fused_qk_norm_mrope", "vg_fused_qk_norm_rope_append",
-                    "vg_fp8_block_gemm", "vg_fp8_block_gemm_silu_mul_fp8", "vg_device_status",
+                    "vg_fp8_block_gemm", "vg_fp8_block_gemm_silu_mul_fp8", "vg_nvfp4_quantize",
+                    "vg_nvfp4_dequantize", "vg_nvfp4_gemm", "vg_nvfp4_gemm_silu_mul_nvfp4",
+                    "vg_device_status",
                     "vg_status_string", "vg_abi_version")
 DEVICE_WAIT_TIMEOUT = 1
 DEVICE_BAD_POSITION = 2
@@ -130,6 +141,14 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.vg_fp8_block_gemm.restype = ctypes.c_int
         lib.vg_fp8_block_gemm_silu_mul_fp8.argtypes = [P, P, P, P, P, P, i64, i64, i64, i32, i32, P]
         lib.vg_fp8_block_gemm_silu_mul_fp8.restype = ctypes.c_int
+        lib.vg_nvfp4_quantize.argtypes = [P, P, P, i64, P, i64, i64, P]
+        lib.vg_nvfp4_quantize.restype = ctypes.c_int
+        lib.vg_nvfp4_dequantize.argtypes = [P, P, P, P, i64, i64, P]
+        lib.vg_nvfp4_dequantize.restype = ctypes.c_int
+        lib.vg_nvfp4_gemm.argtypes = [P] * 6 + [i64, i64, i64, P]
+        lib.vg_nvfp4_gemm.restype = ctypes.c_int
+        lib.vg_nvfp4_gemm_silu_mul_nvfp4.argtypes = [P] * 8 + [i64, i64, i64, P]
+        lib.vg_nvfp4_gemm_silu_mul_nvfp4.restype = ctypes.c_int
         lib.vg_status_string.argtypes = [ctypes.c_int]
         lib.vg_status_string.restype = ctypes.c_char_p
         lib.vg_abi_version.argtypes = []
@@ -607,6 +626,141 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     return q, scale
 
 
+def _one(t, name, dev):
+    """Device pointer of one fp32 value."""
+    if not hasattr(t, "numel") or t.numel() != 1:
+        raise ValueError(f"{name}: expected one fp32 value on the device")
+    f32 = _kinds()[2]
+    if t.dtype not in f32 or t.get_device() != dev:
+        _arg(t, f32, name, dev)
+    return t.data_ptr()
+
+
+def _codes(q4, block_scale, names, dev):
+    """(rows, columns) of a checked NVFP4 tensor: uint8 [T, n/2] with E4M3
+    scales [T, n/16]."""
+    _, fp8, _, _, torch = _kinds()
+    T, half = _rows(q4, names[0])
+    if (half % 8 or block_scale.shape != (T, half // 8) or q4.dtype != torch.uint8
+            or block_scale.dtype not in fp8 or q4.get_device() != dev
+            or block_scale.get_device() != dev or not q4.is_contiguous()
+            or not block_scale.is_contiguous()):
+        if half % 8:
+            raise ValueError(f"{names[0]}: expected whole blocks of 16 columns (8 bytes)")
+        _shape(block_scale, (T, half // 8), names[1])
+        _arg(q4, (torch.uint8,), names[0], dev)
+        _arg(block_scale, fp8, names[1], dev)
+    return T, 2 * half
+
+
+def _codes_out(q4, block_scale, T, n, stream, device):
+    """The NVFP4 tensor that a call writes, allocated where both are None."""
+    _, fp8, _, _, torch = _kinds()
+    if q4 is None and block_scale is None:
+        empty = _allocator(stream)
+        return (empty((T, n // 2), dtype=torch.uint8, device=device),
+                empty((T, n // 16), dtype=fp8[0], device=device))
+    if q4 is None or block_scale is None:
+        raise ValueError("q4 and block_scale: give both or neither")
+    _shape(q4, (T, n // 2), "q4")
+    _codes(q4, block_scale, ("q4", "block_scale"), device.index)
+    return q4, block_scale
+
+
+def vg_nvfp4_quantize(q4, block_scale, x, global_scale, stream=None):
+    """Rows of bf16 to NVFP4 through the C ABI: q4 [T,n/2] uint8, block_scale
+    [T,n/16] E4M3 codes; x [T,n] bf16, rows contiguous (a column slice is
+    fine); global_scale fp32 [1] on the device.  ``q4`` and ``block_scale``
+    both None allocate them; returns (q4, block_scale)."""
+    dev, raw = _here(x, stream)
+    xp, stride, T, n = _rows_ptr(x, "x")
+    if x.get_device() != dev:
+        _arg(x, _kinds()[0], "x", dev, False)
+    gs = _one(global_scale, "global_scale", dev)
+    if n % 16:
+        raise ValueError("x: expected whole blocks of 16 columns")
+    q4, block_scale = _codes_out(q4, block_scale, T, n, stream, x.device)
+    st = (_lib or load()).vg_nvfp4_quantize(q4.data_ptr(), block_scale.data_ptr(), xp,
+                                            stride if T > 1 else n, gs, T, n, raw)
+    if st:
+        _check(st)
+    return q4, block_scale
+
+
+def vg_nvfp4_dequantize(out, q4, block_scale, global_scale, stream=None):
+    """NVFP4 back to bf16 through the C ABI: out [T,n] bf16; the others as for
+    vg_nvfp4_quantize.  ``out`` None allocates it; returns out."""
+    bf16 = _kinds()[0]
+    dev, raw = _here(q4, stream)
+    T, n = _codes(q4, block_scale, ("q4", "block_scale"), dev)
+    gs = _one(global_scale, "global_scale", dev)
+    out = _bf16_out(out, T, n, stream, q4.device)
+    st = (_lib or load()).vg_nvfp4_dequantize(out.data_ptr(), q4.data_ptr(), block_scale.data_ptr(),
+                                              gs, T, n, raw)
+    if st:
+        _check(st)
+    return out
+
+
+def _bf16_out(out, T, n, stream, device):
+    bf16 = _kinds()[0]
+    if out is None:
+        return _allocator(stream)((T, n), dtype=bf16[0], device=device)
+    if (out.shape != (T, n) or out.dtype not in bf16 or out.get_device() != device.index
+            or not out.is_contiguous()):
+        _shape(out, (T, n), "out")
+        _arg(out, bf16, "out", device.index)
+    return out
+
+
+def vg_nvfp4_gemm(out, a, a_scale, w, w_scale, alpha, stream=None):
+    """NVFP4 product through the C ABI: out [T,N] bf16 = alpha (a * a_scale)
+    (w * w_scale)^T.
+
+    a [T,K/2] and w [N,K/2] uint8 (two E2M1 codes a byte) with a_scale
+    [T,K/16] and w_scale [N,K/16] E4M3 codes, as the NVFP4 ops write them;
+    alpha fp32 [1] on the device (1 over the product of the two global
+    scales).  ``out`` None allocates it; returns out."""
+    dev, raw = _here(a, stream)
+    T, K = _codes(a, a_scale, ("a", "a_scale"), dev)
+    N, Kw = _codes(w, w_scale, ("w", "w_scale"), dev)
+    if K != Kw:
+        raise ValueError("a and w must have the same number of columns")
+    al = _one(alpha, "alpha", dev)
+    out = _bf16_out(out, T, N, stream, a.device)
+    st = (_lib or load()).vg_nvfp4_gemm(out.data_ptr(), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
+                                        w_scale.data_ptr(), al, T, N, K, raw)
+    if st:
+        _check(st)
+    return out
+
+
+def vg_nvfp4_gemm_silu_mul_nvfp4(q4, block_scale, a, a_scale, w, w_scale, alpha, global_scale,
+                                 stream=None):
+    """Gated feed-forward projection in NVFP4 through the C ABI: the gate and
+    up products, SiLU(gate) * up and its NVFP4 codes in one kernel.
+
+    a, a_scale and alpha as for vg_nvfp4_gemm; w [2I,K/2] (gate rows [0,I), up
+    rows [I,2I)) with w_scale [2I,K/16]; global_scale fp32 [1] on the device:
+    the output's; q4 [T,I/2] uint8, block_scale [T,I/16] E4M3 codes, or both
+    None to allocate them; returns (q4, block_scale)."""
+    dev, raw = _here(a, stream)
+    T, K = _codes(a, a_scale, ("a", "a_scale"), dev)
+    N, Kw = _codes(w, w_scale, ("w", "w_scale"), dev)
+    if K != Kw:
+        raise ValueError("a and w must have the same number of columns")
+    if N % 32:
+        raise ValueError("w must have an even number of rows (gate, then up), whole blocks of 16 each")
+    al, gs = _one(alpha, "alpha", dev), _one(global_scale, "global_scale", dev)
+    q4, block_scale = _codes_out(q4, block_scale, T, N // 2, stream, a.device)
+    st = (_lib or load()).vg_nvfp4_gemm_silu_mul_nvfp4(
+        q4.data_ptr(), block_scale.data_ptr(), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
+        w_scale.data_ptr(), al, gs, T, N // 2, K, raw)
+    if st:
+        _check(st)
+    return q4, block_scale
+
+
 def vg_device_status(reset: bool = False) -> int:
     """Flags the library's kernels left on the current device
     (DEVICE_WAIT_TIMEOUT: a bounded wait gave up; that call's outputs are
@@ -728,3 +882,23 @@ def fp8_block_gemm_silu_mul_fp8(a, a_scale, w, w_scale, a_options: int = 0, out_
     """Returns (q float8_e4m3fn [T,I], scale)."""
     return vg_fp8_block_gemm_silu_mul_fp8(None, None, a, a_scale, w, w_scale, a_options, out_options,
                                           stream)
+
+
+def nvfp4_quantize(x, global_scale, stream=None):
+    """Returns (q4 uint8 [T,n/2], block_scale float8_e4m3fn [T,n/16])."""
+    return vg_nvfp4_quantize(None, None, x, global_scale, stream)
+
+
+def nvfp4_dequantize(q4, block_scale, global_scale, stream=None):
+    """Returns out bf16 [T,n]."""
+    return vg_nvfp4_dequantize(None, q4, block_scale, global_scale, stream)
+
+
+def nvfp4_gemm(a, a_scale, w, w_scale, alpha, stream=None):
+    """Returns out bf16 [T,N]."""
+    return vg_nvfp4_gemm(None, a, a_scale, w, w_scale, alpha, stream)
+
+
+def nvfp4_gemm_silu_mul_nvfp4(a, a_scale, w, w_scale, alpha, global_scale, stream=None):
+    """Returns (q4 uint8 [T,I/2], block_scale float8_e4m3fn [T,I/16])."""
+    return vg_nvfp4_gemm_silu_mul_nvfp4(None, None, a, a_scale, w, w_scale, alpha, global_scale, stream)

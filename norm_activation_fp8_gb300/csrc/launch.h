@@ -226,4 +226,41 @@ GemmPlan plan_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms);
 cudaError_t launch_fp8_gemm(const GemmArgs &a, bool gated, int sms, cudaStream_t s);
 uint32_t read_gemm_status(bool reset);
 
+// bf16 rows to NVFP4 and back: T rows of nch chunks of 8 columns.
+struct Nvfp4Args {
+  const uint16_t *x;          // quantise: bf16, `stride` elements a row
+  uint16_t *out;              // read back: bf16, dense
+  uint8_t *q;                 // E2M1 codes [T, 4 nch] bytes
+  uint8_t *sf;                // E4M3 block scales [T, nch / 2]
+  const float *global_scale;  // fp32 [1]
+  int64_t T;
+  int64_t nch;
+  int64_t stride;
+  int32_t pf_ctas;            // CTAs below this index prefetch their chunks into L2
+};
+cudaError_t launch_nvfp4_quantize(const Nvfp4Args &a, cudaStream_t s);
+cudaError_t launch_nvfp4_dequantize(const Nvfp4Args &a, cudaStream_t s);
+uint32_t read_nvfp4_status(bool reset);
+
+// NVFP4 product: a [T, K] (tokens), w [rows, K] (weights), both E2M1 codes with
+// an E4M3 scale per 16 columns.  Plain: out [T, N] bf16, rows = N.  Gated: w is
+// gate rows [0, N), up rows [N, 2N); q and sf [T, N] in NVFP4.
+struct Fp4GemmArgs {
+  const uint8_t *a;
+  const uint8_t *a_sf;
+  const uint8_t *w;
+  const uint8_t *w_sf;
+  const float *alpha;         // fp32 [1]
+  const float *global_scale;  // gated: fp32 [1], of the output
+  uint16_t *out;
+  uint8_t *q;
+  uint8_t *sf;
+  int32_t T;
+  int32_t N;                  // output columns
+  int32_t K;
+};
+GemmPlan plan_fp4_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms);
+cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, bool gated, int sms, cudaStream_t s);
+uint32_t read_fp4_gemm_status(bool reset);
+
 }  // namespace vg

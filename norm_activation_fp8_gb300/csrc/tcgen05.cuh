@@ -1,6 +1,6 @@
 // tcgen05.cuh -- the fifth-generation tensor cores and tensor-map TMA, as the
-// FP8 products use them: E4M3 operands in shared memory (K-major rows of 128
-// bytes in the 128-byte swizzle), fp32 accumulators in tensor memory.
+// products use them: E4M3 or E2M1 operands in shared memory (K-major rows of
+// 128 bytes in the 128-byte swizzle), fp32 accumulators in tensor memory.
 #pragma once
 
 #include <cstdint>
@@ -273,6 +273,51 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
                 "setp.ne.b32 p, %4, 0;\n\t"
                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}", ::"r"(d),
                 "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+                : "memory");
+}
+
+// NVFP4 operands: E2M1 codes, two a byte, laid out as above (a row of 128 bytes
+// is 256 codes, one product's K of 64 is 32 bytes), and an E4M3 scale per 16
+// codes in tensor memory.  The scales of one K of 64 and up to 128 operand rows
+// are 32 lanes x 4 columns: the four bytes of row r in lane r mod 32 (and the
+// same lane of the other three quarters), column r / 32.
+__host__ __device__ constexpr uint32_t nvfp4_product_desc(uint32_t m, uint32_t n) {
+  return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// Such scales in shared memory: 32 rows of 16 bytes (lane r mod 32), 512 bytes.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
+  constexpr uint64_t kStride = 8ull << 32;  // eight rows every 128 bytes
+  constexpr uint64_t kVersion = 1ull << 46;
+  return ((uint64_t)(smem_addr >> 4) & 0x3FFFull) | kStride | kVersion;
+}
+
+// Copies them to tensor memory (all four quarters), in order with the products
+// that the same thread issues.  PAIR: in both CTAs, from either's own shared
+// memory to its own tensor memory.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t dst, uint64_t src) {
+  VG_GROUP_FORM(PAIR, "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;",
+                "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;", ::"r"(dst), "l"(src)
+                : "memory");
+}
+
+// D (+)= (A sa) (B sb)^T over K = 64; sa, sb: tensor memory columns.  PAIR as
+// for mma_e4m3: either CTA has the scales of its own rows of A and of all rows
+// of B.
+template <bool PAIR>
+__device__ __forceinline__ void mma_nvfp4(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t sa,
+                                          uint32_t sb, bool accumulate) {
+  VG_GROUP_FORM(PAIR,
+                "{\n\t.reg .pred p;\n\t"
+                "setp.ne.b32 p, %6, 0;\n\t"
+                "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
+                "[%0], %1, %2, %3, [%4], [%5], p;\n\t}",
+                "{\n\t.reg .pred p;\n\t"
+                "setp.ne.b32 p, %6, 0;\n\t"
+                "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X "
+                "[%0], %1, %2, %3, [%4], [%5], p;\n\t}", ::"r"(d),
+                "l"(a), "l"(b), "r"(desc), "r"(sa), "r"(sb), "r"((uint32_t)accumulate)
                 : "memory");
 }
 

@@ -454,6 +454,40 @@ vg_status run_gemm(GemmArgs a, bool gated, int64_t T, int64_t N, int64_t K, int3
   return launch_fp8_gemm(a, gated, sms, (cudaStream_t)stream) == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 
+// NVFP4: rows of whole blocks, as the fused ops write them; a tensor of less
+// than 2^41 columns in all (the grid's limit).
+vg_status check_nvfp4_rows(int64_t T, int64_t n) {
+  if (T < 0 || T > INT32_MAX || n < 16 || n % 16 != 0 || n > VG_MAX_ROW ||
+      T > (1ll << 41) / n - 1)
+    return VG_ERR_BAD_SHAPE;
+  return VG_OK;
+}
+
+// The sizes both NVFP4 products refuse: along K whole products of the tensor
+// cores; output columns in multiples of `unit`.
+vg_status check_fp4_gemm(int64_t T, int64_t N, int64_t K, int64_t max_n, int64_t unit) {
+  if (T < 0 || T > VG_MAX_GEMM_TOKENS || N < unit || N % unit != 0 || N > max_n || K < 64 ||
+      K % 64 != 0 || K > VG_MAX_ROW)
+    return VG_ERR_BAD_SHAPE;
+  return VG_OK;
+}
+
+vg_status run_fp4_gemm(Fp4GemmArgs a, bool gated, int64_t T, int64_t N, int64_t K,
+                       vg_stream_t stream) {
+  if (misaligned(a.a, 16) || misaligned(a.w, 16) || misaligned(a.out, 16) || misaligned(a.q, 16) ||
+      misaligned(a.a_sf, 16) || misaligned(a.w_sf, 16) || misaligned(a.sf, 16) ||
+      misaligned(a.alpha, 4) || misaligned(a.global_scale, 4))
+    return VG_ERR_MISALIGNED;
+  int sms = 0;
+  const vg_status st = check_device(&sms);
+  if (st != VG_OK) return st;
+  clear_stale_error();
+  a.T = (int32_t)T;
+  a.N = (int32_t)N;
+  a.K = (int32_t)K;
+  return launch_fp4_gemm(a, gated, sms, (cudaStream_t)stream) == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+}
+
 }  // namespace
 
 }  // namespace vg
@@ -790,15 +824,99 @@ vg_status vg_silu_mul_nvfp4(uint8_t *q4, uint8_t *block_scale, const uint16_t *g
              : VG_ERR_CUDA;
 }
 
+vg_status vg_nvfp4_quantize(uint8_t *q4, uint8_t *block_scale, const uint16_t *x, int64_t x_stride,
+                            const float *global_scale, int64_t num_tokens, int64_t n,
+                            vg_stream_t stream) {
+  vg_status st = vg::check_nvfp4_rows(num_tokens, n);
+  if (st != VG_OK) return st;
+  if (x_stride < n || x_stride % 8 != 0) return VG_ERR_BAD_SHAPE;
+  if (num_tokens == 0) return VG_OK;
+  if (!q4 || !block_scale || !x || !global_scale) return VG_ERR_NULL_PTR;
+  if (vg::misaligned(q4, 16) || vg::misaligned(x, 16) || vg::misaligned(global_scale, 4))
+    return VG_ERR_MISALIGNED;
+  int sms = 0;
+  if ((st = vg::check_device(&sms)) != VG_OK) return st;
+  vg::clear_stale_error();
+  vg::Nvfp4Args a{};
+  a.x = x;
+  a.stride = x_stride;
+  a.q = q4;
+  a.sf = block_scale;
+  a.global_scale = global_scale;
+  a.T = num_tokens;
+  a.nch = n / 8;
+  a.pf_ctas = 2 * sms;
+  return vg::launch_nvfp4_quantize(a, (cudaStream_t)stream) == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+}
+
+vg_status vg_nvfp4_dequantize(uint16_t *out, const uint8_t *q4, const uint8_t *block_scale,
+                              const float *global_scale, int64_t num_tokens, int64_t n,
+                              vg_stream_t stream) {
+  vg_status st = vg::check_nvfp4_rows(num_tokens, n);
+  if (st != VG_OK || num_tokens == 0) return st;
+  if (!out || !q4 || !block_scale || !global_scale) return VG_ERR_NULL_PTR;
+  if (vg::misaligned(q4, 16) || vg::misaligned(out, 16) || vg::misaligned(global_scale, 4))
+    return VG_ERR_MISALIGNED;
+  int sms = 0;
+  if ((st = vg::check_device(&sms)) != VG_OK) return st;
+  vg::clear_stale_error();
+  vg::Nvfp4Args a{};
+  a.out = out;
+  a.q = const_cast<uint8_t *>(q4);  // read only in this direction
+  a.sf = const_cast<uint8_t *>(block_scale);
+  a.global_scale = global_scale;
+  a.T = num_tokens;
+  a.nch = n / 8;
+  return vg::launch_nvfp4_dequantize(a, (cudaStream_t)stream) == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+}
+
+vg_status vg_nvfp4_gemm(uint16_t *out, const uint8_t *a, const uint8_t *a_scale, const uint8_t *w,
+                        const uint8_t *w_scale, const float *alpha, int64_t num_tokens, int64_t n,
+                        int64_t k, vg_stream_t stream) {
+  const vg_status st = vg::check_fp4_gemm(num_tokens, n, k, VG_MAX_GEMM_COLUMNS, 8);
+  if (st != VG_OK || num_tokens == 0) return st;
+  if (!out || !a || !a_scale || !w || !w_scale || !alpha) return VG_ERR_NULL_PTR;
+  vg::Fp4GemmArgs g{};
+  g.a = a;
+  g.a_sf = a_scale;
+  g.w = w;
+  g.w_sf = w_scale;
+  g.alpha = alpha;
+  g.out = out;
+  return vg::run_fp4_gemm(g, false, num_tokens, n, k, stream);
+}
+
+vg_status vg_nvfp4_gemm_silu_mul_nvfp4(uint8_t *q4, uint8_t *block_scale, const uint8_t *a,
+                                       const uint8_t *a_scale, const uint8_t *w,
+                                       const uint8_t *w_scale, const float *alpha,
+                                       const float *global_scale, int64_t num_tokens, int64_t inter,
+                                       int64_t k, vg_stream_t stream) {
+  const vg_status st = vg::check_fp4_gemm(num_tokens, inter, k, VG_MAX_ROW, 64);
+  if (st != VG_OK || num_tokens == 0) return st;
+  if (!q4 || !block_scale || !a || !a_scale || !w || !w_scale || !alpha || !global_scale)
+    return VG_ERR_NULL_PTR;
+  vg::Fp4GemmArgs g{};
+  g.a = a;
+  g.a_sf = a_scale;
+  g.w = w;
+  g.w_sf = w_scale;
+  g.alpha = alpha;
+  g.global_scale = global_scale;
+  g.q = q4;
+  g.sf = block_scale;
+  return vg::run_fp4_gemm(g, true, num_tokens, inter, k, stream);
+}
+
 vg_status vg_device_status(uint32_t *flags, int32_t reset) {
   if (!flags) return VG_ERR_NULL_PTR;
   const uint32_t v = vg::read_norm_status(reset != 0), w = vg::read_silu_status(reset != 0),
                  r = vg::read_rope_status(reset != 0), m = vg::read_mla_status(reset != 0),
-                 g = vg::read_gemm_status(reset != 0);
+                 g = vg::read_gemm_status(reset != 0), n = vg::read_nvfp4_status(reset != 0),
+                 f = vg::read_fp4_gemm_status(reset != 0);
   if (v == 0xFFFFFFFFu || w == 0xFFFFFFFFu || r == 0xFFFFFFFFu || m == 0xFFFFFFFFu ||
-      g == 0xFFFFFFFFu)
+      g == 0xFFFFFFFFu || n == 0xFFFFFFFFu || f == 0xFFFFFFFFu)
     return VG_ERR_CUDA;
-  *flags = v | w | r | m | g;
+  *flags = v | w | r | m | g | n | f;
   return VG_OK;
 }
 
