@@ -74,22 +74,32 @@ EncodeTiled encoder() {
   return f;
 }
 
-// A row-major [rows, cols] tensor read or written in boxes of box_rows x box_cols.
+// A tensor of `rank` dimensions, innermost first, read or written in boxes;
+// strides in bytes, from the second dimension on.
 // The encoder is a driver call and wants a context: a host thread whose first
 // CUDA call this is has none yet, and setting its device makes it one.
-bool make_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *p, int64_t rows,
-              int64_t cols, int box_rows, int box_cols, CUtensorMapSwizzle swizzle) {
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(cols * size)};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, step[2] = {1, 1};
+inline bool make_map(CUtensorMap *m, CUtensorMapDataType type, const void *p, int rank,
+                     const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                     CUtensorMapSwizzle swizzle) {
+  const cuuint32_t step[4] = {1, 1, 1, 1};
   const EncodeTiled f = encoder();
   if (!f) return false;
   const auto encode = [&] {
-    return f(m, type, 2, const_cast<void *>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return f(m, type, (cuuint32_t)rank, const_cast<void *>(p), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   int dev = 0;
   return encode() || (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode());
+}
+
+// A row-major [rows, cols] tensor in boxes of box_rows x box_cols.
+inline bool make_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *p, int64_t rows,
+                     int64_t cols, int box_rows, int box_cols, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(cols * size)};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  return make_map(m, type, p, 2, dims, strides, box, swizzle);
 }
 
 // launch_pdl with thread-block clusters of `cluster` CTAs along x.

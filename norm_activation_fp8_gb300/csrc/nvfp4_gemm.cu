@@ -326,6 +326,301 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
   cluster_sync();  // nobody reads this CTA's sums any more
 }
 
+// ------------------------------------------------------------- tile kernel
+//
+// Pairs of CTAs, one CTA per SM, compute tiles of 256 tokens x 256 weight rows
+// (gated: 128 gate rows and the same 128 up rows, in turns of 16, so that a
+// thread has gate and up of a block side by side).  A CTA of the pair stages
+// its 128 tokens and one half of the weight rows; the scales of its tokens and
+// of all the weight rows.
+//   warp 0: TMA   warp 1: products   warps 2-5: scales   warps 6-13: epilogue
+// Two accumulators of 256 columns and the scales do not fit into 512 columns,
+// so the accumulators share kOverlap columns, which the epilogue reads first:
+// the next tile's products start when these are in registers.
+
+constexpr int kTileStages = 5;
+constexpr int kTileStageBytes = 2 * kRows * kRowBytes;  // of either CTA
+constexpr int kScaleWarps = 4, kOutWarps = 8, kTileThreads = 32 * (2 + kScaleWarps + kOutWarps);
+constexpr int kAcc = 256;       // columns of an accumulator
+constexpr int kOverlap = 64;    // shared by the two
+constexpr int kSfColumn = 2 * kAcc - kOverlap;  // first column of the scales
+static_assert(kSfColumn + 12 * kChunks <= 512, "tensor memory");
+constexpr int kTileGroup = 16;  // pairs' token tiles that share a sweep over the weight
+
+template <bool GATED>
+struct TileSmem {
+  uint8_t stage[kTileStages][kTileStageBytes];
+  uint8_t out[GATED ? 1 : kOutWarps][2][GATED ? 16 : 32 * 64];  // boxes of 32 rows x 32 columns
+  uint8_t a_sf[kTileStages][kChunks * kAtom], w_sf[kTileStages][2 * kChunks * kAtom];
+  uint64_t full[kTileStages], sf_full[kTileStages], empty[kTileStages];
+  uint64_t acc_full[2], acc_free, drain;
+  uint32_t tmem;
+  uint32_t failed;
+  VG_GEMM_NEVER
+};
+
+// The i-th tile: token tiles run fastest within groups of kTileGroup, so that
+// the tiles in flight share weight rows and the group's activations stay in L2
+// while the weight streams by.
+struct Tile {
+  int t0;  // first token of the pair
+  int n0;  // first output column
+};
+template <bool GATED>
+__device__ __forceinline__ Tile tile_at(uint32_t i, uint32_t num_t, uint32_t num_n) {
+  const uint32_t per_group = kTileGroup * num_n, g = i / per_group, r = i - g * per_group;
+  const uint32_t rows = min((uint32_t)kTileGroup, num_t - g * kTileGroup), n = r / rows;
+  return {(int)(g * kTileGroup + r - n * rows) * 2 * kRows, (int)n * (GATED ? kAcc / 2 : kAcc)};
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    fp4_gemm_tile_kernel(const Fp4GemmArgs a, const __grid_constant__ Fp4Maps maps, int num_t, int num_n) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  TileSmem<GATED> &sm = *reinterpret_cast<TileSmem<GATED> *>(raw);
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  const int num_k = (a.K + kStageK - 1) / kStageK;
+  const uint32_t tiles = (uint32_t)num_t * (uint32_t)num_n;
+  const uint32_t rank = cluster_rank(), first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int my_t = (int)rank * kRows;  // this CTA's tokens within the pair's
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&maps.a);
+    prefetch_tensormap(&maps.w);
+    if (!GATED) prefetch_tensormap(&maps.out);
+    for (int i = 0; i < kTileStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.sf_full[i], 2);  // a scale warp of either CTA (the first CTA's counts)
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.acc_full[i], 1);
+    mbar_init(&sm.acc_free, 2 * kOutWarps);  // of both CTAs (the first CTA's counts)
+    mbar_init(&sm.drain, 1);
+    VG_GEMM_NEVER_INIT(sm);
+    fence_mbar_init();
+    sm.failed = 0;
+  }
+  if (warp == 1) tmem_alloc<true>(&sm.tmem, 512);
+  tcgen05_fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's barriers are initialised
+  tcgen05_fence_after();
+  const uint32_t tmem = sm.tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+  uint32_t issued = 0;  // stages this CTA has filled (warp 0)
+
+  if (warp == 0) {
+    uint32_t s = 0, lap = 0;
+    bool ok = true;
+    for (uint32_t i = first; i < tiles && ok; i += pairs) {
+      const Tile t = tile_at<GATED>(i, num_t, num_n);
+      for (int kb = 0; kb < num_k; ++kb) {
+        if (lap > 0 && !(ok = warp_wait_phase(&sm.empty[s], (lap - 1) & 1, &sm.failed))) break;
+        if (elect_lane()) {
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kTileStageBytes);
+          uint8_t *p = sm.stage[s];
+          const uint32_t bar = cluster_addr(&sm.full[s], 0);
+          tma_load_2d_pair(p, &maps.a, kb * kRowBytes, t.t0 + my_t, bar);
+          if constexpr (GATED)
+            tma_load_4d_pair(p + kRows * kRowBytes, &maps.w, kb * kRowBytes, 0, 0,
+                             t.n0 / 16 + (int)rank * 4, bar);
+          else
+            tma_load_2d_pair(p + kRows * kRowBytes, &maps.w, kb * kRowBytes, t.n0 + (int)rank * kRows, bar);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == kTileStages) s = 0, ++lap;
+      }
+    }
+    // The last stages are released in both CTAs by products that the first one
+    // issued: neither CTA may end before these arrivals have landed.
+    for (uint32_t i = issued < kTileStages ? 0 : issued - kTileStages; i < issued && ok; ++i)
+      ok = warp_wait_phase(&sm.empty[i % kTileStages], (i / kTileStages) & 1, &sm.failed);
+  } else if (warp == 1 && rank == 0) {
+    constexpr uint32_t desc = nvfp4_product_desc(2 * kRows, kAcc);
+    uint32_t s = 0, lap = 0, j = 0;
+    bool ok = true;
+    for (uint32_t i = first; i < tiles && ok; i += pairs, ++j) {
+      const uint32_t acc = tmem + (j & 1) * (kAcc - kOverlap);
+      for (int kb = 0; kb < num_k; ++kb) {
+        const int chunks = min(kChunks, (a.K - kb * kStageK) / 64);
+        // operands, scales and (a tile's first stage) the accumulator: a third
+        // of the lanes wait for each
+        const int who = lane % 3;
+        if (!(ok = __all_sync(0xFFFFFFFFu,
+                              (who == 2 && (kb > 0 || j == 0)) ||
+                                  wait_phase(who == 2 ? &sm.acc_free : (who ? &sm.sf_full[s] : &sm.full[s]),
+                                             who == 2 ? (j - 1) & 1 : lap & 1, &sm.failed))))
+          break;
+        if (VG_GEMM_FORCED_TIMEOUT(sm, j == 0 && kb == 0)) {
+          sm.failed = 1;
+          ok = false;
+          break;
+        }
+        tcgen05_fence_after();
+        if (elect_lane()) {
+          const uint64_t da = operand_desc(smem_u32(sm.stage[s]));
+          const uint64_t dw = operand_desc(smem_u32(sm.stage[s] + kRows * kRowBytes));
+          const uint64_t sa = scale_desc(smem_u32(sm.a_sf[s])), sw = scale_desc(smem_u32(sm.w_sf[s]));
+          const uint32_t ta = tmem + kSfColumn, tw = ta + 4 * kChunks;
+          for (int c = 0; c < chunks; ++c) {
+            tmem_copy_scales<true>(ta + 4 * c, sa + c * (kAtom >> 4));
+            tmem_copy_scales<true>(tw + 8 * c, sw + c * (kAtom >> 4));
+            tmem_copy_scales<true>(tw + 8 * c + 4, sw + (kChunks + c) * (kAtom >> 4));
+          }
+          for (int c = 0; c < chunks; ++c)
+            mma_nvfp4<true>(acc, da + 2 * c, dw + 2 * c, desc, ta + 4 * c, tw + 8 * c, kb + c > 0);
+          mma_commit_pair(&sm.empty[s], 0);
+          if (kb == num_k - 1) mma_commit_pair(&sm.acc_full[j & 1], 0);
+        }
+        __syncwarp();
+        if (++s == kTileStages) s = 0, ++lap;
+      }
+    }
+    // Nothing is in flight once this arrives (at once, unless a wait gave up).
+    if (elect_lane()) mma_commit<true>(&sm.drain);
+    __syncwarp();
+    (void)mbar_wait_bounded(&sm.drain, 0);
+  } else if (warp >= 2 && warp < 2 + kScaleWarps) {
+    // Warp 2 + x has every fourth stage, counted over all tiles.
+    const bool wide = a.K % kStageK == 0;
+    const int64_t pitch = a.K / kNvfp4Block;
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t i = first; i < tiles && ok; i += pairs, it += (uint32_t)num_k) {
+      const Tile t = tile_at<GATED>(i, num_t, num_n);
+      const int row = t.t0 + my_t + lane;
+      // rows l + 32 j of the weight's 256: gated, 16 gate and 16 up rows a turn
+      const int col = GATED ? t.n0 + (lane & 15) : t.n0 + lane;
+      constexpr int kStep = GATED ? 16 : 32;
+      const uint8_t *pa = a.a_sf + row * pitch;
+      const uint8_t *pw = a.w_sf + ((GATED && lane >= 16 ? (int64_t)a.N : 0) + col) * pitch;
+      for (int kb = (int)((uint32_t)(warp - 2) - it & (kScaleWarps - 1)); kb < num_k; kb += kScaleWarps) {
+        const uint32_t n = it + (uint32_t)kb, s = n % kTileStages, lap = n / kTileStages;
+        const int chunks = min(kChunks, (a.K - kb * kStageK) / 64), x = kb * (kStageK / kNvfp4Block);
+        uint4 va[4], vw[2][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          va[j] = load_scales(pa + 32 * j * pitch + x, row + 32 * j < a.T, wide, chunks, a.a_sf, a_sf_extent(a));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int off = (4 * h + j) * kStep;
+            vw[h][j] = load_scales(pw + off * pitch + x, col + off < a.N, wide, chunks, a.w_sf,
+                                   w_sf_extent<GATED>(a));
+          }
+        }
+        if (lap > 0 && !(ok = warp_wait_phase(&sm.empty[s], (lap - 1) & 1, &sm.failed))) break;
+        store_scales(sm.a_sf[s], lane, va);
+        store_scales(sm.w_sf[s], lane, vw[0]);
+        store_scales(sm.w_sf[s] + kChunks * kAtom, lane, vw[1]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_release(cluster_addr(&sm.sf_full[s], 0));
+      }
+    }
+  } else if (warp >= 2 + kScaleWarps) {
+    const int quarter = warp & 3, half = (warp - 2 - kScaleWarps) >> 2;  // lanes, columns
+    const uint32_t free_bar = cluster_addr(&sm.acc_free, 0);
+    const float alpha = __ldg(a.alpha), gs = GATED ? __ldg(a.global_scale) : 0.f;
+    uint32_t j = 0;
+    for (uint32_t i = first; i < tiles; i += pairs, ++j) {
+      const Tile t = tile_at<GATED>(i, num_t, num_n);
+      const uint32_t b = j & 1;
+      if (!warp_wait_phase(&sm.acc_full[b], (j >> 1) & 1, &sm.failed)) break;
+      tcgen05_fence_after();
+      const uint32_t base =
+          tmem + ((uint32_t)(quarter * 32) << 16) + b * (kAcc - kOverlap) + half * (kAcc / 2);
+      const int t0 = t.t0 + my_t + quarter * 32;  // this warp's first token
+#pragma unroll 1
+      for (int p = 0; p < 2; ++p) {
+        // The 64 columns that the other accumulator shares come first: the top
+        // ones of the first, the bottom ones of the second.
+        const int c0 = (b ? p : 1 - p) * 64;
+        uint32_t v[2][32];
+        tmem_load(base + c0, v[0]);
+        tmem_load(base + c0 + 32, v[1]);
+        tmem_load_wait(v[0]);
+        tmem_load_wait(v[1]);
+        if (p == 0) {
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(free_bar);
+        }
+        if constexpr (!GATED) {
+          const int n = t.n0 + half * (kAcc / 2) + c0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // a box of 32 columns, 64 bytes a row
+            uint8_t *box = sm.out[warp - 2 - kScaleWarps][h];
+            if (lane == 0) tma_store_wait_read<1>();
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack_bf16x2_rn(alpha * __uint_as_float(v[h][8 * q + 2 * k]),
+                                      alpha * __uint_as_float(v[h][8 * q + 2 * k + 1]));
+              *reinterpret_cast<uint4 *>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (t0 < a.T && n + 32 * h < a.N) tma_store_2d(&maps.out, box, n + 32 * h, t0);
+              tma_store_commit();
+            }
+          }
+        } else {
+          const int n = t.n0 + (half * (kAcc / 2) + c0) / 2;
+          uint32_t codes[4], sf = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 16 gate columns, then up
+            float y[16], m = 0.f, r;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              y[k] = silu_mul(alpha * __uint_as_float(v[h][k]), alpha * __uint_as_float(v[h][16 + k]));
+              m = fmaxf(m, fabsf(y[k]));
+            }
+            const uint32_t code = block_code(m, gs, r);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float q[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) q[k] = y[8 * x + k] * gs * r;
+              codes[2 * h + x] = code ? quant_e2m1x8(q) : 0u;
+            }
+            sf |= code << (8 * h);
+          }
+          const int64_t token = t0 + lane;
+          if (token < a.T && n < a.N) {  // whole: n and N are multiples of 32 and 64
+            uint8_t *o = a.q + token * (a.N / 2) + n / 2;
+            if (VG_ACCESS_OK(g_fp4_gemm_status, o, 16, a.q, VG_ROWS(a.T) * (uint64_t)(a.N / 2)))
+              *reinterpret_cast<uint4 *>(o) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+            uint8_t *f = a.sf + token * (a.N / kNvfp4Block) + n / kNvfp4Block;
+            if (VG_ACCESS_OK(g_fp4_gemm_status, f, 2, a.sf, VG_ROWS(a.T) * (uint64_t)(a.N / kNvfp4Block)))
+              *reinterpret_cast<uint16_t *>(f) = (uint16_t)sf;
+          }
+        }
+      }
+    }
+    if (!GATED && lane == 0) tma_store_wait_read<0>();
+  }
+
+  __syncthreads();
+  if (sm.failed && warp == 0 && lane == 0) {  // the pair's copies in flight end here
+    atomicOr(&g_fp4_gemm_status, kErrWaitTimeout);
+    if (rank == 0)
+      for (uint32_t it = issued < kTileStages ? 0 : issued - kTileStages; it < issued; ++it)
+        (void)mbar_wait_bounded(&sm.full[it % kTileStages], (it / kTileStages) & 1);
+    // copies that the other CTA issued ahead of this one's count: a millisecond
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
+  cluster_sync();  // the pair is done
+  __syncwarp();
+  if (warp == 1) tmem_dealloc<true>(tmem, 512);
+}
+
 // -------------------------------------------------------------------- host
 
 template <bool GATED, int TN>
@@ -348,8 +643,39 @@ cudaError_t launch_stream(const Fp4GemmArgs &a, int splits, cudaStream_t s) {
 }
 
 template <bool GATED>
-cudaError_t launch_form(const Fp4GemmArgs &a, const GemmPlan &p, cudaStream_t s) {
+cudaError_t launch_tile(const Fp4GemmArgs &a, int sms, cudaStream_t s) {
+  static std::atomic<uint64_t> opted_in{0};
+  const cudaError_t e = opt_in_once(opted_in, (const void *)fp4_gemm_tile_kernel<GATED>);
+  if (e != cudaSuccess) return e;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  Fp4Maps maps;
+  if (!make_map(&maps.a, u8, 1, a.a, a.T, a.K / 2, kRows, kRowBytes, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  if constexpr (GATED) {
+    // byte of a row, row of a turn of 16, gate or up, turn
+    const cuuint64_t row = (cuuint64_t)a.K / 2;
+    const cuuint64_t dims[4] = {row, 16, 2, (cuuint64_t)a.N / 16};
+    const cuuint64_t strides[3] = {row, row * (cuuint64_t)a.N, row * 16};
+    const cuuint32_t box[4] = {kRowBytes, 16, 2, 4};
+    if (!make_map(&maps.w, u8, a.w, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+    maps.out = maps.a;  // not used: the codes are stored by threads
+  } else if (!make_map(&maps.w, u8, 1, a.w, a.N, a.K / 2, kRows, kRowBytes, CU_TENSOR_MAP_SWIZZLE_128B) ||
+             !make_map(&maps.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.out, a.T, a.N, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_64B)) {
+    return cudaErrorInvalidValue;
+  }
+  const int num_t = (a.T + 2 * kRows - 1) / (2 * kRows);
+  const int tile = GATED ? kAcc / 2 : kAcc, num_n = (a.N + tile - 1) / tile;
+  const int64_t tiles = (int64_t)num_t * num_n, pairs = tiles < sms / 2 ? tiles : sms / 2;
+  return launch_pdl_cluster(fp4_gemm_tile_kernel<GATED>, dim3((unsigned)(2 * pairs)), 2,
+                            dim3(kTileThreads), sizeof(TileSmem<GATED>), s, a, maps, num_t, num_n);
+}
+
+template <bool GATED>
+cudaError_t launch_form(const Fp4GemmArgs &a, const GemmPlan &p, int sms, cudaStream_t s) {
   switch (p.tn) {
+    case 0: return launch_tile<GATED>(a, sms, s);
     case 16: return launch_stream<GATED, 16>(a, p.splits, s);
     case 32: return launch_stream<GATED, 32>(a, p.splits, s);
     case 64: return launch_stream<GATED, 64>(a, p.splits, s);
@@ -366,13 +692,18 @@ GemmPlan plan_fp4_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
   const int64_t tiles = (N + tile - 1) / tile * ((T + p.tn - 1) / p.tn);
   const int64_t slots = (int64_t)sms * (p.tn <= 64 ? 2 : 1);
   p.splits = 1;
+  // (a first rule: tiles of 256 x 256 once they fill half of the pairs)
+  if (T > 128 && (T + 255) / 256 * ((N + 2 * tile - 1) / (2 * tile)) >= sms / 4) {
+    p.tn = 0;
+    return p;
+  }
   while (p.splits < kMaxSplit && 2 * p.splits <= blocks && tiles * p.splits * 2 <= slots) p.splits *= 2;
   return p;
 }
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, bool gated, int sms, cudaStream_t s) {
   const GemmPlan p = plan_fp4_gemm(a.T, a.N, a.K, gated, sms);
-  return gated ? launch_form<true>(a, p, s) : launch_form<false>(a, p, s);
+  return gated ? launch_form<true>(a, p, sms, s) : launch_form<false>(a, p, sms, s);
 }
 
 uint32_t read_fp4_gemm_status(bool reset) {

@@ -30,6 +30,16 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
       : "memory");
 }
 
+// The same of a 4-D tensor.
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
+                                                 int32_t z, int32_t w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // One lane of a converged warp, the same one each time.  The warps that issue
 // copies and products run their loops as whole warps and elect the issuing
 // lane at the instruction: with the loop itself on one lane the compiler must
@@ -97,6 +107,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
 // cycles here.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same behind writes to shared memory, which the other side reads.
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Four fp32 values at a cluster address.

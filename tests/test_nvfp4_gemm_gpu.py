@@ -103,6 +103,7 @@ PLAIN = [  # T, N, K
     (65, 640, 256), (100, 264, 32768), (127, 136, 576), (128, 256, 128), (129, 384, 1024),
     (200, 4096, 4096), (256, 4096, 2048), (257, 248, 448), (300, 6144, 1024), (513, 1032, 512),
     (1000, 2056, 832), (2049, 4096, 640), (4100, 264, 256), (512, 1024, 8192),
+    (130, 10248, 192), (700, 9736, 448), (4100, 2056, 64), (385, 8192, 16384), (2304, 5120, 1088),
 ]
 
 
@@ -131,6 +132,7 @@ GATED = [  # T, I, K
     (17, 192, 128), (33, 1024, 704), (57, 2048, 2048), (64, 384, 32768), (65, 320, 512), (127, 640, 256),
     (128, 128, 384), (129, 1152, 576), (200, 14336, 256), (256, 2048, 1024), (300, 64, 896),
     (513, 1024, 512), (1000, 960, 640), (2049, 2048, 256), (4100, 192, 128),
+    (300, 14400, 256), (515, 4160, 1088), (4100, 1344, 64), (257, 8192, 2048),
 ]
 
 
