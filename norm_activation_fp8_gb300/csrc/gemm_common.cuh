@@ -37,6 +37,12 @@ __device__ __forceinline__ bool warp_wait_phase(uint64_t *bar, uint32_t parity, 
   return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, failed));
 }
 
+// The same where a look at the phase (mbar_try_wait) was taken some time ago.
+__device__ __forceinline__ bool warp_wait_phase(bool seen, uint64_t *bar, uint32_t parity,
+                                                volatile uint32_t *failed) {
+  return __all_sync(0xFFFFFFFFu, seen) || warp_wait_phase(bar, parity, failed);
+}
+
 // A barrier of `threads` threads that tells all of them whether any passed true.
 __device__ __forceinline__ bool named_sync_or(int id, int threads, bool p) {
   uint32_t any;
