@@ -69,6 +69,13 @@ __device__ __forceinline__ void store_scales(uint8_t *dst, int lane, const uint4
   p[3 * kAtom / 16] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
 }
 
+// Lane 4 r + p's value to lane 8 p + r.
+__device__ __forceinline__ uint4 swap_lanes(const uint4 &v, int lane) {
+  const int from = (lane & 7) * 4 + (lane >> 3);
+  return make_uint4(__shfl_sync(0xFFFFFFFFu, v.x, from), __shfl_sync(0xFFFFFFFFu, v.y, from),
+                    __shfl_sync(0xFFFFFFFFu, v.z, from), __shfl_sync(0xFFFFFFFFu, v.w, from));
+}
+
 // SiLU(g) u with the accurate exponential and division: an ulp or two, so that
 // codes move only where the value is that near a border.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
@@ -340,14 +347,15 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
 // thread has gate and up of a block side by side).  A CTA of the pair stages
 // its 128 tokens and one half of the weight rows; the scales of its tokens and
 // of all the weight rows.
-//   warp 0: TMA   warp 1: products   warps 2-5: scales   warps 6-13: epilogue
+//   warp 0: TMA   warp 1: products   warps 2-7: scales   warps 8-15: epilogue
 // Two accumulators of 256 columns and the scales do not fit into 512 columns,
 // so the accumulators share kOverlap columns, which the epilogue reads first:
 // the next tile's products start when these are in registers.
 
 constexpr int kTileStages = 5;
 constexpr int kTileStageBytes = 2 * kRows * kRowBytes;  // of either CTA
-constexpr int kScaleWarps = 4, kOutWarps = 8, kTileThreads = 32 * (2 + kScaleWarps + kOutWarps);
+constexpr int kScaleWarps = 6, kOutWarps = 8, kTileThreads = 32 * (2 + kScaleWarps + kOutWarps);
+constexpr int kGroup = 4;       // stages whose scales are loaded at once
 constexpr int kAcc = 256;       // columns of an accumulator
 constexpr int kOverlap = 64;    // shared by the two: what the epilogue reads first
 constexpr int kSfColumn = 2 * kAcc - kOverlap;  // first column of the scales
@@ -357,9 +365,9 @@ constexpr int kTileGroup = 16;  // pairs' token tiles that share a sweep over th
 template <bool GATED>
 struct TileSmem {
   uint8_t stage[kTileStages][kTileStageBytes];
-  uint8_t out[GATED ? 1 : kOutWarps][2][GATED ? 16 : 32 * 64];  // boxes of 32 rows x 32 columns
-  uint8_t a_sf[kTileStages][kChunks * kAtom], w_sf[kTileStages][2 * kChunks * kAtom];
-  uint64_t full[kTileStages], empty[kTileStages];
+  uint8_t out[GATED ? 1 : kOutWarps][GATED ? 16 : 32 * 64];  // boxes of 32 rows x 32 columns
+  uint8_t sf[2][kGroup][3][kChunks * kAtom];  // of the tokens, of the weight's halves
+  uint64_t full[kTileStages], empty[kTileStages], sf_full[2], sf_empty[2];
   uint64_t acc_full[2], acc_free, drain;
   uint32_t tmem;
   uint32_t failed;
@@ -396,10 +404,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     prefetch_tensormap(&maps.w);
     if (!GATED) prefetch_tensormap(&maps.out);
     for (int i = 0; i < kTileStages; ++i) {
-      mbar_init(&sm.full[i], 3);  // copies, a scale warp of either CTA (the first CTA's counts)
+      mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.acc_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.acc_full[i], 1);
+      mbar_init(&sm.sf_full[i], 6);  // three warps of both CTAs (the first CTA's counts)
+      mbar_init(&sm.sf_empty[i], 1);
+    }
     mbar_init(&sm.acc_free, 2 * kOutWarps);  // of both CTAs (the first CTA's counts)
     mbar_init(&sm.drain, 1);
     VG_GEMM_NEVER_INIT(sm);
@@ -445,12 +457,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = warp_wait_phase(&sm.empty[i % kTileStages], (i / kTileStages) & 1, &sm.failed);
   } else if (warp == 1 && rank == 0) {
     constexpr uint32_t desc = nvfp4_product_desc(2 * kRows, kAcc);
-    uint32_t s = 0, lap = 0, j = 0;
-    bool ok = true, seen = false;
+    uint32_t s = 0, lap = 0, j = 0, group = 0;
+    bool ok = true, seen = false, seen_sf = false;
     for (uint32_t i = first; i < tiles && ok; i += pairs, ++j) {
       const uint32_t acc = tmem + (j & 1) * (kAcc - kOverlap);
       if (j > 0 && !(ok = warp_wait_phase(&sm.acc_free, (j - 1) & 1, &sm.failed))) break;
       for (int kb = 0; kb < num_k; ++kb) {
+        const int part = kb % kGroup;
+        if (part == 0 && !(ok = warp_wait_phase(seen_sf, &sm.sf_full[group & 1], (group >> 1) & 1, &sm.failed)))
+          break;
         if (!(ok = warp_wait_phase(seen, &sm.full[s], lap & 1, &sm.failed))) break;
         if (VG_GEMM_FORCED_TIMEOUT(sm, j == 0 && kb == 0)) {
           sm.failed = 1;
@@ -463,10 +478,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // A look at the next stage while this one's products are issued (even
         // a wait for nothing takes some 160 cycles).
         seen = mbar_try_look(&sm.full[s], lap & 1);
+        const bool last = part == kGroup - 1 || kb == num_k - 1;
+        if (last) seen_sf = mbar_try_look(&sm.sf_full[(group + 1) & 1], ((group + 1) >> 1) & 1);
         if (elect_lane()) {
           const uint64_t da = operand_desc(smem_u32(sm.stage[now]));
           const uint64_t dw = operand_desc(smem_u32(sm.stage[now] + kRows * kRowBytes));
-          const uint64_t sa = scale_desc(smem_u32(sm.a_sf[now])), sw = scale_desc(smem_u32(sm.w_sf[now]));
+          const uint64_t sa = scale_desc(smem_u32(sm.sf[group & 1][part][0]));
+          const uint64_t sw = sa + (kChunks * kAtom >> 4);
           const uint32_t ta = tmem + kSfColumn, tw = ta + 4 * kChunks;
           // Each product right behind its own scales (all of a stage's scales
           // first: 4390 instead of 5270 TFLOP/s): they are copied while the
@@ -485,9 +503,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int c = 0; c < a.K % kStageK / 64; ++c) issue(c);
           }
           mma_commit_pair(&sm.empty[now], 0);
+          if (last) mma_commit_pair(&sm.sf_empty[group & 1], 0);
           if (kb == num_k - 1) mma_commit_pair(&sm.acc_full[j & 1], 0);
         }
         __syncwarp();
+        group += last;
       }
     }
     // Nothing is in flight once this arrives (at once, unless a wait gave up).
@@ -495,42 +515,52 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncwarp();
     (void)mbar_wait_bounded(&sm.drain, 0);
   } else if (warp >= 2 && warp < 2 + kScaleWarps) {
-    // Warp 2 + x has every fourth stage, counted over all tiles.
-    const bool wide = a.K % kStageK == 0;
+    // Scales of 128 rows (tokens, either half of the weight's), every other
+    // group of kGroup stages, counted over all tiles.  A row's scales of a
+    // group are 64 bytes: four lanes load them, so that a load of the warp
+    // touches eight rows (a lane a row and stage: 32 lines a load, of which the
+    // SM asks for one in about two cycles; 4876 instead of 7700 TFLOP/s).
+    // Then the lanes change places: eight rows of one stage side by side.
+    const int role = (warp - 2) % 3, turn = (warp - 2) / 3;
+    const bool wide = a.K % kStageK == 0, tokens = role == 0, pairs16 = GATED && !tokens;
     const int64_t pitch = a.K / kNvfp4Block;
-    uint32_t it = 0;
+    const uint8_t *src = tokens ? a.a_sf : a.w_sf;
+    const uint64_t extent = tokens ? a_sf_extent(a) : w_sf_extent<GATED>(a);
+    const int limit = tokens ? a.T : a.N;
+    uint32_t group = 0, lap = 0;  // groups so far, this warp's
     bool ok = true;
-    for (uint32_t i = first; i < tiles && ok; i += pairs, it += (uint32_t)num_k) {
+    for (uint32_t i = first; i < tiles && ok; i += pairs) {
       const Tile t = tile_at<GATED>(i, num_t, num_n);
-      const int row = t.t0 + my_t + lane;
-      // rows l + 32 j of the weight's 256: gated, 16 gate and 16 up rows a turn
-      const int col = GATED ? t.n0 + (lane & 15) : t.n0 + lane;
-      constexpr int kStep = GATED ? 16 : 32;
-      const uint8_t *pa = a.a_sf + row * pitch;
-      const uint8_t *pw = a.w_sf + ((GATED && lane >= 16 ? (int64_t)a.N : 0) + col) * pitch;
-      for (int kb = (int)((uint32_t)(warp - 2) - it & (kScaleWarps - 1)); kb < num_k; kb += kScaleWarps) {
-        const uint32_t n = it + (uint32_t)kb, s = n % kTileStages, lap = n / kTileStages;
-        const int chunks = min(kChunks, (a.K - kb * kStageK) / 64), x = kb * (kStageK / kNvfp4Block);
-        uint4 va[4], vw[2][4];
+      // gated, a block's rows are turns of 16 gate and 16 up rows
+      const int row = (tokens ? t.t0 + my_t : t.n0 + (role - 1) * (pairs16 ? kRows / 2 : kRows)) + (lane >> 2);
+      for (int k = 0; k < num_k; k += kGroup, ++group) {
+        if ((int)(group & 1) != turn) continue;
+        const int kb = k + (lane & 3), chunks = min(kChunks, (a.K - kb * kStageK) / 64);
+        uint4 v[4][4];  // row 8 x + lane / 4 of 32, 32-row part
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          va[j] = load_scales(pa + 32 * j * pitch + x, row + 32 * j < a.T, wide, chunks, a.a_sf, a_sf_extent(a));
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int off = (4 * h + j) * kStep;
-            vw[h][j] = load_scales(pw + off * pitch + x, col + off < a.N, wide, chunks, a.w_sf,
-                                   w_sf_extent<GATED>(a));
+          for (int j = 0; j < 4; ++j) {
+            const int r = row + (pairs16 ? 16 * j + 8 * (x & 1) : 32 * j + 8 * x);
+            const int64_t line = r + (pairs16 && x >= 2 ? (int64_t)a.N : 0);
+            v[x][j] = load_scales(src + line * pitch + kb * (kStageK / kNvfp4Block), r < limit && kb < num_k,
+                                  wide, chunks, src, extent);
           }
+        if (lap > 0 && !(ok = warp_wait_phase(&sm.sf_empty[turn], (lap - 1) & 1, &sm.failed))) break;
+        ++lap;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[x][j] = swap_lanes(v[x][j], lane);
+          store_scales(sm.sf[turn][lane >> 3][role], 8 * x + (lane & 7), v[x]);
         }
-        if (lap > 0 && !(ok = warp_wait_phase(&sm.empty[s], (lap - 1) & 1, &sm.failed))) break;
-        store_scales(sm.a_sf[s], lane, va);
-        store_scales(sm.w_sf[s], lane, vw[0]);
-        store_scales(sm.w_sf[s] + kChunks * kAtom, lane, vw[1]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_written(cluster_addr(&sm.full[s], 0));
+        if (lane == 0) mbar_arrive_cluster_written(cluster_addr(&sm.sf_full[turn], 0));
       }
     }
+    // (as for the stages: the last release has landed)
+    if (lap > 0 && ok) (void)warp_wait_phase(&sm.sf_empty[turn], (lap - 1) & 1, &sm.failed);
   } else if (warp >= 2 + kScaleWarps) {
     const int quarter = warp & 3, half = (warp - 2 - kScaleWarps) >> 2;  // lanes, columns
     const uint32_t free_bar = cluster_addr(&sm.acc_free, 0);
@@ -563,8 +593,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int n = t.n0 + half * (kAcc / 2) + c0;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // a box of 32 columns, 64 bytes a row
-            uint8_t *box = sm.out[warp - 2 - kScaleWarps][h];
-            if (lane == 0) tma_store_wait_read<1>();
+            uint8_t *box = sm.out[warp - 2 - kScaleWarps];
+            if (lane == 0) tma_store_wait_read<0>();
             __syncwarp();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
