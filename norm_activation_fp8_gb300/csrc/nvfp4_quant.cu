@@ -133,7 +133,8 @@ __device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
 __global__ void __launch_bounds__(kThreads) nvfp4_dequantize_kernel(const Nvfp4Args a) {
   const int64_t total = a.T * a.nch, first = (int64_t)blockIdx.x * (kThreads * kPer);
   pdl_wait();
-  const float gs = __ldg(a.global_scale);
+  const float gs = __ldg(a.global_scale), inv = __frcp_rn(gs);
+  const bool far = !(gs > 0x1p-100f && gs < 0x1p100f);
   uint32_t c[kPer], s[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
@@ -145,7 +146,10 @@ __global__ void __launch_bounds__(kThreads) nvfp4_dequantize_kernel(const Nvfp4A
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int64_t i = first + k * kThreads + threadIdx.x;
-    const float r = __fdiv_rn(e4m3_value(s[k]), gs);
+    // decode(sf) / gs, correctly rounded: one step from the reciprocal (the
+    // division itself takes its slow way for a zero scale)
+    const float d = e4m3_value(s[k]), q = d * inv;
+    const float r = far ? __fdiv_rn(d, gs) : fmaf(fmaf(-q, gs, d), inv, q);
     const float2 r2 = make_float2(r, r);
     uint32_t o[4];
 #pragma unroll
