@@ -4,12 +4,11 @@
 //   q  = e2m1(x gs / decode(sf)); +0 where sf is 0
 //   back: bf16(e2m1 value * (decode(sf) / gs))
 //
-// Both directions are elementwise but for a block's maximum, so the tensor is
-// one run of chunks of eight columns (16 bytes of bf16, four of codes): a lane
-// takes a chunk, two neighbouring lanes a block.  Every code is the one that
-// the exact value rounds to, at next to no cost: the fp32 values decide where
-// they are far enough from a border, which a second conversion tells, and
-// exact remainders where they are not.
+// Both directions are elementwise but for a block's maximum, so a tensor is one
+// run of blocks (32 bytes of bf16, eight of codes, a lane each) or, on the way
+// back, of half blocks.  Every code is the one that the exact value rounds to:
+// the fp32 values decide where they are far enough from a border, which a
+// second conversion tells, and exact remainders where they are not.
 #include "common.cuh"
 #include "launch.h"
 #include "nvfp4.cuh"
@@ -21,97 +20,114 @@ __device__ uint32_t g_nvfp4_status;
 
 namespace {
 
-constexpr int kThreads = 256, kPer = 4;  // chunks a thread
+constexpr int kThreads = 256;
+constexpr int kBlocks = 2;  // quantise: blocks of 16 columns a thread
+constexpr int kChunks = 4;  // read back: chunks of 8 columns a thread
 
 __device__ __forceinline__ uint64_t codes_extent(const Nvfp4Args &a) { return VG_ROWS(a.T) * (uint64_t)a.nch * 4; }
 __device__ __forceinline__ uint64_t scales_extent(const Nvfp4Args &a) { return VG_ROWS(a.T) * (uint64_t)a.nch / 2; }
 
-__device__ __forceinline__ float e2m1_level(uint32_t c) {  // of a code without its sign
-  return c < 4 ? 0.5f * (float)c : (c < 6 ? (float)(c - 2) : (float)(2 * c - 8));
-}
-
-// The code of y gs / d where the fp32 quotient lies next to a midpoint m of
-// two levels: y gs = p + e exactly, m d is exact (three times four bits), and
-// so is its difference from a p that near.
-__device__ __noinline__ uint32_t e2m1_exact(float y, float gs, float d) {
-  const float a = fabsf(y), p = a * gs, e = fmaf(a, gs, -p), v = p * __frcp_rn(d);
-  const float two[8] = {v * (1.0f - 0x1p-20f), v * (1.0f + 0x1p-20f)};
-  const uint32_t cc = quant_e2m1x8(two), lo = cc & 7u, hi = (cc >> 4) & 7u;
-  uint32_t c = lo;
-  if (lo != hi) {
-    const float diff = p - 0.5f * (e2m1_level(lo) + e2m1_level(hi)) * d;
-    const float s = diff != 0.f ? diff : e;  // |e| is at most half an ulp of p
-    c = s > 0.f || (s == 0.f && (lo & 1u)) ? hi : lo;
+// 32 bytes, read once: one load (32-byte aligned), or two.
+template <bool WIDE>
+__device__ __forceinline__ void ld_block(const uint16_t *p, uint32_t (&w)[8]) {
+  if constexpr (WIDE) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
-  return c | (__float_as_uint(y) >> 31 << 3);
-}
-__device__ __noinline__ uint32_t e2m1x8_exact(uint4 x, float gs, float d) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t r = 0;
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i)
-    r |= e2m1_exact(i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]), gs, d) << (4 * i);
-  return r;
 }
 
-// FLAT: the rows follow one another without a gap.
-template <bool FLAT>
+// Which of two neighbouring codes X = gs v rounds to on a grid that is `unit`
+// times as wide: gs v = p + e exactly, mid (the codes' midpoint) times unit is
+// exact (few bits), and so is its difference from a p that near.
+__device__ __forceinline__ bool above_midpoint(float v, float gs, float p, float mid, float unit, uint32_t lo) {
+  const float e = fmaf(v, gs, -p), diff = p - mid * unit;  // |e| is at most half an ulp of p
+  const float s = diff != 0.f ? diff : e;
+  return s > 0.f || (s == 0.f && (lo & 1u));  // a tie: the even code
+}
+
+// Settles the codes of eight columns where the two words of codes differ: scaled
+// quotients next to a midpoint.  (A call: it keeps the rest's registers free,
+// and a tensor's scale of 6 * 448 over its largest magnitude makes quotients
+// of bf16 numbers that lie on a midpoint or a rounding beside it common.)
+__device__ __noinline__ uint32_t settle(uint32_t lo, uint32_t hi, uint32_t w0, uint32_t w1, uint32_t w2,
+                                        uint32_t w3, float gs, float d) {
+  uint32_t diff = lo ^ hi;
+  while (diff) {
+    const int i = (__ffs((int)diff) - 1) >> 2;
+    const uint32_t w = i < 4 ? (i < 2 ? w0 : w1) : (i < 6 ? w2 : w3);
+    const float v = fabsf(i & 1 ? bf16_hi(w) : bf16_lo(w));
+    const uint32_t c = (lo >> (4 * i)) & 7u;  // the lower code: its midpoint with the next
+    const float mid = c < 4 ? 0.5f * (float)c + 0.25f : (c < 6 ? (float)c - 1.5f : 5.0f);
+    if (above_midpoint(v, gs, v * gs, mid, d, c)) lo += 1u << (4 * i);
+    diff &= ~(15u << (4 * i));
+  }
+  return lo;
+}
+
+// A lane a block.  FLAT: the rows follow one another without a gap.
+template <bool FLAT, bool WIDE>
 __global__ void __launch_bounds__(kThreads) nvfp4_quantize_kernel(const Nvfp4Args a) {
-  const int64_t total = a.T * a.nch, first = (int64_t)blockIdx.x * (kThreads * kPer);
+  const int64_t blocks = a.nch / 2, total = a.T * blocks, first = (int64_t)blockIdx.x * (kThreads * kBlocks);
   if (FLAT && threadIdx.x == 0 && blockIdx.x < (unsigned)a.pf_ctas) {
-    const int64_t n = total - first < kThreads * kPer ? total - first : kThreads * kPer;
-    prefetch_l2(a.x + first * kElemsPerChunk, (uint32_t)n * 16u);
+    const int64_t n = total - first < kThreads * kBlocks ? total - first : kThreads * kBlocks;
+    prefetch_l2(a.x + first * kNvfp4Block, (uint32_t)n * 32u);
   }
   pdl_wait();
   const float gs = __ldg(a.global_scale);
-  uint4 v[kPer];
+  uint32_t w[kBlocks][8];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
+  for (int k = 0; k < kBlocks; ++k) {
     const int64_t i = first + k * kThreads + threadIdx.x;
-    int64_t at = i * kElemsPerChunk;
+    int64_t at = i * kNvfp4Block;
     if (!FLAT) {
-      const int64_t row = total < (1ll << 32) ? (int64_t)((uint32_t)i / (uint32_t)a.nch) : i / a.nch;
-      at = row * a.stride + (i - row * a.nch) * kElemsPerChunk;
+      const int64_t row = total < (1ll << 32) ? (int64_t)((uint32_t)i / (uint32_t)blocks) : i / blocks;
+      at = row * a.stride + (i - row * blocks) * kNvfp4Block;
     }
-    v[k] = i < total ? ld_stream_ro(a.x + at) : make_uint4(0, 0, 0, 0);
+    if (i < total) ld_block<WIDE>(a.x + at, w[k]);
+    else
+      for (int j = 0; j < 8; ++j) w[k][j] = 0;
   }
   pdl_launch_dependents();
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
+  for (int k = 0; k < kBlocks; ++k) {
     const int64_t i = first + k * kThreads + threadIdx.x;
-    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-    float2 y[4];
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      y[j] = bf16x2_to_f2(w[j]);
-      m = fmax3(m, fabsf(y[j].x), fabsf(y[j].y));
+    for (int j = 0; j < 8; ++j) m = fmax3(m, fabsf(bf16_lo(w[k][j])), fabsf(bf16_hi(w[k][j])));
+    // p / 6 to 2^-22: where the two conversions agree, so does the exact value's
+    const float p = m * gs, x = p * (1.0f / kE2M1Max);
+    const uint32_t cc = cvt_e4m3x2(x * (1.0f - 0x1p-21f), x * (1.0f + 0x1p-21f));
+    uint32_t code = cc & 0xFFu;
+    if (code != cc >> 8) {
+      const float mid = 0.5f * (e4m3_value(code) + e4m3_value(cc >> 8));
+      if (above_midpoint(m, gs, p, mid, kE2M1Max, code)) code = cc >> 8;
     }
-    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    const float p = m * gs;
-    const uint32_t code = e4m3_code_settled(p * (1.0f / kE2M1Max), [&] {
-      const float e = fmaf(m, gs, -p), xh = __fdiv_rn(p, kE2M1Max);
-      const float xl = __fdiv_rn(fmaf(-xh, kE2M1Max, p) + e, kE2M1Max);
-      const float x = xh + xl;
-      return e4m3_code_df(x, xl - (x - xh));
-    });
     const float d = e4m3_value(code), r = code ? __frcp_rn(d) : 0.f;
-    const float2 g2 = make_float2(gs, gs), r2 = make_float2(r, r);
-    const float2 dn = make_float2(1.0f - 0x1p-21f, 1.0f - 0x1p-21f);
-    const float2 up = make_float2(1.0f + 0x1p-21f, 1.0f + 0x1p-21f);
-    float lo[8], hi[8];
+    const float2 g2 = make_float2(gs, gs);
+    const float dn = r * (1.0f - 0x1p-20f), up = r * (1.0f + 0x1p-20f);
+    uint32_t q[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 q = f2_mul(f2_mul(y[j], g2), r2), l = f2_mul(q, dn), h = f2_mul(q, up);
-      lo[2 * j] = l.x, lo[2 * j + 1] = l.y, hi[2 * j] = h.x, hi[2 * j + 1] = h.y;
+    for (int h = 0; h < 2; ++h) {  // (y gs) / d to 2^-21, the same way
+      float lo[8], hi[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = f2_mul(bf16x2_to_f2(w[k][4 * h + j]), g2);
+        const float2 l = f2_mul(y, make_float2(dn, dn)), u = f2_mul(y, make_float2(up, up));
+        lo[2 * j] = l.x, lo[2 * j + 1] = l.y, hi[2 * j] = u.x, hi[2 * j + 1] = u.y;
+      }
+      const uint32_t cl = quant_e2m1x8(lo), ch = quant_e2m1x8(hi);
+      q[h] = cl == ch ? cl
+                      : settle(cl, ch, w[k][4 * h], w[k][4 * h + 1], w[k][4 * h + 2], w[k][4 * h + 3], gs, d);
+      if (code == 0) q[h] = 0;
     }
-    uint32_t codes = quant_e2m1x8(lo);
-    if (codes != quant_e2m1x8(hi)) codes = e2m1x8_exact(v[k], gs, d);
-    if (code == 0) codes = 0;
     if (i < total) {
-      if (VG_ACCESS_OK(g_nvfp4_status, a.q + i * 4, 4, a.q, codes_extent(a))) st_stream(a.q + i * 4, codes);
-      uint8_t *s = a.sf + (i >> 1);
-      if (!(i & 1) && VG_ACCESS_OK(g_nvfp4_status, s, 1, a.sf, scales_extent(a))) *s = (uint8_t)code;
+      if (VG_ACCESS_OK(g_nvfp4_status, a.q + i * 8, 8, a.q, codes_extent(a)))
+        st_stream(a.q + i * 8, make_uint2(q[0], q[1]));
+      if (VG_ACCESS_OK(g_nvfp4_status, a.sf + i, 1, a.sf, scales_extent(a))) a.sf[i] = (uint8_t)code;
     }
   }
 }
@@ -131,20 +147,20 @@ __device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
 }
 
 __global__ void __launch_bounds__(kThreads) nvfp4_dequantize_kernel(const Nvfp4Args a) {
-  const int64_t total = a.T * a.nch, first = (int64_t)blockIdx.x * (kThreads * kPer);
+  const int64_t total = a.T * a.nch, first = (int64_t)blockIdx.x * (kThreads * kChunks);
   pdl_wait();
   const float gs = __ldg(a.global_scale), inv = __frcp_rn(gs);
   const bool far = !(gs > 0x1p-100f && gs < 0x1p100f);
-  uint32_t c[kPer], s[kPer];
+  uint32_t c[kChunks], s[kChunks];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
+  for (int k = 0; k < kChunks; ++k) {
     const int64_t i = first + k * kThreads + threadIdx.x;
     c[k] = i < total ? __ldg(reinterpret_cast<const uint32_t *>(a.q) + i) : 0u;
     s[k] = i < total ? __ldg(a.sf + (i >> 1)) : 0u;
   }
   pdl_launch_dependents();
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
+  for (int k = 0; k < kChunks; ++k) {
     const int64_t i = first + k * kThreads + threadIdx.x;
     // decode(sf) / gs, correctly rounded: one step from the reciprocal (the
     // division itself takes its slow way for a zero scale)
@@ -166,13 +182,17 @@ __global__ void __launch_bounds__(kThreads) nvfp4_dequantize_kernel(const Nvfp4A
 }  // namespace
 
 cudaError_t launch_nvfp4_quantize(const Nvfp4Args &a, cudaStream_t s) {
-  const dim3 g((unsigned)((a.T * a.nch + kThreads * kPer - 1) / (kThreads * kPer))), b(kThreads);
-  return a.stride == a.nch * kElemsPerChunk ? launch_pdl(nvfp4_quantize_kernel<true>, g, b, 0, s, a)
-                                            : launch_pdl(nvfp4_quantize_kernel<false>, g, b, 0, s, a);
+  const dim3 g((unsigned)((a.T * (a.nch / 2) + kThreads * kBlocks - 1) / (kThreads * kBlocks))), b(kThreads);
+  const bool flat = a.stride == a.nch * kElemsPerChunk || a.T == 1;
+  const bool wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 && (flat || a.stride % 16 == 0);
+  return flat ? (wide ? launch_pdl(nvfp4_quantize_kernel<true, true>, g, b, 0, s, a)
+                      : launch_pdl(nvfp4_quantize_kernel<true, false>, g, b, 0, s, a))
+              : (wide ? launch_pdl(nvfp4_quantize_kernel<false, true>, g, b, 0, s, a)
+                      : launch_pdl(nvfp4_quantize_kernel<false, false>, g, b, 0, s, a));
 }
 
 cudaError_t launch_nvfp4_dequantize(const Nvfp4Args &a, cudaStream_t s) {
-  const dim3 g((unsigned)((a.T * a.nch + kThreads * kPer - 1) / (kThreads * kPer))), b(kThreads);
+  const dim3 g((unsigned)((a.T * a.nch + kThreads * kChunks - 1) / (kThreads * kChunks))), b(kThreads);
   return launch_pdl(nvfp4_dequantize_kernel, g, b, 0, s, a);
 }
 
