@@ -30,6 +30,7 @@ constexpr int kChunks = kStageK / 64;     // products per stage
 constexpr int kRowBytes = kStageK / 2;
 constexpr int kRows = 128;                // rows of a stage's larger operand
 constexpr int kAtom = 512;                // bytes of the scales of 128 rows and a K of 64
+constexpr int kMaxSplit = 8;              // shares of K, a CTA each (stream kernel), of a cluster
 
 struct Fp4Maps {
   CUtensorMap a, w, out;
@@ -69,11 +70,41 @@ __device__ __forceinline__ void store_scales(uint8_t *dst, int lane, const uint4
   p[3 * kAtom / 16] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
 }
 
+// Scales of 128 rows and a group of kGroup stages.  A row's scales of a group are
+// 64 bytes: four lanes load them, so that a load of the warp touches eight rows
+// (a lane a row and stage: 32 lines a load, of which an SM asks for one in about
+// two cycles; the tile kernel fell from 7700 to 4876 TFLOP/s).  p0: this lane's
+// 16 bytes of row lane / 4.  line(x, j): the distance of row 8 x + 32 j from it
+// in the tensor (in bytes it fits 32 bits); place(x, j): in the tile, where rows
+// from `left` on are not there.
+constexpr int kGroup = 4;
+template <class Place, class Line>
+__device__ __forceinline__ void load_group(uint4 (&v)[4][4], const uint8_t *p0, int pitch, int left, bool wide,
+                                           int chunks, const uint8_t *base, uint64_t extent, Place place,
+                                           Line line) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[x][j] = load_scales(p0 + line(x, j) * pitch, place(x, j) < left, wide, chunks, base, extent);
+}
+
 // Lane 4 r + p's value to lane 8 p + r.
 __device__ __forceinline__ uint4 swap_lanes(const uint4 &v, int lane) {
   const int from = (lane & 7) * 4 + (lane >> 3);
   return make_uint4(__shfl_sync(0xFFFFFFFFu, v.x, from), __shfl_sync(0xFFFFFFFFu, v.y, from),
                     __shfl_sync(0xFFFFFFFFu, v.z, from), __shfl_sync(0xFFFFFFFFu, v.w, from));
+}
+
+// ... and to shared memory, the lanes having changed places: eight rows of one
+// stage side by side.  dst: the place of this lane's stage, lane / 8.
+__device__ __forceinline__ void store_group(uint8_t *dst, int lane, uint4 (&v)[4][4]) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[x][j] = swap_lanes(v[x][j], lane);
+    store_scales(dst, 8 * x + (lane & 7), v[x]);
+  }
 }
 
 // SiLU(g) u with the accurate exponential and a division of two ulps (the
@@ -116,6 +147,32 @@ __device__ __forceinline__ void store_gated4(const Fp4GemmArgs &a, int64_t t, bo
   }
 }
 
+__device__ __forceinline__ float4 scaled4(const float4 &v, float s) {
+  return make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
+}
+
+// Adds the cluster's partial sums at `from` (HALVES: and 64 columns behind it) in
+// the order of the shares; all loads are on their way before the first is added.
+template <int HALVES>
+__device__ __forceinline__ void sum_shares(float4 (&c)[HALVES], const float *from, int splits) {
+  float4 p[kMaxSplit][HALVES];
+#pragma unroll
+  for (int x = 0; x < kMaxSplit; ++x)
+    if (x < splits)
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) p[x][h] = ld_cluster4(cluster_addr(from + h * (kRows / 2), (uint32_t)x));
+#pragma unroll
+  for (int h = 0; h < HALVES; ++h) c[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int x = 0; x < kMaxSplit; ++x)
+    if (x < splits)
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) {
+        const float4 q = p[x][h];
+        c[h] = make_float4(c[h].x + q.x, c[h].y + q.y, c[h].z + q.z, c[h].w + q.w);
+      }
+}
+
 // ----------------------------------------------------------- stream kernel
 //
 // For few tokens, where the weight's bytes are the cost.  The weight is the
@@ -125,7 +182,6 @@ __device__ __forceinline__ void store_gated4(const Fp4GemmArgs &a, int64_t t, bo
 // in a fixed order, every CTA some of the tokens.
 //   warp 0: TMA   warp 1: products   warps 2-5: scales, then the sums
 
-constexpr int kMaxSplit = 8;
 constexpr int kStreamThreads = 6 * 32;
 
 template <int TN>
@@ -232,17 +288,24 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
         const uint64_t sw = scale_desc(smem_u32(sm.w_sf[now])), sa = scale_desc(smem_u32(sm.a_sf[now]));
         // the scales of alternate stages at two places of tensor memory
         const uint32_t tw = tmem + Smem::kSfColumn + (it & 1) * 32, ta = tw + 16;
-        const auto issue = [&](int c) {
-          tmem_copy_scales<false>(tw + 4 * c, sw + c * (kAtom >> 4));
-          tmem_copy_scales<false>(ta + 4 * c, sa + c * (kAtom >> 4));
-          mma_nvfp4<false>(tmem, dw + 2 * c, da + 2 * c, desc, tw + 4 * c, ta + 4 * c, it + c > 0);
-        };
+        // All of a stage's scales, then its products: these are too short to
+        // hide a copy each (one token x 8192 x 28672, two shares: 23.2 us).
         if (kb < num_k - 1 || a.K % kStageK == 0) {
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) issue(c);
+          for (int c = 0; c < kChunks; ++c) {
+            tmem_copy_scales<false>(tw + 4 * c, sw + c * (kAtom >> 4));
+            tmem_copy_scales<false>(ta + 4 * c, sa + c * (kAtom >> 4));
+          }
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            mma_nvfp4<false>(tmem, dw + 2 * c, da + 2 * c, desc, tw + 4 * c, ta + 4 * c, it + c > 0);
         } else {
 #pragma unroll 1
-          for (int c = 0; c < a.K % kStageK / 64; ++c) issue(c);
+          for (int c = 0; c < a.K % kStageK / 64; ++c) {
+            tmem_copy_scales<false>(tw + 4 * c, sw + c * (kAtom >> 4));
+            tmem_copy_scales<false>(ta + 4 * c, sa + c * (kAtom >> 4));
+            mma_nvfp4<false>(tmem, dw + 2 * c, da + 2 * c, desc, tw + 4 * c, ta + 4 * c, it + c > 0);
+          }
         }
         mma_commit<false>(&sm.empty[now]);
       }
@@ -282,7 +345,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
       if (lane == 0) mbar_arrive(&sm.full[s]);
     }
     // The products are done: nothing reads the stages any more.
-    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const int quarter = warp & 3;
     if (warp_wait_phase(&sm.drain, 0, &sm.failed) && !*(volatile uint32_t *)&sm.failed) {
       tcgen05_fence_after();
 #pragma unroll
@@ -291,7 +354,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
         tmem_load(tmem + ((uint32_t)(quarter * 32) << 16) + c * 16, v);
         tmem_load_wait(v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sm.part[c * 16 + j][row] = __uint_as_float(v[j]);
+        for (int j = 0; j < 16; ++j) sm.part[c * 16 + j][quarter * 32 + lane] = __uint_as_float(v[j]);
       }
       tcgen05_fence_before();
     }
@@ -310,32 +373,27 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
 
   const int tokens = min(TN, a.T - t0);
   const float alpha = __ldg(a.alpha);
-  if constexpr (!GATED) {  // a warp a token, a lane four columns
-    for (int j = split + warp * splits; j < tokens; j += kStreamThreads / 32 * splits) {
-      float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = 0; x < splits; ++x) {
-        const float4 p = ld_cluster4(cluster_addr(&sm.part[j][4 * lane], (uint32_t)x));
-        c = make_float4(c.x + p.x, c.y + p.y, c.z + p.z, c.w + p.w);
-      }
-      c = make_float4(alpha * c.x, alpha * c.y, alpha * c.z, alpha * c.w);
-      store_out4(a, t0 + j, n0 + 4 * lane, c);
+  const float gs = GATED ? __ldg(a.global_scale) : 0.f;
+  // Plain: a warp a token, a lane four columns; gated: half a warp.  The loads
+  // of kAtOnce tokens are on their way before the first is added.
+  constexpr int kPerWarp = GATED ? 2 : 1, kAtOnce = 2;
+  const int col = GATED ? 4 * (lane & 15) : 4 * lane, mine = GATED ? lane >> 4 : 0;
+  for (int j0 = split + kPerWarp * warp * splits; j0 < tokens;
+       j0 += kAtOnce * kPerWarp * (kStreamThreads / 32) * splits) {
+    float4 c[kAtOnce][kPerWarp];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int j = j0 + (i * kPerWarp * (kStreamThreads / 32) + mine) * splits;
+      const float *from = &sm.part[j < tokens ? j : 0][col];
+      sum_shares<kPerWarp>(c[i], from, splits);
     }
-  } else {  // half a warp a token
-    const float gs = __ldg(a.global_scale);
-    const int col = 4 * (lane & 15);
-    for (int j0 = split + 2 * warp * splits; j0 < tokens; j0 += kStreamThreads / 16 * splits) {
-      const int j = j0 + (lane >> 4) * splits;
-      const bool live = j < tokens;
-      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
-      for (int x = 0; x < splits; ++x) {
-        const uint32_t at = cluster_addr(&sm.part[live ? j : 0][col], (uint32_t)x);
-        const float4 p = ld_cluster4(at), q = ld_cluster4(at + 4 * kRows / 2);
-        g = make_float4(g.x + p.x, g.y + p.y, g.z + p.z, g.w + p.w);
-        u = make_float4(u.x + q.x, u.y + q.y, u.z + q.z, u.w + q.w);
-      }
-      g = make_float4(alpha * g.x, alpha * g.y, alpha * g.z, alpha * g.w);
-      u = make_float4(alpha * u.x, alpha * u.y, alpha * u.z, alpha * u.w);
-      store_gated4(a, t0 + j, live, n0 + col, lane, gs, g, u);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int j = j0 + (i * kPerWarp * (kStreamThreads / 32) + mine) * splits;
+      if constexpr (GATED)
+        store_gated4(a, t0 + j, j < tokens, n0 + col, lane, gs, scaled4(c[i][0], alpha), scaled4(c[i][1], alpha));
+      else if (j < tokens)
+        store_out4(a, t0 + j, n0 + col, scaled4(c[i][0], alpha));
     }
   }
   cluster_sync();  // nobody reads this CTA's sums any more
@@ -352,20 +410,26 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
 // Two accumulators of 256 columns and the scales do not fit into 512 columns,
 // so the accumulators share kOverlap columns, which the epilogue reads first:
 // the next tile's products start when these are in registers.
+// Many tiles: persistent pairs.  Few tiles and a long K (SPLIT): up to four
+// pairs of a cluster share a tile's K and add their sums through distributed
+// shared memory in a fixed order.
 
 constexpr int kTileStages = 5;
 constexpr int kTileStageBytes = 2 * kRows * kRowBytes;  // of either CTA
 constexpr int kScaleWarps = 6, kOutWarps = 8, kTileThreads = 32 * (2 + kScaleWarps + kOutWarps);
-constexpr int kGroup = 4;       // stages whose scales are loaded at once
 constexpr int kAcc = 256;       // columns of an accumulator
 constexpr int kOverlap = 64;    // shared by the two: what the epilogue reads first
 constexpr int kSfColumn = 2 * kAcc - kOverlap;  // first column of the scales
 static_assert(kSfColumn + 12 * kChunks <= 512, "tensor memory");
+constexpr int kTileSplit = 4;   // shares of K, a pair each, of a cluster
 constexpr int kTileGroup = 16;  // pairs' token tiles that share a sweep over the weight
 
 template <bool GATED>
 struct TileSmem {
-  uint8_t stage[kTileStages][kTileStageBytes];
+  union {
+    uint8_t stage[kTileStages][kTileStageBytes];
+    float4 part[kRows][kAcc / 4];  // split K: partial sums, once the products are done
+  };
   uint8_t out[GATED ? 1 : kOutWarps][GATED ? 16 : 32 * 64];  // boxes of 32 rows x 32 columns
   uint8_t sf[2][kGroup][3][kChunks * kAtom];  // of the tokens, of the weight's halves
   uint64_t full[kTileStages], empty[kTileStages], sf_full[2], sf_empty[2];
@@ -389,15 +453,22 @@ __device__ __forceinline__ Tile tile_at(uint32_t i, uint32_t num_t, uint32_t num
   return {(int)(g * kTileGroup + r - n * rows) * 2 * kRows, (int)n * (GATED ? kAcc / 2 : kAcc)};
 }
 
-template <bool GATED>
+template <bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    fp4_gemm_tile_kernel(const Fp4GemmArgs a, const __grid_constant__ Fp4Maps maps, int num_t, int num_n) {
+    fp4_gemm_tile_kernel(const Fp4GemmArgs a, const __grid_constant__ Fp4Maps maps, int num_t, int num_n,
+                         int splits) {
   extern __shared__ __align__(1024) uint8_t raw[];
   TileSmem<GATED> &sm = *reinterpret_cast<TileSmem<GATED> *>(raw);
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-  const int num_k = (a.K + kStageK - 1) / kStageK;
+  const int all_k = (a.K + kStageK - 1) / kStageK;
   const uint32_t tiles = (uint32_t)num_t * (uint32_t)num_n;
-  const uint32_t rank = cluster_rank(), first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // rank in the pair, the pair's first rank in the cluster; the tiles of the
+  // pair (SPLIT: one, shared by the cluster's pairs) and its stages of K
+  const uint32_t rank = cluster_rank() & 1u, base = SPLIT ? cluster_rank() & ~1u : 0u;
+  const uint32_t first = SPLIT ? blockIdx.x / (2u * (uint32_t)splits) : blockIdx.x >> 1;
+  const uint32_t pairs = SPLIT ? tiles : gridDim.x >> 1;
+  const int k_lo = SPLIT ? all_k * (int)(base >> 1) / splits : 0;
+  const int num_k = (SPLIT ? all_k * (int)((base >> 1) + 1) / splits : all_k) - k_lo;
   const int my_t = (int)rank * kRows;  // this CTA's tokens within the pair's
 
   if (warp == 0 && lane == 0) {
@@ -439,13 +510,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (elect_lane()) {
           if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kTileStageBytes);
           uint8_t *p = sm.stage[s];
-          const uint32_t bar = cluster_addr(&sm.full[s], 0);
-          tma_load_2d_pair(p, &maps.a, kb * kRowBytes, t.t0 + my_t, bar);
+          const uint32_t bar = cluster_addr(&sm.full[s], base);
+          const int x = (k_lo + kb) * kRowBytes;
+          tma_load_2d_pair(p, &maps.a, x, t.t0 + my_t, bar);
           if constexpr (GATED)
-            tma_load_4d_pair(p + kRows * kRowBytes, &maps.w, kb * kRowBytes, 0, 0,
-                             t.n0 / 16 + (int)rank * 4, bar);
+            tma_load_4d_pair(p + kRows * kRowBytes, &maps.w, x, 0, 0, t.n0 / 16 + (int)rank * 4, bar);
           else
-            tma_load_2d_pair(p + kRows * kRowBytes, &maps.w, kb * kRowBytes, t.n0 + (int)rank * kRows, bar);
+            tma_load_2d_pair(p + kRows * kRowBytes, &maps.w, x, t.n0 + (int)rank * kRows, bar);
         }
         __syncwarp();
         ++issued;
@@ -496,16 +567,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_copy_scales<true>(tw + 8 * c + 4, sw + (kChunks + c) * (kAtom >> 4));
             mma_nvfp4<true>(acc, da + 2 * c, dw + 2 * c, desc, ta + 4 * c, tw + 8 * c, kb + c > 0);
           };
-          if (kb < num_k - 1 || a.K % kStageK == 0) {
+          if (k_lo + kb < all_k - 1 || a.K % kStageK == 0) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) issue(c);
           } else {
 #pragma unroll 1
             for (int c = 0; c < a.K % kStageK / 64; ++c) issue(c);
           }
-          mma_commit_pair(&sm.empty[now], 0);
-          if (last) mma_commit_pair(&sm.sf_empty[group & 1], 0);
-          if (kb == num_k - 1) mma_commit_pair(&sm.acc_full[j & 1], 0);
+          mma_commit_pair(&sm.empty[now], base);
+          if (last) mma_commit_pair(&sm.sf_empty[group & 1], base);
+          if (kb == num_k - 1) mma_commit_pair(&sm.acc_full[j & 1], base);
         }
         __syncwarp();
         group += last;
@@ -517,13 +588,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     (void)mbar_wait_bounded(&sm.drain, 0);
   } else if (warp >= 2 && warp < 2 + kScaleWarps) {
     // Scales of 128 rows (tokens, either half of the weight's), every other
-    // group of kGroup stages, counted over all tiles.  A row's scales of a
-    // group are 64 bytes: four lanes load them, so that a load of the warp
-    // touches eight rows (a lane a row and stage: 32 lines a load, of which the
-    // SM asks for one in about two cycles; 4876 instead of 7700 TFLOP/s).
-    // Then the lanes change places: eight rows of one stage side by side.
+    // group of stages, counted over all tiles.
     const int role = (warp - 2) % 3, turn = (warp - 2) / 3;
-    const bool wide = a.K % kStageK == 0, tokens = role == 0, pairs16 = GATED && !tokens;
+    const bool wide = a.K % kStageK == 0, tokens = role == 0;
     const int pitch = a.K / kNvfp4Block;
     const uint8_t *src = tokens ? a.a_sf : a.w_sf;
     const uint64_t extent = tokens ? a_sf_extent(a) : w_sf_extent<GATED>(a);
@@ -533,40 +600,34 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (uint32_t i = first; i < tiles && ok; i += pairs) {
       const Tile t = tile_at<GATED>(i, num_t, num_n);
       // gated, a block's rows are turns of 16 gate and 16 up rows
-      const int row = (tokens ? t.t0 + my_t : t.n0 + (role - 1) * (pairs16 ? kRows / 2 : kRows)) + (lane >> 2);
+      const int row = (tokens ? t.t0 + my_t : t.n0 + (role - 1) * (GATED ? kRows / 2 : kRows)) + (lane >> 2);
       for (int k = 0; k < num_k; k += kGroup, ++group) {
         if ((int)(group & 1) != turn) continue;
-        const int kb = k + (lane & 3), chunks = min(kChunks, (a.K - kb * kStageK) / 64);
-        // one pointer; the rows' distances from it fit 32 bits (2^16 rows of 2^11)
+        const int kb = k_lo + k + (lane & 3), chunks = min(kChunks, (a.K - kb * kStageK) / 64);
         const uint8_t *p0 = src + (int64_t)row * pitch + kb * (kStageK / kNvfp4Block);
-        const int left = kb < num_k ? limit - row : 0;
-        uint4 v[4][4];  // row 8 x + lane / 4 of 32, 32-row part
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int d = pairs16 ? 16 * j + 8 * (x & 1) : 32 * j + 8 * x;
-            const int line = d + (pairs16 && x >= 2 ? a.N : 0);
-            v[x][j] = load_scales(p0 + line * pitch, d < left, wide, chunks, src, extent);
-          }
+        const int left = k + (lane & 3) < num_k ? limit - row : 0;
+        uint4 v[4][4];
+        const auto in_turn = [](int x, int j) { return 32 * j + 8 * x; };
+        if (GATED && !tokens) {  // 16 gate rows, the same 16 up rows
+          const auto col = [](int x, int j) { return 16 * j + 8 * (x & 1); };
+          load_group(v, p0, pitch, left, wide, chunks, src, extent, col,
+                     [&](int x, int j) { return col(x, j) + (x >= 2 ? a.N : 0); });
+        } else {
+          load_group(v, p0, pitch, left, wide, chunks, src, extent, in_turn, in_turn);
+        }
         if (lap > 0 && !(ok = warp_wait_phase(&sm.sf_empty[turn], (lap - 1) & 1, &sm.failed))) break;
         ++lap;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[x][j] = swap_lanes(v[x][j], lane);
-          store_scales(sm.sf[turn][lane >> 3][role], 8 * x + (lane & 7), v[x]);
-        }
+        store_group(sm.sf[turn][lane >> 3][role], lane, v);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_written(cluster_addr(&sm.sf_full[turn], 0));
+        if (lane == 0) mbar_arrive_cluster_written(cluster_addr(&sm.sf_full[turn], base));
       }
     }
     // (as for the stages: the last release has landed)
     if (lap > 0 && ok) (void)warp_wait_phase(&sm.sf_empty[turn], (lap - 1) & 1, &sm.failed);
   } else if (warp >= 2 + kScaleWarps) {
     const int quarter = warp & 3, half = (warp - 2 - kScaleWarps) >> 2;  // lanes, columns
-    const uint32_t free_bar = cluster_addr(&sm.acc_free, 0);
+    const uint32_t free_bar = cluster_addr(&sm.acc_free, base);
     const float alpha = __ldg(a.alpha), gs = GATED ? __ldg(a.global_scale) : 0.f;
     uint32_t j = 0;
     for (uint32_t i = first; i < tiles; i += pairs, ++j) {
@@ -587,6 +648,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tmem_load(base + c0 + 32, v[1]);
         tmem_load_wait(v[0]);
         tmem_load_wait(v[1]);
+        if constexpr (SPLIT) {
+          // Partial sums to shared memory (the products are done, so nothing
+          // reads the stages), 16-byte chunks swizzled by the row.
+          const int c = (half * (kAcc / 2) + c0) / 4;
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const uint32_t *x = &v[q >> 3][4 * (q & 7)];
+            sm.part[quarter * 32 + lane][(c + q) ^ (lane & 7)] =
+                make_float4(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]), __uint_as_float(x[3]));
+          }
+          continue;
+        }
         if (p == 0) {
           tcgen05_fence_before();
           __syncwarp();
@@ -661,9 +734,44 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // copies that the other CTA issued ahead of this one's count: a millisecond
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   }
-  cluster_sync();  // the pair is done
+  cluster_sync();  // SPLIT: all partial sums are in place; otherwise the pair is done
   __syncwarp();
   if (warp == 1) tmem_dealloc<true>(tmem, 512);
+  if constexpr (SPLIT) {
+    // Each pair of the cluster adds some of the tile's rows, in a fixed order:
+    // a warp a token row, a lane four columns of either half (gated: gate and
+    // up of four columns).
+    const Tile t = tile_at<GATED>(first, num_t, num_n);
+    const float alpha = __ldg(a.alpha), gs = GATED ? __ldg(a.global_scale) : 0.f;
+    for (int row = (int)(base >> 1) + warp * splits; row < kRows; row += kTileThreads / 32 * splits) {
+      const int64_t token = t.t0 + my_t + row;
+      if (token >= a.T) break;
+      // gated: turns of 16 gate and 16 up columns, four lanes each
+      const int c0 = GATED ? 8 * (lane >> 2) + (lane & 3) : lane, c1 = c0 + (GATED ? 4 : kAcc / 8);
+      float4 p[kTileSplit][2], c[2] = {};
+#pragma unroll
+      for (int x = 0; x < kTileSplit; ++x)
+        if (x < splits) {
+          const uint32_t from = 2u * (uint32_t)x + rank;
+          p[x][0] = ld_cluster4(cluster_addr(&sm.part[row][c0 ^ (row & 7)], from));
+          p[x][1] = ld_cluster4(cluster_addr(&sm.part[row][c1 ^ (row & 7)], from));
+        }
+#pragma unroll
+      for (int x = 0; x < kTileSplit; ++x)
+        if (x < splits)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            c[h] = make_float4(c[h].x + p[x][h].x, c[h].y + p[x][h].y, c[h].z + p[x][h].z, c[h].w + p[x][h].w);
+      const int n = t.n0 + 4 * lane;
+      if constexpr (!GATED) {
+        store_out4(a, token, n, scaled4(c[0], alpha));
+        store_out4(a, token, n + kAcc / 2, scaled4(c[1], alpha));
+      } else {
+        store_gated4(a, token, n < a.N, n, lane, gs, scaled4(c[0], alpha), scaled4(c[1], alpha));
+      }
+    }
+    cluster_sync();  // nobody reads this CTA's sums any more
+  }
 }
 
 // -------------------------------------------------------------------- host
@@ -687,10 +795,10 @@ cudaError_t launch_stream(const Fp4GemmArgs &a, int splits, cudaStream_t s) {
                             dim3(kStreamThreads), sizeof(StreamSmem<TN>), s, a, maps, num_n, splits, w_once);
 }
 
-template <bool GATED>
-cudaError_t launch_tile(const Fp4GemmArgs &a, int sms, cudaStream_t s) {
+template <bool GATED, bool SPLIT>
+cudaError_t launch_tile(const Fp4GemmArgs &a, int splits, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> opted_in{0};
-  const cudaError_t e = opt_in_once(opted_in, (const void *)fp4_gemm_tile_kernel<GATED>);
+  const cudaError_t e = opt_in_once(opted_in, (const void *)fp4_gemm_tile_kernel<GATED, SPLIT>);
   if (e != cudaSuccess) return e;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   Fp4Maps maps;
@@ -712,19 +820,23 @@ cudaError_t launch_tile(const Fp4GemmArgs &a, int sms, cudaStream_t s) {
   }
   const int num_t = (a.T + 2 * kRows - 1) / (2 * kRows);
   const int tile = GATED ? kAcc / 2 : kAcc, num_n = (a.N + tile - 1) / tile;
-  const int64_t tiles = (int64_t)num_t * num_n, pairs = tiles < sms / 2 ? tiles : sms / 2;
-  return launch_pdl_cluster(fp4_gemm_tile_kernel<GATED>, dim3((unsigned)(2 * pairs)), 2,
-                            dim3(kTileThreads), sizeof(TileSmem<GATED>), s, a, maps, num_t, num_n);
+  const int64_t tiles = (int64_t)num_t * num_n;
+  const int64_t pairs = SPLIT ? tiles * splits : (tiles < sms / 2 ? tiles : sms / 2);
+  return launch_pdl_cluster(fp4_gemm_tile_kernel<GATED, SPLIT>, dim3((unsigned)(2 * pairs)),
+                            SPLIT ? 2 * splits : 2, dim3(kTileThreads), sizeof(TileSmem<GATED>), s, a, maps,
+                            num_t, num_n, splits);
 }
 
 template <bool GATED>
 cudaError_t launch_form(const Fp4GemmArgs &a, const GemmPlan &p, int sms, cudaStream_t s) {
   switch (p.tn) {
-    case 0: return launch_tile<GATED>(a, sms, s);
     case 16: return launch_stream<GATED, 16>(a, p.splits, s);
     case 32: return launch_stream<GATED, 32>(a, p.splits, s);
     case 64: return launch_stream<GATED, 64>(a, p.splits, s);
-    default: return launch_stream<GATED, 128>(a, p.splits, s);
+    case 128: return launch_stream<GATED, 128>(a, p.splits, s);
+    default:
+      return p.splits > 1 ? launch_tile<GATED, true>(a, p.splits, sms, s)
+                          : launch_tile<GATED, false>(a, 1, sms, s);
   }
 }
 
