@@ -420,7 +420,7 @@ def _here(t, stream):
     if t.get_device() < 0:
         return -2, 0
     torch = _kinds()[4]
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()  # (the tensor has made its context)
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
     return dev, _stream(stream)
@@ -626,45 +626,36 @@ def vg_fp8_block_gemm_silu_mul_fp8(q, scale, a, a_scale, w, w_scale, a_options: 
     return q, scale
 
 
-def _one(t, name, dev):
-    """Device pointer of one fp32 value."""
+@functools.cache
+def _nvfp4_kinds():
+    """(uint8, fp8, bf16, fp32 dtypes, torch)"""
+    bf16, fp8, f32, _, torch = _kinds()
+    return torch.uint8, fp8, bf16, f32[0], torch
+
+
+def _check_one(t, name, dev):
+    """Refuses what is not one fp32 value on the device ``dev``."""
     if not hasattr(t, "numel") or t.numel() != 1:
         raise ValueError(f"{name}: expected one fp32 value on the device")
-    f32 = _kinds()[2]
-    if t.dtype not in f32 or t.get_device() != dev:
-        _arg(t, f32, name, dev)
-    return t.data_ptr()
+    _arg(t, _kinds()[2], name, dev)
 
 
-def _codes(q4, block_scale, names, dev):
-    """(rows, columns) of a checked NVFP4 tensor: uint8 [T, n/2] with E4M3
-    scales [T, n/16]."""
-    _, fp8, _, _, torch = _kinds()
+def _check_codes(q4, block_scale, names, dev):
+    """Refuses what is not an NVFP4 tensor: uint8 [T, n/2] with E4M3 scales [T, n/16]."""
     T, half = _rows(q4, names[0])
-    if (half % 8 or block_scale.shape != (T, half // 8) or q4.dtype != torch.uint8
-            or block_scale.dtype not in fp8 or q4.get_device() != dev
-            or block_scale.get_device() != dev or not q4.is_contiguous()
-            or not block_scale.is_contiguous()):
-        if half % 8:
-            raise ValueError(f"{names[0]}: expected whole blocks of 16 columns (8 bytes)")
-        _shape(block_scale, (T, half // 8), names[1])
-        _arg(q4, (torch.uint8,), names[0], dev)
-        _arg(block_scale, fp8, names[1], dev)
-    return T, 2 * half
+    if half % 8:
+        raise ValueError(f"{names[0]}: expected whole blocks of 16 columns (8 bytes)")
+    _shape(block_scale, (T, half // 8), names[1])
+    _arg(q4, (_nvfp4_kinds()[0],), names[0], dev)
+    _arg(block_scale, _nvfp4_kinds()[1], names[1], dev)
 
 
-def _codes_out(q4, block_scale, T, n, stream, device):
-    """The NVFP4 tensor that a call writes, allocated where both are None."""
-    _, fp8, _, _, torch = _kinds()
-    if q4 is None and block_scale is None:
-        empty = _allocator(stream)
-        return (empty((T, n // 2), dtype=torch.uint8, device=device),
-                empty((T, n // 16), dtype=fp8[0], device=device))
+def _check_codes_out(q4, block_scale, T, n, dev):
+    """The same for an NVFP4 tensor to be written."""
     if q4 is None or block_scale is None:
         raise ValueError("q4 and block_scale: give both or neither")
     _shape(q4, (T, n // 2), "q4")
-    _codes(q4, block_scale, ("q4", "block_scale"), device.index)
-    return q4, block_scale
+    _check_codes(q4, block_scale, ("q4", "block_scale"), dev)
 
 
 def vg_nvfp4_quantize(q4, block_scale, x, global_scale, stream=None):
@@ -672,16 +663,29 @@ def vg_nvfp4_quantize(q4, block_scale, x, global_scale, stream=None):
     [T,n/16] E4M3 codes; x [T,n] bf16, rows contiguous (a column slice is
     fine); global_scale fp32 [1] on the device.  ``q4`` and ``block_scale``
     both None allocate them; returns (q4, block_scale)."""
+    u8, fp8, bf16, f32, torch = _nvfp4_kinds()
     dev, raw = _here(x, stream)
-    xp, stride, T, n = _rows_ptr(x, "x")
-    if x.get_device() != dev:
-        _arg(x, _kinds()[0], "x", dev, False)
-    gs = _one(global_scale, "global_scale", dev)
-    if n % 16:
+    shape = x.shape
+    if (len(shape) != 2 or x.dtype not in bf16 or x.get_device() != dev or shape[1] % 16
+            or not (x.is_contiguous() or x.stride(1) == 1) or global_scale.dtype != f32
+            or global_scale.get_device() != dev or global_scale.numel() != 1):
+        _rows_ptr(x, "x")
+        _arg(x, bf16, "x", dev, False)
+        _check_one(global_scale, "global_scale", dev)
         raise ValueError("x: expected whole blocks of 16 columns")
-    q4, block_scale = _codes_out(q4, block_scale, T, n, stream, x.device)
-    st = (_lib or load()).vg_nvfp4_quantize(q4.data_ptr(), block_scale.data_ptr(), xp,
-                                            stride if T > 1 else n, gs, T, n, raw)
+    T, n = shape
+    if q4 is None and block_scale is None:
+        empty = torch.empty if stream is None else _allocator(stream)
+        q4 = empty((T, n // 2), dtype=u8, device=x.device)
+        block_scale = empty((T, n // 16), dtype=fp8[0], device=x.device)
+    elif (q4 is None or block_scale is None or q4.shape != (T, n // 2) or q4.dtype != u8
+          or q4.get_device() != dev or not q4.is_contiguous() or block_scale.shape != (T, n // 16)
+          or block_scale.dtype not in fp8 or block_scale.get_device() != dev
+          or not block_scale.is_contiguous()):
+        _check_codes_out(q4, block_scale, T, n, dev)
+    st = (_lib or load()).vg_nvfp4_quantize(
+        q4.data_ptr(), block_scale.data_ptr(), x.data_ptr(), n if x.is_contiguous() else x.stride(0),
+        global_scale.data_ptr(), T, n, raw)
     if st:
         _check(st)
     return q4, block_scale
@@ -690,27 +694,46 @@ def vg_nvfp4_quantize(q4, block_scale, x, global_scale, stream=None):
 def vg_nvfp4_dequantize(out, q4, block_scale, global_scale, stream=None):
     """NVFP4 back to bf16 through the C ABI: out [T,n] bf16; the others as for
     vg_nvfp4_quantize.  ``out`` None allocates it; returns out."""
-    bf16 = _kinds()[0]
+    u8, fp8, bf16, f32, torch = _nvfp4_kinds()
     dev, raw = _here(q4, stream)
-    T, n = _codes(q4, block_scale, ("q4", "block_scale"), dev)
-    gs = _one(global_scale, "global_scale", dev)
-    out = _bf16_out(out, T, n, stream, q4.device)
+    T, half = _rows(q4, "q4")
+    if (half % 8 or block_scale.shape != (T, half // 8) or q4.dtype != u8 or block_scale.dtype not in fp8
+            or q4.get_device() != dev or block_scale.get_device() != dev or not q4.is_contiguous()
+            or not block_scale.is_contiguous() or global_scale.dtype != f32
+            or global_scale.get_device() != dev or global_scale.numel() != 1):
+        _check_codes(q4, block_scale, ("q4", "block_scale"), dev)
+        _check_one(global_scale, "global_scale", dev)
+    n = 2 * half
+    if out is None:
+        out = (torch.empty if stream is None else _allocator(stream))((T, n), dtype=bf16[0], device=q4.device)
+    elif (out.shape != (T, n) or out.dtype not in bf16 or out.get_device() != dev
+          or not out.is_contiguous()):
+        _shape(out, (T, n), "out")
+        _arg(out, bf16, "out", dev)
     st = (_lib or load()).vg_nvfp4_dequantize(out.data_ptr(), q4.data_ptr(), block_scale.data_ptr(),
-                                              gs, T, n, raw)
+                                              global_scale.data_ptr(), T, n, raw)
     if st:
         _check(st)
     return out
 
 
-def _bf16_out(out, T, n, stream, device):
-    bf16 = _kinds()[0]
-    if out is None:
-        return _allocator(stream)((T, n), dtype=bf16[0], device=device)
-    if (out.shape != (T, n) or out.dtype not in bf16 or out.get_device() != device.index
-            or not out.is_contiguous()):
-        _shape(out, (T, n), "out")
-        _arg(out, bf16, "out", device.index)
-    return out
+def _fp4_gemm_sizes(a, a_scale, w, w_scale, alpha, dev):
+    """T, N and K of an NVFP4 product's checked operands."""
+    u8, fp8, _, f32, _ = _nvfp4_kinds()
+    N, half = _rows(w, "w")
+    T = a.shape[0]
+    if (half % 8 or a.shape != (T, half) or a_scale.shape != (T, half // 8) or w_scale.shape != (N, half // 8)
+            or a.dtype != u8 or a.get_device() != dev or not a.is_contiguous()
+            or w.dtype != u8 or w.get_device() != dev or not w.is_contiguous()
+            or a_scale.dtype not in fp8 or a_scale.get_device() != dev or not a_scale.is_contiguous()
+            or w_scale.dtype not in fp8 or w_scale.get_device() != dev or not w_scale.is_contiguous()
+            or alpha.dtype != f32 or alpha.get_device() != dev or alpha.numel() != 1):
+        _check_codes(a, a_scale, ("a", "a_scale"), dev)
+        _check_codes(w, w_scale, ("w", "w_scale"), dev)
+        if a.shape[1] != half:
+            raise ValueError("a and w must have the same number of columns")
+        _check_one(alpha, "alpha", dev)
+    return T, N, 2 * half
 
 
 def vg_nvfp4_gemm(out, a, a_scale, w, w_scale, alpha, stream=None):
@@ -721,15 +744,17 @@ def vg_nvfp4_gemm(out, a, a_scale, w, w_scale, alpha, stream=None):
     [T,K/16] and w_scale [N,K/16] E4M3 codes, as the NVFP4 ops write them;
     alpha fp32 [1] on the device (1 over the product of the two global
     scales).  ``out`` None allocates it; returns out."""
+    _, _, bf16, _, torch = _nvfp4_kinds()
     dev, raw = _here(a, stream)
-    T, K = _codes(a, a_scale, ("a", "a_scale"), dev)
-    N, Kw = _codes(w, w_scale, ("w", "w_scale"), dev)
-    if K != Kw:
-        raise ValueError("a and w must have the same number of columns")
-    al = _one(alpha, "alpha", dev)
-    out = _bf16_out(out, T, N, stream, a.device)
+    T, N, K = _fp4_gemm_sizes(a, a_scale, w, w_scale, alpha, dev)
+    if out is None:
+        out = (torch.empty if stream is None else _allocator(stream))((T, N), dtype=bf16[0], device=a.device)
+    elif (out.shape != (T, N) or out.dtype not in bf16 or out.get_device() != dev
+          or not out.is_contiguous()):
+        _shape(out, (T, N), "out")
+        _arg(out, bf16, "out", dev)
     st = (_lib or load()).vg_nvfp4_gemm(out.data_ptr(), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
-                                        w_scale.data_ptr(), al, T, N, K, raw)
+                                        w_scale.data_ptr(), alpha.data_ptr(), T, N, K, raw)
     if st:
         _check(st)
     return out
@@ -744,18 +769,27 @@ def vg_nvfp4_gemm_silu_mul_nvfp4(q4, block_scale, a, a_scale, w, w_scale, alpha,
     rows [I,2I)) with w_scale [2I,K/16]; global_scale fp32 [1] on the device:
     the output's; q4 [T,I/2] uint8, block_scale [T,I/16] E4M3 codes, or both
     None to allocate them; returns (q4, block_scale)."""
+    u8, fp8, _, f32, torch = _nvfp4_kinds()
     dev, raw = _here(a, stream)
-    T, K = _codes(a, a_scale, ("a", "a_scale"), dev)
-    N, Kw = _codes(w, w_scale, ("w", "w_scale"), dev)
-    if K != Kw:
-        raise ValueError("a and w must have the same number of columns")
-    if N % 32:
-        raise ValueError("w must have an even number of rows (gate, then up), whole blocks of 16 each")
-    al, gs = _one(alpha, "alpha", dev), _one(global_scale, "global_scale", dev)
-    q4, block_scale = _codes_out(q4, block_scale, T, N // 2, stream, a.device)
+    T, N, K = _fp4_gemm_sizes(a, a_scale, w, w_scale, alpha, dev)
+    if (N % 32 or global_scale.dtype != f32 or global_scale.get_device() != dev
+            or global_scale.numel() != 1):
+        if N % 32:
+            raise ValueError("w must have an even number of rows (gate, then up), whole blocks of 16 each")
+        _check_one(global_scale, "global_scale", dev)
+    inter = N // 2
+    if q4 is None and block_scale is None:
+        empty = torch.empty if stream is None else _allocator(stream)
+        q4 = empty((T, inter // 2), dtype=u8, device=a.device)
+        block_scale = empty((T, inter // 16), dtype=fp8[0], device=a.device)
+    elif (q4 is None or block_scale is None or q4.shape != (T, inter // 2) or q4.dtype != u8
+          or q4.get_device() != dev or not q4.is_contiguous() or block_scale.shape != (T, inter // 16)
+          or block_scale.dtype not in fp8 or block_scale.get_device() != dev
+          or not block_scale.is_contiguous()):
+        _check_codes_out(q4, block_scale, T, inter, dev)
     st = (_lib or load()).vg_nvfp4_gemm_silu_mul_nvfp4(
         q4.data_ptr(), block_scale.data_ptr(), a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
-        w_scale.data_ptr(), al, gs, T, N // 2, K, raw)
+        w_scale.data_ptr(), alpha.data_ptr(), global_scale.data_ptr(), T, inter, K, raw)
     if st:
         _check(st)
     return q4, block_scale

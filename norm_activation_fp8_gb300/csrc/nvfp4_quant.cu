@@ -21,7 +21,6 @@ __device__ uint32_t g_nvfp4_status;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocks = 2;  // quantise: blocks of 16 columns a thread
 constexpr int kChunks = 4;  // read back: chunks of 8 columns a thread
 
 __device__ __forceinline__ uint64_t codes_extent(const Nvfp4Args &a) { return VG_ROWS(a.T) * (uint64_t)a.nch * 4; }
@@ -68,8 +67,9 @@ __device__ __noinline__ uint32_t settle(uint32_t lo, uint32_t hi, uint32_t w0, u
   return lo;
 }
 
-// A lane a block.  FLAT: the rows follow one another without a gap.
-template <bool FLAT, bool WIDE>
+// A lane a block, kBlocks blocks a thread.  FLAT: the rows follow one another
+// without a gap.
+template <bool FLAT, bool WIDE, int kBlocks>
 __global__ void __launch_bounds__(kThreads) nvfp4_quantize_kernel(const Nvfp4Args a) {
   const int64_t blocks = a.nch / 2, total = a.T * blocks, first = (int64_t)blockIdx.x * (kThreads * kBlocks);
   if (FLAT && threadIdx.x == 0 && blockIdx.x < (unsigned)a.pf_ctas) {
@@ -181,14 +181,25 @@ __global__ void __launch_bounds__(kThreads) nvfp4_dequantize_kernel(const Nvfp4A
 
 }  // namespace
 
-cudaError_t launch_nvfp4_quantize(const Nvfp4Args &a, cudaStream_t s) {
+namespace {
+
+template <int kBlocks>
+cudaError_t launch_quantize(const Nvfp4Args &a, cudaStream_t s) {
   const dim3 g((unsigned)((a.T * (a.nch / 2) + kThreads * kBlocks - 1) / (kThreads * kBlocks))), b(kThreads);
   const bool flat = a.stride == a.nch * kElemsPerChunk || a.T == 1;
   const bool wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 && (flat || a.stride % 16 == 0);
-  return flat ? (wide ? launch_pdl(nvfp4_quantize_kernel<true, true>, g, b, 0, s, a)
-                      : launch_pdl(nvfp4_quantize_kernel<true, false>, g, b, 0, s, a))
-              : (wide ? launch_pdl(nvfp4_quantize_kernel<false, true>, g, b, 0, s, a)
-                      : launch_pdl(nvfp4_quantize_kernel<false, false>, g, b, 0, s, a));
+  return flat ? (wide ? launch_pdl(nvfp4_quantize_kernel<true, true, kBlocks>, g, b, 0, s, a)
+                      : launch_pdl(nvfp4_quantize_kernel<true, false, kBlocks>, g, b, 0, s, a))
+              : (wide ? launch_pdl(nvfp4_quantize_kernel<false, true, kBlocks>, g, b, 0, s, a)
+                      : launch_pdl(nvfp4_quantize_kernel<false, false, kBlocks>, g, b, 0, s, a));
+}
+
+}  // namespace
+
+// Few blocks: one a thread (33 x 8192, in a run of calls, 1.25 us; four a thread
+// 1.97); many: four (16384 x 4096 25.7 us, 6.7 TB/s; one a thread 28.5).
+cudaError_t launch_nvfp4_quantize(const Nvfp4Args &a, cudaStream_t s) {
+  return a.T * a.nch < 1 << 20 ? launch_quantize<1>(a, s) : launch_quantize<4>(a, s);
 }
 
 cudaError_t launch_nvfp4_dequantize(const Nvfp4Args &a, cudaStream_t s) {
