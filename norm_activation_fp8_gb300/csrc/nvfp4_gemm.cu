@@ -44,14 +44,31 @@ template <bool GATED>
   return (GATED ? 2ull : 1ull) * (uint64_t)a.N * (uint64_t)(a.K / kNvfp4Block);
 }
 
-// The scales of one row and a stage's K: a word per K of 64, the first `chunks`
-// of them; zeros for a row that is not there.  Rows whose length is no multiple
-// of 256 are not 16-byte aligned.
-__device__ __forceinline__ uint4 load_scales(const uint8_t *p, bool live, bool wide, int chunks,
-                                             const uint8_t *base, uint64_t extent) {
+// 16 bytes, or zeros (nothing is read) where `live` is false: a predicate, not a
+// branch, so that loads follow one another at once.  It stays where it is
+// written, ahead of the wait for the place that the data goes to.
+__device__ __forceinline__ uint4 ld_live16(const uint8_t *p, bool live) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)live));
+  return v;
+}
+
+// The scales of one row and a stage's K: a word per K of 64; zeros for a row
+// that is not there.  WIDE: all four, 16-byte aligned; otherwise (rows whose
+// length is no multiple of 256) the first `chunks`.
+template <bool WIDE>
+__device__ __forceinline__ uint4 load_scales(const uint8_t *p, bool live, int chunks, const uint8_t *base,
+                                             uint64_t extent) {
+  live = live && VG_ACCESS_OK(g_fp4_gemm_status, p, WIDE ? 16 : 4 * chunks, base, extent);
+  if constexpr (WIDE) return ld_live16(p, live);
   uint4 v = make_uint4(0, 0, 0, 0);
-  if (!live || !VG_ACCESS_OK(g_fp4_gemm_status, p, 4 * chunks, base, extent)) return v;
-  if (wide) return __ldg(reinterpret_cast<const uint4 *>(p));
+  if (!live) return v;
   const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
   v.x = __ldg(q);
   if (chunks > 1) v.y = __ldg(q + 1);
@@ -78,15 +95,14 @@ __device__ __forceinline__ void store_scales(uint8_t *dst, int lane, const uint4
 // in the tensor (in bytes it fits 32 bits); place(x, j): in the tile, where rows
 // from `left` on are not there.
 constexpr int kGroup = 4;
-template <class Place, class Line>
-__device__ __forceinline__ void load_group(uint4 (&v)[4][4], const uint8_t *p0, int pitch, int left, bool wide,
-                                           int chunks, const uint8_t *base, uint64_t extent, Place place,
-                                           Line line) {
+template <bool WIDE, class Place, class Line>
+__device__ __forceinline__ void load_group(uint4 (&v)[4][4], const uint8_t *p0, int pitch, int left, int chunks,
+                                           const uint8_t *base, uint64_t extent, Place place, Line line) {
 #pragma unroll
   for (int x = 0; x < 4; ++x)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      v[x][j] = load_scales(p0 + line(x, j) * pitch, place(x, j) < left, wide, chunks, base, extent);
+      v[x][j] = load_scales<WIDE>(p0 + line(x, j) * pitch, place(x, j) < left, chunks, base, extent);
 }
 
 // Lane 4 r + p's value to lane 8 p + r.
@@ -334,8 +350,13 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
       uint4 vw[4], va[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        vw[j] = load_scales(row_w[j] + x, live_w[j], wide, chunks, a.w_sf, w_sf_extent<GATED>(a));
-        va[j] = load_scales(row_a[j] + x, live_a[j], wide, chunks, a.a_sf, a_sf_extent(a));
+        if (wide) {
+          vw[j] = load_scales<true>(row_w[j] + x, live_w[j], chunks, a.w_sf, w_sf_extent<GATED>(a));
+          va[j] = load_scales<true>(row_a[j] + x, live_a[j], chunks, a.a_sf, a_sf_extent(a));
+        } else {
+          vw[j] = load_scales<false>(row_w[j] + x, live_w[j], chunks, a.w_sf, w_sf_extent<GATED>(a));
+          va[j] = load_scales<false>(row_a[j] + x, live_a[j], chunks, a.a_sf, a_sf_extent(a));
+        }
       }
       if (lap > 0 && !warp_wait_phase(&sm.empty[s], (lap - 1) & 1, &sm.failed)) break;
       store_scales(sm.w_sf[s], lane, vw);
@@ -590,7 +611,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // Scales of 128 rows (tokens, either half of the weight's), every other
     // group of stages, counted over all tiles.
     const int role = (warp - 2) % 3, turn = (warp - 2) / 3;
-    const bool wide = a.K % kStageK == 0, tokens = role == 0;
+    const bool wide = a.K % kStageK == 0, tokens = role == 0, turns = GATED && !tokens;
     const int pitch = a.K / kNvfp4Block;
     const uint8_t *src = tokens ? a.a_sf : a.w_sf;
     const uint64_t extent = tokens ? a_sf_extent(a) : w_sf_extent<GATED>(a);
@@ -607,14 +628,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint8_t *p0 = src + (int64_t)row * pitch + kb * (kStageK / kNvfp4Block);
         const int left = k + (lane & 3) < num_k ? limit - row : 0;
         uint4 v[4][4];
-        const auto in_turn = [](int x, int j) { return 32 * j + 8 * x; };
-        if (GATED && !tokens) {  // 16 gate rows, the same 16 up rows
-          const auto col = [](int x, int j) { return 16 * j + 8 * (x & 1); };
-          load_group(v, p0, pitch, left, wide, chunks, src, extent, col,
-                     [&](int x, int j) { return col(x, j) + (x >= 2 ? a.N : 0); });
-        } else {
-          load_group(v, p0, pitch, left, wide, chunks, src, extent, in_turn, in_turn);
-        }
+        // (four calls: with the choice inside, at run time, the gated form
+        // spilled; 4096 x 28672 x 8192 660 instead of 613 us)
+        const auto plain = [](int x, int j) { return 32 * j + 8 * x; };
+        const auto col = [](int x, int j) { return 16 * j + 8 * (x & 1); };  // 16 gate rows, the same 16 up rows
+        const auto turned = [&](int x, int j) { return col(x, j) + (x >= 2 ? a.N : 0); };
+        if (turns && wide)
+          load_group<true>(v, p0, pitch, left, chunks, src, extent, col, turned);
+        else if (turns)
+          load_group<false>(v, p0, pitch, left, chunks, src, extent, col, turned);
+        else if (wide)
+          load_group<true>(v, p0, pitch, left, chunks, src, extent, plain, plain);
+        else
+          load_group<false>(v, p0, pitch, left, chunks, src, extent, plain, plain);
         if (lap > 0 && !(ok = warp_wait_phase(&sm.sf_empty[turn], (lap - 1) & 1, &sm.failed))) break;
         ++lap;
         store_group(sm.sf[turn][lane >> 3][role], lane, v);
