@@ -474,6 +474,44 @@ __device__ __forceinline__ Tile tile_at(uint32_t i, uint32_t num_t, uint32_t num
   return {(int)(g * kTileGroup + r - n * rows) * 2 * kRows, (int)n * (GATED ? kAcc / 2 : kAcc)};
 }
 
+// The rows of scales that a scale warp moves for a tile: role 0 the CTA's tokens,
+// 1 and 2 either half of the weight's; a lane row lane / 4 and what lies 8 x +
+// 32 j behind it in the tile.
+template <bool GATED>
+struct ScaleRows {
+  const uint8_t *p, *base;  // this lane's row (of any stage)
+  int left, pitch, up;      // rows from its own that are there; bytes a row; gate to up
+  bool wide, turns;         // turns: of 16 gate rows and the same 16 up rows
+  __device__ __forceinline__ ScaleRows(const Fp4GemmArgs &a, const Tile &t, int my_t, int role, int lane)
+      : pitch(a.K / kNvfp4Block), up(a.N), wide(a.K % kStageK == 0), turns(GATED && role > 0) {
+    const int row = (role == 0 ? t.t0 + my_t : t.n0 + (role - 1) * (GATED ? kRows / 2 : kRows)) + (lane >> 2);
+    base = role == 0 ? a.a_sf : a.w_sf;
+    p = base + (int64_t)row * pitch + (lane & 3) * (kStageK / kNvfp4Block);
+    left = (role == 0 ? a.T : a.N) - row;
+  }
+  static __device__ __forceinline__ int plain(int x, int j) { return 32 * j + 8 * x; }
+  static __device__ __forceinline__ int col(int x, int j) { return 16 * j + 8 * (x & 1); }
+
+  // The group of stages from kb on, of those before `end`.
+  __device__ __forceinline__ void load(uint4 (&v)[4][4], const Fp4GemmArgs &a, int kb, int end) const {
+    const int mine = kb + ((int)threadIdx.x & 3), chunks = min(kChunks, (a.K - mine * kStageK) / 64);
+    const uint8_t *q = p + kb * (kStageK / kNvfp4Block);
+    const int n = mine < end ? left : 0;
+    const uint64_t extent = base == a.a_sf ? a_sf_extent(a) : w_sf_extent<GATED>(a);
+    const auto turned = [&](int x, int j) { return col(x, j) + (x >= 2 ? up : 0); };
+    // (four calls: with the choice inside, at run time, the gated form spilled;
+    // 4096 x 28672 x 8192 660 instead of 613 us)
+    if (turns && wide)
+      load_group<true>(v, q, pitch, n, chunks, base, extent, col, turned);
+    else if (turns)
+      load_group<false>(v, q, pitch, n, chunks, base, extent, col, turned);
+    else if (wide)
+      load_group<true>(v, q, pitch, n, chunks, base, extent, plain, plain);
+    else
+      load_group<false>(v, q, pitch, n, chunks, base, extent, plain, plain);
+  }
+};
+
 template <bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fp4_gemm_tile_kernel(const Fp4GemmArgs a, const __grid_constant__ Fp4Maps maps, int num_t, int num_n,
@@ -514,7 +552,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == 1) tmem_alloc<true>(&sm.tmem, 512);
   tcgen05_fence_before();
   __syncthreads();
-  cluster_sync();  // the pair's barriers are initialised
+  // The pair's barriers are initialised.  (Relaxed: they are all that the other
+  // CTA may see by now, and fence_mbar_init() has ordered them; a release here
+  // took 1.3 us.)
+  cluster_arrive_relaxed();
+  // Launched with programmatic dependent launch: nothing but L2 prefetches of
+  // the first stages before the previous grid has finished.
+  const Tile t_first = tile_at<GATED>(first, num_t, num_n);
+  const ScaleRows<GATED> rows(a, t_first, my_t, (warp + 1) % 3, lane);  // (warps 2-7; of the first tile)
+  if (warp == 2 + kScaleWarps && lane < 2 * kTileStages && (lane >> 1) < num_k) {
+    const int x = (k_lo + (lane >> 1)) * kRowBytes;
+    if (lane & 1)
+      tma_prefetch_2d(&maps.a, x, t_first.t0 + my_t);
+    else if constexpr (GATED)
+      tma_prefetch_4d(&maps.w, x, 0, 0, t_first.n0 / 16 + (int)rank * 4);
+    else
+      tma_prefetch_2d(&maps.w, x, t_first.n0 + (int)rank * kRows);
+  }
+  cluster_wait();
   tcgen05_fence_after();
   const uint32_t tmem = sm.tmem;
   pdl_wait();
@@ -611,36 +666,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // Scales of 128 rows (tokens, either half of the weight's), every other
     // group of stages, counted over all tiles.
     const int role = (warp - 2) % 3, turn = (warp - 2) / 3;
-    const bool wide = a.K % kStageK == 0, tokens = role == 0, turns = GATED && !tokens;
-    const int pitch = a.K / kNvfp4Block;
-    const uint8_t *src = tokens ? a.a_sf : a.w_sf;
-    const uint64_t extent = tokens ? a_sf_extent(a) : w_sf_extent<GATED>(a);
-    const int limit = tokens ? a.T : a.N;
     uint32_t group = 0, lap = 0;  // groups so far, this warp's
     bool ok = true;
     for (uint32_t i = first; i < tiles && ok; i += pairs) {
-      const Tile t = tile_at<GATED>(i, num_t, num_n);
-      // gated, a block's rows are turns of 16 gate and 16 up rows
-      const int row = (tokens ? t.t0 + my_t : t.n0 + (role - 1) * (GATED ? kRows / 2 : kRows)) + (lane >> 2);
+      const ScaleRows<GATED> r = i == first ? rows : ScaleRows<GATED>(a, tile_at<GATED>(i, num_t, num_n), my_t, role, lane);
       for (int k = 0; k < num_k; k += kGroup, ++group) {
         if ((int)(group & 1) != turn) continue;
-        const int kb = k_lo + k + (lane & 3), chunks = min(kChunks, (a.K - kb * kStageK) / 64);
-        const uint8_t *p0 = src + (int64_t)row * pitch + kb * (kStageK / kNvfp4Block);
-        const int left = k + (lane & 3) < num_k ? limit - row : 0;
         uint4 v[4][4];
-        // (four calls: with the choice inside, at run time, the gated form
-        // spilled; 4096 x 28672 x 8192 660 instead of 613 us)
-        const auto plain = [](int x, int j) { return 32 * j + 8 * x; };
-        const auto col = [](int x, int j) { return 16 * j + 8 * (x & 1); };  // 16 gate rows, the same 16 up rows
-        const auto turned = [&](int x, int j) { return col(x, j) + (x >= 2 ? a.N : 0); };
-        if (turns && wide)
-          load_group<true>(v, p0, pitch, left, chunks, src, extent, col, turned);
-        else if (turns)
-          load_group<false>(v, p0, pitch, left, chunks, src, extent, col, turned);
-        else if (wide)
-          load_group<true>(v, p0, pitch, left, chunks, src, extent, plain, plain);
-        else
-          load_group<false>(v, p0, pitch, left, chunks, src, extent, plain, plain);
+        r.load(v, a, k_lo + k, k_lo + num_k);
         if (lap > 0 && !(ok = warp_wait_phase(&sm.sf_empty[turn], (lap - 1) & 1, &sm.failed))) break;
         ++lap;
         store_group(sm.sf[turn][lane >> 3][role], lane, v);

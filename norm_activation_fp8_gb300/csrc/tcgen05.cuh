@@ -86,6 +86,13 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *m, int32_t x,
                : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *m, int32_t x, int32_t y, int32_t z,
+                                                int32_t w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(m), "r"(x), "r"(y),
+               "r"(z), "r"(w)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -132,6 +139,12 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+
+// Its two halves, the arrival without a release of earlier writes.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // One box from shared memory to a 2-D tensor; what lies outside the tensor is
 // not written.  x and y must not be negative.  Then tma_store_commit().
