@@ -667,7 +667,7 @@ def vg_nvfp4_quantize(q4, block_scale, x, global_scale, stream=None):
     dev, raw = _here(x, stream)
     shape = x.shape
     if (len(shape) != 2 or x.dtype not in bf16 or x.get_device() != dev or shape[1] % 16
-            or not (x.is_contiguous() or x.stride(1) == 1) or global_scale.dtype != f32
+            or not (x.is_contiguous() or x.stride(1) == 1) or getattr(global_scale, "dtype", None) != f32
             or global_scale.get_device() != dev or global_scale.numel() != 1):
         _rows_ptr(x, "x")
         _arg(x, bf16, "x", dev, False)
@@ -699,7 +699,7 @@ def vg_nvfp4_dequantize(out, q4, block_scale, global_scale, stream=None):
     T, half = _rows(q4, "q4")
     if (half % 8 or block_scale.shape != (T, half // 8) or q4.dtype != u8 or block_scale.dtype not in fp8
             or q4.get_device() != dev or block_scale.get_device() != dev or not q4.is_contiguous()
-            or not block_scale.is_contiguous() or global_scale.dtype != f32
+            or not block_scale.is_contiguous() or getattr(global_scale, "dtype", None) != f32
             or global_scale.get_device() != dev or global_scale.numel() != 1):
         _check_codes(q4, block_scale, ("q4", "block_scale"), dev)
         _check_one(global_scale, "global_scale", dev)
@@ -727,7 +727,7 @@ def _fp4_gemm_sizes(a, a_scale, w, w_scale, alpha, dev):
             or w.dtype != u8 or w.get_device() != dev or not w.is_contiguous()
             or a_scale.dtype not in fp8 or a_scale.get_device() != dev or not a_scale.is_contiguous()
             or w_scale.dtype not in fp8 or w_scale.get_device() != dev or not w_scale.is_contiguous()
-            or alpha.dtype != f32 or alpha.get_device() != dev or alpha.numel() != 1):
+            or getattr(alpha, "dtype", None) != f32 or alpha.get_device() != dev or alpha.numel() != 1):
         _check_codes(a, a_scale, ("a", "a_scale"), dev)
         _check_codes(w, w_scale, ("w", "w_scale"), dev)
         if a.shape[1] != half:
@@ -772,7 +772,7 @@ def vg_nvfp4_gemm_silu_mul_nvfp4(q4, block_scale, a, a_scale, w, w_scale, alpha,
     u8, fp8, _, f32, torch = _nvfp4_kinds()
     dev, raw = _here(a, stream)
     T, N, K = _fp4_gemm_sizes(a, a_scale, w, w_scale, alpha, dev)
-    if (N % 32 or global_scale.dtype != f32 or global_scale.get_device() != dev
+    if (N % 32 or getattr(global_scale, "dtype", None) != f32 or global_scale.get_device() != dev
             or global_scale.numel() != 1):
         if N % 32:
             raise ValueError("w must have an even number of rows (gate, then up), whole blocks of 16 each")

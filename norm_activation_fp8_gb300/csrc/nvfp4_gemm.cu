@@ -901,19 +901,62 @@ cudaError_t launch_form(const Fp4GemmArgs &a, const GemmPlan &p, int sms, cudaSt
 
 }  // namespace
 
+// Which kernel, and its split, by an estimate of either one's time, in
+// microseconds (fitted on GB300 to T = 1..2048, N = 1024..28672, K =
+// 4096..28672, plain and gated; over those 117 sizes the choice was on average
+// 1.5 %, at most 12 % above the best one):
+//   tile kernel    8.1 (one share) .. 10 (four) for start and end, 1.2 for each
+//                  further wave of pairs, and 0.26 per stage of K or the
+//                  weight's bytes at 6 TB/s, whichever is longer
+//   stream kernel  a wave of CTAs: 3.5 and 0.11 for each CTA of a cluster, and
+//                  0.2 (128 tokens: 0.4) per stage of its share or the weight's
+//                  bytes at 6.3 TB/s (0.7 of that again for every further token
+//                  tile, which reads the weight from L2), whichever is longer,
+//                  with a fifth of the other
+// Clusters do not fill every SM, and a second wave costs as much as the first,
+// so a wave is taken as the part of the slots that clusters of that size were
+// seen to fill.  Splits of the stream kernel are powers of two: others pack
+// worse.
 GemmPlan plan_fp4_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms) {
   GemmPlan p;
-  p.tn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
-  const int64_t tile = gated ? kRows / 2 : kRows, blocks = (K + kStageK - 1) / kStageK;
-  const int64_t tiles = (N + tile - 1) / tile * ((T + p.tn - 1) / p.tn);
-  const int64_t slots = (int64_t)sms * (p.tn <= 64 ? 2 : 1);
-  p.splits = 1;
-  // (a first rule: tiles of 256 x 256 once they fill half of the pairs)
-  if (T > 128 && (T + 255) / 256 * ((N + 2 * tile - 1) / (2 * tile)) >= sms / 4) {
-    p.tn = 0;
-    return p;
+  const int64_t blocks = (K + kStageK - 1) / kStageK;
+  const double bytes = (double)N * (double)K * (gated ? 2 : 1) * 0.5625e-6;  // of the weight, in MB
+  const auto waves_of = [](int64_t n, int64_t slots) { return (double)((n + slots - 1) / slots); };
+  const auto part = [](int64_t slots, int64_t percent) { return slots < 8 ? slots : slots * percent / 100; };
+  const int64_t column = gated ? kAcc / 2 : kAcc;
+  const int64_t pairs = (T + 2 * kRows - 1) / (2 * kRows) * ((N + column - 1) / column);
+  static const double kFixed[kTileSplit] = {8.1, 8.4, 9.0, 10.0};
+  static const int kFill[kTileSplit] = {100, 90, 64, 64};
+  double best = 1e30;
+  for (int s = 1; s <= kTileSplit && s <= blocks; ++s) {
+    const double waves = waves_of(pairs * s, part(sms < 2 ? 1 : sms / 2, kFill[s - 1]));
+    if (s > 1 && waves > 1) break;
+    const double chain = waves * 0.26 * (double)((blocks + s - 1) / s), traffic = bytes / 6.0;
+    const double cost = kFixed[s - 1] + 1.2 * (waves - 1) + (chain > traffic ? chain : traffic);
+    if (cost < best) {
+      best = cost;
+      p.splits = s;
+    }
   }
-  while (p.splits < kMaxSplit && 2 * p.splits <= blocks && tiles * p.splits * 2 <= slots) p.splits *= 2;
+  // one token tile, or for more than 64 tokens tiles of 64 or 128
+  const int64_t rows = gated ? N / (kRows / 2) : (N + kRows - 1) / kRows;
+  const int smallest = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
+  for (int tn = smallest; tn <= (T <= 64 ? smallest : 128); tn *= 2) {
+    const int64_t token_tiles = (T + tn - 1) / tn, slots = (int64_t)sms * (tn <= 64 ? 2 : 1);
+    if (rows * token_tiles * kMaxSplit > INT32_MAX) continue;
+    for (int s = 1; s <= kMaxSplit && s <= blocks; s *= 2) {
+      const double waves = waves_of(rows * token_tiles * s, part(slots, s == 8 ? 64 : 86));
+      const double chain = (double)((blocks + s - 1) / s) * (tn <= 64 ? 0.2 : 0.4);
+      const double traffic = bytes * (1.0 + 0.7 * (double)(token_tiles - 1)) / waves / 6.3;
+      const double cost =
+          waves * (3.5 + 0.11 * s + (chain > traffic ? chain + 0.2 * traffic : traffic + 0.2 * chain));
+      if (cost < best) {
+        best = cost;
+        p.tn = tn;
+        p.splits = s;
+      }
+    }
+  }
   return p;
 }
 

@@ -104,7 +104,18 @@ PLAIN = [  # T, N, K
     (200, 4096, 4096), (256, 4096, 2048), (257, 248, 448), (300, 6144, 1024), (513, 1032, 512),
     (1000, 2056, 832), (2049, 4096, 640), (4100, 264, 256), (512, 1024, 8192),
     (130, 10248, 192), (700, 9736, 448), (4100, 2056, 64), (385, 8192, 16384), (2304, 5120, 1088),
+    # the plans that the sizes above do not take
+    (1677, 936, 4928), (1090, 624, 12672), (460, 1432, 13440), (1, 24, 14080), (20, 16, 192),
+    (18, 16, 3392), (24, 16, 8704), (140, 15832, 256), (75, 1456, 13824),
 ]
+
+
+def test_sizes_take_every_plan():
+    """On 152 SMs the sizes of these tests run every kernel with every split that
+    some size takes."""
+    import test_nvfp4_gemm_host as host
+    for sizes, gated in ((PLAIN, False), (GATED, True)):
+        assert {host.plan(*x, gated, 152) for x in sizes} >= host.reachable(gated)
 
 
 @pytest.mark.parametrize("T,N,K", PLAIN)
@@ -133,6 +144,8 @@ GATED = [  # T, I, K
     (128, 128, 384), (129, 1152, 576), (200, 14336, 256), (256, 2048, 1024), (300, 64, 896),
     (513, 1024, 512), (1000, 960, 640), (2049, 2048, 256), (4100, 192, 128),
     (300, 14400, 256), (515, 4160, 1088), (4100, 1344, 64), (257, 8192, 2048),
+    (604, 960, 6592), (985, 448, 10304), (337, 704, 18176), (1, 64, 24704), (31, 64, 704),
+    (32, 64, 2624), (25, 128, 5504), (59, 128, 3584), (3205, 64, 4096), (69, 768, 19264),
 ]
 
 
@@ -171,3 +184,146 @@ def test_gated(T, I, K):
         check_gated(q4, sf, c[:, :I], c[:, I:], e[:, :I], e[:, I:], gs)
         assert intact(qbuf) and intact(sbuf)
     assert vg.vg_device_status() == 0
+
+
+@pytest.mark.parametrize("T,N,K", [
+    (1, 8, 64), (1, 6144, 4096), (20, 96, 128), (31, 384, 960), (50, 2056, 512), (70, 3800, 6912),
+    (196, 3704, 6912), (1000, 2056, 896), (2049, 4096, 640)])
+def test_sums_are_held_in_fp32(T, N, K):
+    """Every K of 64 has +96^2 and -96^2, in it or with the one beside it, and
+    products that are multiples of 2^-8: their sum has to come out exact.  Every
+    partial sum, in whatever order, is a multiple of 2^-8 below 2 * 96^2 + 2^-4 K
+    < 2^16, so it has at most 24 bits; an accumulator of fewer, or products
+    aligned to fewer, loses some."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    f8 = torch.float8_e4m3fn
+    for apart in (False, True):
+        # values 0, +-0.5, +-1 (codes 0 to 2) under scales of 2^-3
+        ca = torch.randint(0, 3, (T, K), generator=g, device="cuda") | torch.randint(0, 2, (T, K), generator=g, device="cuda") << 3
+        cw = torch.randint(0, 3, (N, K), generator=g, device="cuda") | torch.randint(0, 2, (N, K), generator=g, device="cuda") << 3
+        sa, sw = torch.full((T, K // 16), 0.125, device="cuda"), torch.full((N, K // 16), 0.125, device="cuda")
+        st = torch.randint(0, 2, (T, 1), generator=g, device="cuda") * 8
+        sn = torch.randint(0, 2, (N, 1), generator=g, device="cuda") * 8
+        for k in range(0, K, 64 if not apart else 128):
+            # two blocks of 16 that hold one code 6 under a scale of 16 each
+            first, second = k, k + 48 if not apart else min(k + 64, K - 16)
+            if first == second:
+                continue
+            for b in (first, second):
+                ca[:, b:b + 16], cw[:, b:b + 16] = 0, 0
+                sa[:, b // 16], sw[:, b // 16] = 16.0, 16.0
+                ca[:, [b + 5]], cw[:, [b + 5]] = 7 | st, 7 | (sn if b == first else sn ^ 8)
+        a, w = packed(ca.to(torch.uint8)), packed(cw.to(torch.uint8))
+        want = scaled(a, sa) @ scaled(w, sw).t()
+        assert float(want.abs().max()) <= 2.0 ** -6 * K
+        out = vg.nvfp4_gemm(a, sa.to(f8), w, sw.to(f8), one(1.0))
+        assert torch.equal(out, want.to(torch.bfloat16))
+
+
+def test_outputs_past_32_bit_offsets():
+    """Outputs of more than 2^31 elements: rows sampled over all of them."""
+    import torch
+    T, N, K = 70001, 32768, 64
+    a, sa = operand(T, K, 5, exact=True)
+    w, sw = operand(N, K, 6, exact=True)
+    rows = torch.tensor([0, 127, 128, 40000, 65535, 65536, 65537, 69999, 70000], device="cuda")
+    out = vg.nvfp4_gemm(a, sa, w, sw, one(1.0))
+    W = scaled(w, sw)
+    assert torch.equal(out[rows], (scaled(a[rows], sa.view(torch.uint8)[rows].view(sa.dtype)) @ W.t()).to(torch.bfloat16))
+    del out
+    w2, sw2 = torch.cat([w, w]), torch.cat([sw.view(torch.uint8)] * 2).view(sw.dtype)
+    q4, sf = vg.nvfp4_gemm_silu_mul_nvfp4(a, sa, w2, sw2, one(0.1), one(10.0))
+    few = vg.nvfp4_gemm_silu_mul_nvfp4(a[rows], sa.view(torch.uint8)[rows].view(sa.dtype), w2, sw2, one(0.1), one(10.0))
+    # the sums are exact in either kernel, and the same steps follow
+    assert torch.equal(q4[rows], few[0])
+    assert torch.equal(sf.view(torch.uint8)[rows], few[1].view(torch.uint8))
+
+
+@pytest.mark.parametrize("T,N", [(3, 262160), (262160, 16)])
+def test_operands_past_32_bit_offsets(T, N):
+    """A weight, then activations, of more than 2^32 bytes of codes; rows sampled."""
+    import torch
+    K, big = 32768, max(T, N)
+    few, sfew = operand(min(T, N), K, 1, exact=True)
+    base, sbase = operand(997, K, 2, exact=True)
+    many = base.repeat(big // 997 + 1, 1)[:big].contiguous()
+    smany = sbase.view(torch.uint8).repeat(big // 997 + 1, 1)[:big].contiguous().view(sbase.dtype)
+    a, sa, w, sw = (few, sfew, many, smany) if T < N else (many, smany, few, sfew)
+    out = vg.nvfp4_gemm(a, sa, w, sw, one(1.0))
+    at = torch.tensor([0, 127, 131071, 131072, 131073, 262143, 262144, big - 1], device="cuda")
+    rows = torch.arange(T, device="cuda") if T < N else at
+    cols = at if T < N else torch.arange(N, device="cuda")
+    pick = lambda q, s, i: scaled(q[i], s.view(torch.uint8)[i].view(s.dtype))  # noqa: E731
+    assert torch.equal(out[rows][:, cols], (pick(a, sa, rows) @ pick(w, sw, cols).t()).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("T", [1, 40, 300, 700])
+def test_gated_zero_rows_and_saturated_gates(T):
+    """A zero token gives zero scales and codes, and is no slower for it; gates far
+    on either side: silu(g) = g, or 0; an output scale that saturates the blocks."""
+    import torch
+    I, K = 256, 256
+    a, sa = operand(T, K, T)
+    w, sw = operand(2 * I, K, T + 1)
+    a[T // 2] = 0
+    alpha = float(np.float32(1e-4))
+    A, W = scaled(a, sa), scaled(w, sw) * alpha
+    c, e = A @ W.t(), product_error(A, W, K)
+    assert T == 1 or float(c[:, :I].abs().max()) > 90  # exp() over- and underflows
+    for gs in (1e-3, 1.0, 1e6):
+        q4, sf = vg.nvfp4_gemm_silu_mul_nvfp4(a, sa, w, sw, one(alpha), one(gs))
+        assert not bool(q4[T // 2].any()) and not bool(sf.view(torch.uint8)[T // 2].any())
+        check_gated(q4, sf, c[:, :I], c[:, I:], e[:, :I], e[:, I:], gs)
+
+
+@pytest.mark.parametrize("T", [1, 40, 700])
+def test_infinite_factors_follow_ieee_arithmetic(T):
+    import torch
+    N, K = 256, 256
+    a, sa = operand(T, K, 8, exact=True)
+    w, sw = operand(N, K, 9, exact=True)
+    c = scaled(a, sa) @ scaled(w, sw).t()
+    out = vg.nvfp4_gemm(a, sa, w, sw, one(float("inf"))).float()
+    want = torch.where(c == 0, float("nan"), c.sign() * float("inf")).float()
+    assert torch.equal(out.nan_to_num(7.0, 8.0, 9.0), want.nan_to_num(7.0, 8.0, 9.0))
+    assert bool(vg.nvfp4_gemm(a, sa, w, sw, one(float("nan"))).isnan().all())
+
+
+@pytest.mark.parametrize("T", [1, 50, 200, 700])
+def test_captured_calls_and_two_streams(T):
+    """Captured calls follow their inputs, and calls on two streams at once do not
+    disturb each other: there is no workspace to share."""
+    import torch
+    N, K = 4096, 2048
+    sets = [(*operand(T, K, 10 + k), *operand(N, K, 20 + k), one(1e-4 * (k + 1))) for k in range(2)]
+    xs = [torch.randn((T, K), device="cuda", generator=torch.Generator(device="cuda").manual_seed(k)).bfloat16()
+          for k in range(2)]
+
+    def run(s, x):
+        q4, sf = vg.nvfp4_quantize(x, s[4])
+        g4, gf = vg.nvfp4_gemm_silu_mul_nvfp4(*s, s[4])
+        return (vg.nvfp4_gemm(*s), q4, sf.view(torch.uint8), vg.nvfp4_dequantize(q4, sf, s[4]), g4,
+                gf.view(torch.uint8))
+    want = [run(s, x) for s, x in zip(sets, xs)]
+    live, x = [t.clone() for t in sets[0]], xs[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(live, x)
+    for k in (1, 0):
+        for dst, src in zip((*live, x), (*sets[k], xs[k])):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want[k]))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k].append(run(sets[k], xs[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(p, q) for r in got[k] for p, q in zip(r, want[k]))

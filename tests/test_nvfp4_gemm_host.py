@@ -1,6 +1,9 @@
 """The NVFP4 quantiser and products on the host (no GPU): every bad argument is
 refused before any CUDA call, so fake pointers are safe; and the binding's own
 checks."""
+import ctypes
+import random
+
 import pytest
 
 import norm_activation_fp8_gb300 as vg
@@ -76,6 +79,55 @@ def test_product_refusals(lib):
         assert gated(lib, **{k: A + 2}) == ALIGN, k
     assert gemm(lib, out=None, a=None, sa=None, w=None, sw=None, alpha=None, T=0) == OK
     assert gated(lib, q4=None, sf=None, a=None, sa=None, w=None, sw=None, alpha=None, gs=None, T=0) == OK
+
+
+class GemmPlan(ctypes.Structure):
+    _fields_ = [("tn", ctypes.c_int), ("splits", ctypes.c_int)]
+
+
+def plan(T, N, K, gated, sms):
+    """The library's own plan: (tokens a tile of the stream kernel or 0 for the
+    tile kernel, ways that K is split)."""
+    f = vg.load()._ZN2vg13plan_fp4_gemmElllbi
+    f.restype, f.argtypes = GemmPlan, [ctypes.c_int64] * 3 + [ctypes.c_bool, ctypes.c_int]
+    p = f(T, N, K, gated, sms)
+    return p.tn, p.splits
+
+
+def _sizes(gated, n, seed):
+    r = random.Random(seed)
+    unit = 64 if gated else 8
+    for _ in range(n):
+        yield (max(1, int(2 ** (13 * r.random()))), unit * int(2 ** ((9 if gated else 13) * r.random())),
+               64 * int(2 ** (9 * r.random())))
+
+
+def reachable(gated):
+    return {plan(*x, gated, 152) for x in _sizes(gated, 20000, 1)}
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_every_plan_can_be_launched(lib, gated):
+    """A split never exceeds the stages of K or its cluster the eight CTAs that
+    may form one, the grid stays within its limits, and few tokens take one
+    token tile."""
+    sizes = list(_sizes(gated, 5000, 2)) + [(2 ** 24, 2 ** 15, 64), (2 ** 24, 64, 32768), (1, 64, 64)]
+    if not gated:
+        sizes += [(1, 2 ** 20, 32768), (2 ** 24, 8, 64), (128, 2 ** 20, 64), (1, 8, 32768), (2 ** 24, 2 ** 20, 64)]
+    for sms in (152, 148, 132, 16, 2, 1):
+        for T, N, K in sizes:
+            tn, splits = plan(T, N, K, gated, sms)
+            assert 1 <= splits <= (K + 255) // 256
+            if tn == 0:
+                assert splits <= 4
+                tiles = (T + 255) // 256 * ((N + 127) // 128 if gated else (N + 255) // 256)
+                assert splits == 1 or 2 * splits * tiles < 2 ** 31
+                assert tiles < 2 ** 32
+            else:
+                assert tn in (16, 32, 64, 128) and splits in (1, 2, 4, 8)
+                assert T > 64 or tn >= T
+                assert (T + tn - 1) // tn * (N // 64 if gated else (N + 127) // 128) * splits < 2 ** 31
+    assert {tn for tn, _ in reachable(gated)} == {0, 16, 32, 64, 128}
 
 
 def test_binding_refuses_before_the_library():

@@ -149,3 +149,59 @@ def test_no_tokens():
     q4, sf = vg.nvfp4_quantize(x, one(1.0))
     assert q4.shape == (0, 32) and sf.shape == (0, 4)
     assert vg.nvfp4_dequantize(q4, sf, one(1.0)).shape == (0, 64)
+
+
+@pytest.mark.parametrize("pitch", [32768, 32776])
+def test_offsets_past_32_bits(pitch):
+    """More than 2^31 elements, rows one after the other and apart; rows sampled."""
+    import torch
+    T, n = 70001, 32768
+    base = randn(997, n, 3)
+    x = torch.empty((T, pitch), dtype=torch.bfloat16, device="cuda")[:, :n]
+    for t in range(0, T, 997):
+        x[t:t + 997] = base[:min(997, T - t)]
+    q4, sf = vg.nvfp4_quantize(x, one(168.0))
+    back = vg.nvfp4_dequantize(q4, sf, one(168.0))
+    rows = torch.tensor([0, 65535, 65536, 65537, 69999, 70000], device="cuda")
+    few = sf.view(torch.uint8)[rows].view(sf.dtype)
+    check(x[rows], q4[rows], few, 168.0)
+    assert torch.equal(back[rows], vg.nvfp4_dequantize(q4[rows], few, one(168.0)))
+
+
+def test_unaligned_slices_and_refusals():
+    """Rows that start at 16 but not at 32 bytes; what the binding refuses."""
+    import torch
+    x = randn(40, 2048, 1)
+    run(x.view(-1)[8:8 + 39 * 2048].view(39, 2048), 168.0)
+    gs = one(1.0)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        vg.nvfp4_quantize(x.t(), gs)
+    with pytest.raises(TypeError, match="x"):
+        vg.nvfp4_quantize(x.float(), gs)
+    with pytest.raises(ValueError, match="blocks"):
+        vg.nvfp4_quantize(x[:, :24], gs)
+    with pytest.raises(vg.VgError, match="MISALIGNED"):
+        vg.nvfp4_quantize(x[:, 4:20], gs)
+    with pytest.raises(vg.VgError, match="BAD_SHAPE"):
+        vg.nvfp4_quantize(x[:1, :16].expand(5, 16), gs)
+    with pytest.raises(TypeError, match="global_scale"):
+        vg.nvfp4_quantize(x, gs.double())
+    with pytest.raises(ValueError, match="global_scale"):
+        vg.nvfp4_quantize(x, gs.cpu())
+    with pytest.raises(ValueError, match="global_scale"):
+        vg.nvfp4_quantize(x, torch.ones(2, device="cuda"))
+    q4, sf = vg.nvfp4_quantize(x, gs)
+    with pytest.raises(ValueError, match="both or neither"):
+        vg.vg_nvfp4_quantize(q4, None, x, gs)
+    with pytest.raises(ValueError, match="q4"):
+        vg.vg_nvfp4_quantize(q4[:, :512].contiguous(), sf, x, gs)
+    with pytest.raises(ValueError, match="block_scale"):
+        vg.vg_nvfp4_quantize(q4, sf[:5], x, gs)
+    with pytest.raises(TypeError, match="q4"):
+        vg.nvfp4_dequantize(q4.view(torch.int8), sf, gs)
+    with pytest.raises(ValueError, match="contiguous"):
+        vg.nvfp4_dequantize(q4[:, ::2][:, :8], sf[:, :1], gs)
+    with pytest.raises(ValueError, match="out"):
+        vg.vg_nvfp4_dequantize(torch.empty((40, 16), dtype=torch.bfloat16, device="cuda"), q4, sf, gs)
+    with pytest.raises(TypeError, match="out"):
+        vg.vg_nvfp4_dequantize(torch.empty((40, 2048), device="cuda"), q4, sf, gs)
