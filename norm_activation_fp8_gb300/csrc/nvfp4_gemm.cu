@@ -204,6 +204,10 @@ template <int TN>
 struct StreamSmem {
   static constexpr int kStageBytes = (kRows + TN) * kRowBytes;
   static constexpr int kStages = TN == 16 ? 5 : (TN <= 64 ? 4 : 6);
+  // A scale warp that comes to stage i has seen stage i - 4 - kStages released,
+  // so i - 2 kStages too: only then does the parity of its wait for the slot
+  // (stage i - kStages) name one phase.
+  static_assert(kStages >= 4, "four scale warps take turns");
   static constexpr int kSfColumn = TN < 32 ? 32 : TN;                          // of tensor memory
   static constexpr int kColumns = kSfColumn + 64 <= 128 ? 128 : 256;
   union {
