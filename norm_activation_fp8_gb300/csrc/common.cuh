@@ -151,6 +151,26 @@ __device__ __forceinline__ uint4 ld_stream_ro(const void *p) {
   return v;
 }
 
+// Read-only data of other sizes.  (Like all loads here volatile, so that none is
+// moved ahead of pdl_wait(); __ldg() promises the compiler that the data never
+// changes, and it may be moved.)
+__device__ __forceinline__ uint4 ld_ro16(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_ro4(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_ro1(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_ro_f32(const float *p) { return __uint_as_float(ld_ro4(p)); }
+
 // Data streamed once that this kernel may also overwrite (the residual when
 // updated in place): coherent load, no L1 allocation.
 __device__ __forceinline__ uint4 ld_stream(const void *p) {

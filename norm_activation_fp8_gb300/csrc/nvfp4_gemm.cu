@@ -69,11 +69,10 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t *p, bool live, int ch
   if constexpr (WIDE) return ld_live16(p, live);
   uint4 v = make_uint4(0, 0, 0, 0);
   if (!live) return v;
-  const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
-  v.x = __ldg(q);
-  if (chunks > 1) v.y = __ldg(q + 1);
-  if (chunks > 2) v.z = __ldg(q + 2);
-  if (chunks > 3) v.w = __ldg(q + 3);
+  v.x = ld_ro4(p);
+  if (chunks > 1) v.y = ld_ro4(p + 4);
+  if (chunks > 2) v.z = ld_ro4(p + 8);
+  if (chunks > 3) v.w = ld_ro4(p + 12);
   return v;
 }
 
@@ -397,8 +396,8 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
   if (warp == 1) tmem_dealloc<false>(tmem, Smem::kColumns);
 
   const int tokens = min(TN, a.T - t0);
-  const float alpha = __ldg(a.alpha);
-  const float gs = GATED ? __ldg(a.global_scale) : 0.f;
+  const float alpha = ld_ro_f32(a.alpha);
+  const float gs = GATED ? ld_ro_f32(a.global_scale) : 0.f;
   // Plain: a warp a token, a lane four columns; gated: half a warp.  The loads
   // of kAtOnce tokens are on their way before the first is added.
   constexpr int kPerWarp = GATED ? 2 : 1, kAtOnce = 2;
@@ -691,7 +690,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else if (warp >= 2 + kScaleWarps) {
     const int quarter = warp & 3, half = (warp - 2 - kScaleWarps) >> 2;  // lanes, columns
     const uint32_t free_bar = cluster_addr(&sm.acc_free, base);
-    const float alpha = __ldg(a.alpha), gs = GATED ? __ldg(a.global_scale) : 0.f;
+    const float alpha = ld_ro_f32(a.alpha), gs = GATED ? ld_ro_f32(a.global_scale) : 0.f;
     uint32_t j = 0;
     for (uint32_t i = first; i < tiles; i += pairs, ++j) {
       const Tile t = tile_at<GATED>(i, num_t, num_n);
@@ -805,7 +804,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // a warp a token row, a lane four columns of either half (gated: gate and
     // up of four columns).
     const Tile t = tile_at<GATED>(first, num_t, num_n);
-    const float alpha = __ldg(a.alpha), gs = GATED ? __ldg(a.global_scale) : 0.f;
+    const float alpha = ld_ro_f32(a.alpha), gs = GATED ? ld_ro_f32(a.global_scale) : 0.f;
     for (int row = (int)(base >> 1) + warp * splits; row < kRows; row += kTileThreads / 32 * splits) {
       const int64_t token = t.t0 + my_t + row;
       if (token >= a.T) break;

@@ -23,8 +23,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunks = 4;  // read back: chunks of 8 columns a thread
 
-__device__ __forceinline__ uint64_t codes_extent(const Nvfp4Args &a) { return VG_ROWS(a.T) * (uint64_t)a.nch * 4; }
-__device__ __forceinline__ uint64_t scales_extent(const Nvfp4Args &a) { return VG_ROWS(a.T) * (uint64_t)a.nch / 2; }
+[[maybe_unused]] __device__ __forceinline__ uint64_t codes_extent(const Nvfp4Args &a) { return VG_ROWS(a.T) * (uint64_t)a.nch * 4; }
+[[maybe_unused]] __device__ __forceinline__ uint64_t scales_extent(const Nvfp4Args &a) { return VG_ROWS(a.T) * (uint64_t)a.nch / 2; }
 
 // 32 bytes, read once: one load (32-byte aligned), or two.
 template <bool WIDE>
@@ -34,7 +34,7 @@ __device__ __forceinline__ void ld_block(const uint16_t *p, uint32_t (&w)[8]) {
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                  : "l"(p));
   } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    const uint4 a = ld_ro16(p), b = ld_ro16(p + 8);
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
 }
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads) nvfp4_quantize_kernel(const Nvfp4Arg
     prefetch_l2(a.x + first * kNvfp4Block, (uint32_t)n * 32u);
   }
   pdl_wait();
-  const float gs = __ldg(a.global_scale);
+  const float gs = ld_ro_f32(a.global_scale);
   uint32_t w[kBlocks][8];
 #pragma unroll
   for (int k = 0; k < kBlocks; ++k) {
@@ -149,14 +149,14 @@ __device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
 __global__ void __launch_bounds__(kThreads) nvfp4_dequantize_kernel(const Nvfp4Args a) {
   const int64_t total = a.T * a.nch, first = (int64_t)blockIdx.x * (kThreads * kChunks);
   pdl_wait();
-  const float gs = __ldg(a.global_scale), inv = __frcp_rn(gs);
+  const float gs = ld_ro_f32(a.global_scale), inv = __frcp_rn(gs);
   const bool far = !(gs > 0x1p-100f && gs < 0x1p100f);
   uint32_t c[kChunks], s[kChunks];
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     const int64_t i = first + k * kThreads + threadIdx.x;
-    c[k] = i < total ? __ldg(reinterpret_cast<const uint32_t *>(a.q) + i) : 0u;
-    s[k] = i < total ? __ldg(a.sf + (i >> 1)) : 0u;
+    c[k] = i < total ? ld_ro4(a.q + 4 * i) : 0u;
+    s[k] = i < total ? ld_ro1(a.sf + (i >> 1)) : 0u;
   }
   pdl_launch_dependents();
 #pragma unroll
