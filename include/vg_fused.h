@@ -483,7 +483,8 @@ vg_status vg_nvfp4_dequantize(uint16_t *out, const uint8_t *q4, const uint8_t *b
  *   num_tokens T in [0, VG_MAX_GEMM_TOKENS]; n N: a multiple of 8 in
  *             [8, VG_MAX_GEMM_COLUMNS]; k K: a multiple of 64 in
  *             [64, VG_MAX_ROW] (else VG_ERR_BAD_SHAPE)
- * All tensors 16-byte aligned, the scales too; alpha 4-byte.  No workspace.
+ * out, a and w 16-byte, the scales and alpha 4-byte aligned (rows from any one on
+ * are an operand).  No workspace.
  */
 vg_status vg_nvfp4_gemm(uint16_t *out, const uint8_t *a, const uint8_t *a_scale, const uint8_t *w,
                         const uint8_t *w_scale, const float *alpha, int64_t num_tokens, int64_t n,
@@ -503,7 +504,9 @@ vg_status vg_nvfp4_gemm(uint16_t *out, const uint8_t *a, const uint8_t *a_scale,
  *   inter I: a multiple of 64 in [64, VG_MAX_ROW] (else VG_ERR_BAD_SHAPE)
  * Besides what the errors of g and u make of it, y is off by at most 2^-21 |y|
  * (below g = -87 it may be 0), and gs amax / 6 and y gs / sf by 2^-21 of
- * theirs: codes are those of values that near.
+ * theirs: codes are those of values that near.  block_scale is 4-byte aligned.
+ * Not finite: silu(-inf) is NaN; a NaN never wins the amax and its code is a
+ * saturated one; a block with an infinity gets the scale 448, and it +-6.
  */
 vg_status vg_nvfp4_gemm_silu_mul_nvfp4(uint8_t *q4, uint8_t *block_scale, const uint8_t *a,
                                        const uint8_t *a_scale, const uint8_t *w,

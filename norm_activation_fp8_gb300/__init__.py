@@ -696,7 +696,8 @@ def vg_nvfp4_dequantize(out, q4, block_scale, global_scale, stream=None):
     vg_nvfp4_quantize.  ``out`` None allocates it; returns out."""
     u8, fp8, bf16, f32, torch = _nvfp4_kinds()
     dev, raw = _here(q4, stream)
-    T, half = _rows(q4, "q4")
+    shape = q4.shape
+    T, half = shape if len(shape) == 2 else _rows(q4, "q4")
     if (half % 8 or block_scale.shape != (T, half // 8) or q4.dtype != u8 or block_scale.dtype not in fp8
             or q4.get_device() != dev or block_scale.get_device() != dev or not q4.is_contiguous()
             or not block_scale.is_contiguous() or getattr(global_scale, "dtype", None) != f32
@@ -720,7 +721,8 @@ def vg_nvfp4_dequantize(out, q4, block_scale, global_scale, stream=None):
 def _fp4_gemm_sizes(a, a_scale, w, w_scale, alpha, dev):
     """T, N and K of an NVFP4 product's checked operands."""
     u8, fp8, _, f32, _ = _nvfp4_kinds()
-    N, half = _rows(w, "w")
+    shape = w.shape
+    N, half = shape if len(shape) == 2 else _rows(w, "w")
     T = a.shape[0]
     if (half % 8 or a.shape != (T, half) or a_scale.shape != (T, half // 8) or w_scale.shape != (N, half // 8)
             or a.dtype != u8 or a.get_device() != dev or not a.is_contiguous()
@@ -919,7 +921,9 @@ def fp8_block_gemm_silu_mul_fp8(a, a_scale, w, w_scale, a_options: int = 0, out_
 
 
 def nvfp4_quantize(x, global_scale, stream=None):
-    """Returns (q4 uint8 [T,n/2], block_scale float8_e4m3fn [T,n/16])."""
+    """Returns (q4 uint8 [T,n/2], block_scale float8_e4m3fn [T,n/16]);
+    global_scale is an fp32 [1] device tensor, as a rule 2688 over x's largest
+    magnitude (6 and 448, the largest code and block scale)."""
     return vg_nvfp4_quantize(None, None, x, global_scale, stream)
 
 

@@ -258,6 +258,7 @@ struct Fp4GemmArgs {
   int32_t T;
   int32_t N;                  // output columns
   int32_t K;
+  int32_t wide;               // rows of scales are whole 16 bytes, 16-byte aligned
 };
 GemmPlan plan_fp4_gemm(int64_t T, int64_t N, int64_t K, bool gated, int sms);
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, bool gated, int sms, cudaStream_t s);

@@ -10,10 +10,9 @@
 // The tensor cores apply the block scales themselves, so a sum over all of K
 // stays in tensor memory.  They want the scales of 128 rows and one K of 64 as
 // 32 lanes x 4 columns; the tensors hold them row by row, as the quantising
-// ops write them.  Warps that have nothing else to do until the epilogue move
-// them: a lane loads the 16 bytes (K of 256, a stage) of rows l, l + 32, ...
-// and stores, for each K of 64, the four rows' words as one 16-byte row of the
-// copy to tensor memory.
+// ops write them.  Warps of their own move them: from 16 bytes (K of 256, a
+// stage) of rows l, l + 32, ... come, for each K of 64, the four rows' words as
+// one 16-byte row of the copy to tensor memory.
 #include "dyn_scale.cuh"
 #include "gemm_common.cuh"
 #include "nvfp4.cuh"
@@ -61,7 +60,7 @@ __device__ __forceinline__ uint4 ld_live16(const uint8_t *p, bool live) {
 
 // The scales of one row and a stage's K: a word per K of 64; zeros for a row
 // that is not there.  WIDE: all four, 16-byte aligned; otherwise (rows whose
-// length is no multiple of 256) the first `chunks`.
+// length is no multiple of 256) the first `chunks`, 7 to 15 % slower in all.
 template <bool WIDE>
 __device__ __forceinline__ uint4 load_scales(const uint8_t *p, bool live, int chunks, const uint8_t *base,
                                              uint64_t extent) {
@@ -196,6 +195,15 @@ __device__ __forceinline__ void sum_shares(float4 (&c)[HALVES], const float *fro
 // end each CTA puts its partial sums in shared memory and the cluster adds them
 // in a fixed order, every CTA some of the tokens.
 //   warp 0: TMA   warp 1: products   warps 2-5: scales, then the sums
+// A scale warp has every fourth stage, a lane rows l, l + 32, ... (four lanes a
+// row and four stages at once, as in the tile kernel: 57 x 28672 x 8192 gated 49
+// -> 52 us).  Up to 64 tokens two CTAs share an SM.
+//
+// Bound by the weight's bytes and 3.5 us for start and end (some 1.2 for the
+// first stage, 0.3 for the last products, 0.9 for the sums): gated 28672 x 8192,
+// one token, 44 us (6.0 TB/s), 14336 x 4096 13.3 us (5.0); 57 tokens x 28672 x
+// 8192 gated 49 us (5.4; 448 CTAs are a wave and a half); 6144 x 4096, one
+// token, 6.1 us (2.3).
 
 constexpr int kStreamThreads = 6 * 32;
 
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
     (void)mbar_wait_bounded(&sm.drain, 0);
   } else {
     // Scales: warp 2 + x has every fourth stage.
-    const bool wide = a.K % kStageK == 0;
+    const bool wide = a.wide != 0;
     const int64_t pitch = a.K / kNvfp4Block;
     const uint8_t *row_w[4], *row_a[4];
     bool live_w[4], live_a[4];
@@ -437,6 +445,17 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
 // Many tiles: persistent pairs.  Few tiles and a long K (SPLIT): up to four
 // pairs of a cluster share a tile's K and add their sums through distributed
 // shared memory in a fixed order.
+//
+// What bounds it, at 8192 x 8192 x 8192 (175 us, 6280 TFLOP/s in a burst; under
+// the power limit of a long run 190 us): a product of a pair takes 135 cycles, a
+// stage's four 540, beside which the scales (three copies a product, 400 cycles
+// of the issuing thread a stage) and the loads run; between two tiles some 600
+// cycles pass until the shared columns are read.  Without the scales' loads it
+// runs at 7150.  One wave of short tiles is bound by its start and end: 1024 x
+// 4096 x 4096 12.5 us, 2.4 of them from the wait for the previous grid to the
+// first products, 2.2 for the epilogue.
+// Narrow TMA boxes for the scales (64 bytes a row) were slower (4096 x 8192 x
+// 28672 290 -> 331 us): they hold up the data's.
 
 constexpr int kTileStages = 5;
 constexpr int kTileStageBytes = 2 * kRows * kRowBytes;  // of either CTA
@@ -486,7 +505,7 @@ struct ScaleRows {
   int left, pitch, up;      // rows from its own that are there; bytes a row; gate to up
   bool wide, turns;         // turns: of 16 gate rows and the same 16 up rows
   __device__ __forceinline__ ScaleRows(const Fp4GemmArgs &a, const Tile &t, int my_t, int role, int lane)
-      : pitch(a.K / kNvfp4Block), up(a.N), wide(a.K % kStageK == 0), turns(GATED && role > 0) {
+      : pitch(a.K / kNvfp4Block), up(a.N), wide(a.wide != 0), turns(GATED && role > 0) {
     const int row = (role == 0 ? t.t0 + my_t : t.n0 + (role - 1) * (GATED ? kRows / 2 : kRows)) + (lane >> 2);
     base = role == 0 ? a.a_sf : a.w_sf;
     p = base + (int64_t)row * pitch + (lane & 3) * (kStageK / kNvfp4Block);

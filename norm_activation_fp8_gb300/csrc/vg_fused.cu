@@ -475,8 +475,8 @@ vg_status check_fp4_gemm(int64_t T, int64_t N, int64_t K, int64_t max_n, int64_t
 vg_status run_fp4_gemm(Fp4GemmArgs a, bool gated, int64_t T, int64_t N, int64_t K,
                        vg_stream_t stream) {
   if (misaligned(a.a, 16) || misaligned(a.w, 16) || misaligned(a.out, 16) || misaligned(a.q, 16) ||
-      misaligned(a.a_sf, 16) || misaligned(a.w_sf, 16) || misaligned(a.sf, 16) ||
-      misaligned(a.alpha, 4) || misaligned(a.global_scale, 4))
+      misaligned(a.a_sf, 4) || misaligned(a.w_sf, 4) || misaligned(a.sf, 4) || misaligned(a.alpha, 4) ||
+      misaligned(a.global_scale, 4))
     return VG_ERR_MISALIGNED;
   int sms = 0;
   const vg_status st = check_device(&sms);
@@ -485,6 +485,7 @@ vg_status run_fp4_gemm(Fp4GemmArgs a, bool gated, int64_t T, int64_t N, int64_t 
   a.T = (int32_t)T;
   a.N = (int32_t)N;
   a.K = (int32_t)K;
+  a.wide = K % 256 == 0 && !misaligned(a.a_sf, 16) && !misaligned(a.w_sf, 16);
   return launch_fp4_gemm(a, gated, sms, (cudaStream_t)stream) == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 

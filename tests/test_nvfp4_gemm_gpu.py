@@ -290,6 +290,46 @@ def test_infinite_factors_follow_ieee_arithmetic(T):
     assert bool(vg.nvfp4_gemm(a, sa, w, sw, one(float("nan"))).isnan().all())
 
 
+@pytest.mark.parametrize("T", [1, 40, 700])
+def test_gated_not_finite(T):
+    """Infinite and NaN gates and ups, and blocks of NaNs alone."""
+    import torch
+    I, K = 256, 256
+    a, sa = operand(T, K, 8, exact=True)
+    w, sw = operand(2 * I, K, 9, exact=True)
+    w[32:48], w[I + 64:I + 80] = 0, 0  # zero sums: NaN with an infinite alpha
+    q4, sf = vg.nvfp4_gemm_silu_mul_nvfp4(a, sa, w, sw, one(float("inf")), one(1.0))
+    c = (scaled(a, sa) @ scaled(w, sw).t() * float("inf"))
+    g, u = c[:, :I], c[:, I:]
+    y = torch.where(g == -float("inf"), float("nan"), g) * u
+    block = lambda x: x.view(T, I // 16, 16)  # noqa: E731
+    inf = torch.isinf(block(y)).any(-1)
+    assert torch.equal(sf.float(), torch.where(inf, 448.0, 0.0).float())
+    got = block(values(q4))
+    assert bool((got[~inf] == 0).all()) and bool((got[inf].abs() == 6).all())
+    at = torch.isinf(block(y))
+    assert torch.equal(got[at].sign(), block(y)[at].sign())
+
+
+@pytest.mark.parametrize("K", [64, 192, 256, 448, 512])
+@pytest.mark.parametrize("T,N", [(5, 72), (300, 10240)])
+def test_rows_of_larger_tensors(T, N, K):
+    """Operands and outputs that are some rows of larger tensors, at any row, and
+    scales that are 4-byte aligned only."""
+    import torch
+    a, sa = operand(T + 9, K, 1, exact=True)
+    w, sw = operand(N + 64, K, 2, exact=True)
+    for i, j in ((1, 3), (8, 64)):
+        buf = torch.zeros((T + 9, N), dtype=torch.bfloat16, device="cuda")
+        vg.vg_nvfp4_gemm(buf[i:i + T], a[i:i + T], sa[i:i + T], w[j:j + N], sw[j:j + N], one(1.0))
+        want = (scaled(a[i:i + T], sa[i:i + T]) @ scaled(w[j:j + N], sw[j:j + N]).t()).to(torch.bfloat16)
+        assert torch.equal(buf[i:i + T], want)
+        assert not bool(buf[:i].any()) and not bool(buf[i + T:].any())
+    odd = torch.zeros(sa.numel() + 4, dtype=torch.uint8, device="cuda")[4:].view(sa.dtype).view(sa.shape)
+    odd.copy_(sa)
+    assert torch.equal(vg.nvfp4_gemm(a, odd, w, sw, one(1.0)), vg.nvfp4_gemm(a, sa, w, sw, one(1.0)))
+
+
 @pytest.mark.parametrize("T", [1, 50, 200, 700])
 def test_captured_calls_and_two_streams(T):
     """Captured calls follow their inputs, and calls on two streams at once do not

@@ -70,12 +70,13 @@ def test_product_refusals(lib):
         assert gemm(lib, **{k: None}) == NULL, k
     for k in ("q4", "sf", "a", "sa", "w", "sw", "alpha", "gs"):
         assert gated(lib, **{k: None}) == NULL, k
-    for k in ("out", "a", "sa", "w", "sw"):
+    for k in ("out", "a", "w"):
         assert gemm(lib, **{k: A + 8}) == ALIGN, k
-    for k in ("q4", "sf", "a", "sa", "w", "sw"):
+    for k in ("q4", "a", "w"):
         assert gated(lib, **{k: A + 8}) == ALIGN, k
-    assert gemm(lib, alpha=A + 2) == ALIGN
-    for k in ("alpha", "gs"):
+    for k in ("sa", "sw", "alpha"):
+        assert gemm(lib, **{k: A + 2}) == ALIGN, k
+    for k in ("sf", "sa", "sw", "alpha", "gs"):
         assert gated(lib, **{k: A + 2}) == ALIGN, k
     assert gemm(lib, out=None, a=None, sa=None, w=None, sw=None, alpha=None, T=0) == OK
     assert gated(lib, q4=None, sf=None, a=None, sa=None, w=None, sw=None, alpha=None, gs=None, T=0) == OK
