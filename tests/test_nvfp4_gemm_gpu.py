@@ -240,6 +240,24 @@ def test_outputs_past_32_bit_offsets():
     assert torch.equal(sf.view(torch.uint8)[rows], few[1].view(torch.uint8))
 
 
+@pytest.mark.parametrize("T,N,K", [(2 ** 24, 8, 64), (1, 2 ** 20, 64), (130, 2 ** 20, 64), (5, 8, 32768)])
+def test_largest_sizes(T, N, K):
+    import torch
+    a, sa = operand(T, K, 1, exact=True)
+    w, sw = operand(N, K, 2, exact=True)
+    out = vg.nvfp4_gemm(a, sa, w, sw, one(1.0))
+    at = lambda n: torch.tensor(sorted({0, n // 3, n // 2, n - 1}), device="cuda")  # noqa: E731
+    pick = lambda q, s, i: scaled(q[i], s.view(torch.uint8)[i].view(s.dtype))  # noqa: E731
+    want = pick(a, sa, at(T)) @ pick(w, sw, at(N)).t()
+    assert torch.equal(out[at(T)][:, at(N)], want.to(torch.bfloat16))
+    if T == 2 ** 24:
+        w, sw = operand(128, K, 3, exact=True)
+        q4, sf = vg.nvfp4_gemm_silu_mul_nvfp4(a, sa, w, sw, one(0.1), one(10.0))
+        few = vg.nvfp4_gemm_silu_mul_nvfp4(a[at(T)], sa.view(torch.uint8)[at(T)].view(sa.dtype), w, sw, one(0.1), one(10.0))
+        assert torch.equal(q4[at(T)], few[0])
+        assert torch.equal(sf.view(torch.uint8)[at(T)], few[1].view(torch.uint8))
+
+
 @pytest.mark.parametrize("T,N", [(3, 262160), (262160, 16)])
 def test_operands_past_32_bit_offsets(T, N):
     """A weight, then activations, of more than 2^32 bytes of codes; rows sampled."""
