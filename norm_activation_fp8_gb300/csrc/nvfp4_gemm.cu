@@ -13,7 +13,6 @@
 // ops write them.  Warps of their own move them: from 16 bytes (K of 256, a
 // stage) of rows l, l + 32, ... come, for each K of 64, the four rows' words as
 // one 16-byte row of the copy to tensor memory.
-#include "dyn_scale.cuh"
 #include "gemm_common.cuh"
 #include "nvfp4.cuh"
 
