@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
       if (++s == kStages) s = 0, ++lap;
     }
   } else if (warp == 1) {
+    VG_LOOKS;
     constexpr uint32_t desc = nvfp4_product_desc(kRows, TN);
     int s = 0, lap = 0;
     bool seen = false;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
       tcgen05_fence_after();
       const int now = s;
       if (++s == kStages) s = 0, ++lap;
-      seen = mbar_try_look(&sm.full[s], lap & 1);  // while this stage's products are issued
+      mbar_look<0>(&sm.full[s], lap & 1);  // while this stage's products are issued
       if (elect_lane()) {
         const uint64_t dw = operand_desc(smem_u32(sm.stage[now]));
         const uint64_t da = operand_desc(smem_u32(sm.stage[now] + kRows * kRowBytes));
@@ -336,6 +337,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
         mma_commit<false>(&sm.empty[now]);
       }
       __syncwarp();
+      seen = mbar_seen<0>();
     }
     if (elect_lane()) mma_commit<false>(&sm.drain);
     __syncwarp();
@@ -625,6 +627,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (uint32_t i = issued < kTileStages ? 0 : issued - kTileStages; i < issued && ok; ++i)
       ok = warp_wait_phase(&sm.empty[i % kTileStages], (i / kTileStages) & 1, &sm.failed);
   } else if (warp == 1 && rank == 0) {
+    VG_LOOKS;
     constexpr uint32_t desc = nvfp4_product_desc(2 * kRows, kAcc);
     uint32_t s = 0, lap = 0, j = 0, group = 0;
     bool ok = true, seen = false, seen_sf = false;
@@ -646,9 +649,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (++s == kTileStages) s = 0, ++lap;
         // A look at the next stage while this one's products are issued (even
         // a wait for nothing takes some 160 cycles).
-        seen = mbar_try_look(&sm.full[s], lap & 1);
+        mbar_look<0>(&sm.full[s], lap & 1);
         const bool last = part == kGroup - 1 || kb == num_k - 1;
-        if (last) seen_sf = mbar_try_look(&sm.sf_full[(group + 1) & 1], ((group + 1) >> 1) & 1);
+        if (last) mbar_look<1>(&sm.sf_full[(group + 1) & 1], ((group + 1) >> 1) & 1);
         if (elect_lane()) {
           const uint64_t da = operand_desc(smem_u32(sm.stage[now]));
           const uint64_t dw = operand_desc(smem_u32(sm.stage[now] + kRows * kRowBytes));
@@ -676,6 +679,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (kb == num_k - 1) mma_commit_pair(&sm.acc_full[j & 1], base);
         }
         __syncwarp();
+        seen = mbar_seen<0>();
+        if (last) seen_sf = mbar_seen<1>();
         group += last;
       }
     }

@@ -63,16 +63,27 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
   return done != 0;
 }
 
-// Whether the phase with the given parity is over, without waiting.
-__device__ __forceinline__ bool mbar_try_look(uint64_t *bar, uint32_t parity) {
+// Whether the phase with the given parity is over, without waiting: asked now,
+// the answer taken later.  The answer rests in a predicate register N (0 or 1)
+// that VG_LOOKS declares for the whole kernel: as a value of the same statement
+// it would hold up what is issued in between, some 120 cycles.
+#define VG_LOOKS asm volatile(".reg .pred vg_look0, vg_look1;")
+template <int N>
+__device__ __forceinline__ void mbar_look(uint64_t *bar, uint32_t parity) {
+  if constexpr (N == 0)
+    asm volatile("mbarrier.test_wait.parity.shared::cta.b64 vg_look0, [%0], %1;" ::"r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+  else
+    asm volatile("mbarrier.test_wait.parity.shared::cta.b64 vg_look1, [%0], %1;" ::"r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ bool mbar_seen() {
   uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  if constexpr (N == 0)
+    asm volatile("selp.u32 %0, 1, 0, vg_look0;" : "=r"(done)::"memory");
+  else
+    asm volatile("selp.u32 %0, 1, 0, vg_look1;" : "=r"(done)::"memory");
   return done != 0;
 }
 
