@@ -447,14 +447,15 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
 // pairs of a cluster share a tile's K and add their sums through distributed
 // shared memory in a fixed order.
 //
-// What bounds it, at 8192 x 8192 x 8192 (175 us, 6280 TFLOP/s in a burst; under
-// the power limit of a long run 190 us): a product of a pair takes 135 cycles, a
-// stage's four 540, beside which the scales (three copies a product, 400 cycles
-// of the issuing thread a stage) and the loads run; between two tiles some 600
-// cycles pass until the shared columns are read.  Without the scales' loads it
-// runs at 7150.  One wave of short tiles is bound by its start and end: 1024 x
-// 4096 x 4096 12.5 us, 2.4 of them from the wait for the previous grid to the
-// first products, 2.2 for the epilogue.
+// What bounds it, at 8192 x 8192 x 8192 (168 to 182 us by box, 6030 to 6530
+// TFLOP/s in a burst; in a long run the power limit, 4093 x 8192 x 28672 293 us
+// and then 328): a product of a pair takes 135 cycles, a stage's four 540. The
+// issuing thread takes some 500 a stage (16 copies and products 130, two commits
+// 80, the waits' votes 130, a look ahead 50, descriptors 50; the answer to the
+// look taken at once was 120 more, 182 -> 193 us).  Between two tiles some 600
+// cycles pass until the shared columns are read.  One wave of short tiles is
+// bound by its start and end: 1024 x 4096 x 4096 12.3 us, 2.4 of them from the
+// wait for the previous grid to the first products, 2.2 for the epilogue.
 // Narrow TMA boxes for the scales (64 bytes a row) were slower (4096 x 8192 x
 // 28672 290 -> 331 us): they hold up the data's.
 
@@ -647,8 +648,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tcgen05_fence_after();
         const uint32_t now = s;
         if (++s == kTileStages) s = 0, ++lap;
-        // A look at the next stage while this one's products are issued (even
-        // a wait for nothing takes some 160 cycles).
+        // A look at the next stage, answered once this one's products are issued
+        // (even a wait for nothing takes some 160 cycles).
         mbar_look<0>(&sm.full[s], lap & 1);
         const bool last = part == kGroup - 1 || kb == num_k - 1;
         if (last) mbar_look<1>(&sm.sf_full[(group + 1) & 1], ((group + 1) >> 1) & 1);
