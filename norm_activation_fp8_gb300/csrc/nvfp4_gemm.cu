@@ -199,10 +199,11 @@ __device__ __forceinline__ void sum_shares(float4 (&c)[HALVES], const float *fro
 // -> 52 us).  Up to 64 tokens two CTAs share an SM.
 //
 // Bound by the weight's bytes and 3.5 us for start and end (some 1.2 for the
-// first stage, 0.3 for the last products, 0.9 for the sums): gated 28672 x 8192,
-// one token, 44 us (6.0 TB/s), 14336 x 4096 13.3 us (5.0); 57 tokens x 28672 x
-// 8192 gated 49 us (5.4; 448 CTAs are a wave and a half); 6144 x 4096, one
-// token, 6.1 us (2.3).
+// first stage, 0.3 for the last products, 0.9 for the sums of a cluster): gated
+// 28672 x 8192, one token, 42 us (6.3 TB/s), 14336 x 4096 13.6 us (4.8); 57
+// tokens x 28672 x 8192 gated 50 us (5.3; 448 CTAs are a wave and a half); 6144 x
+// 4096, one token, 6.1 to 6.7 us (2.2).  A CTA that has no cluster waits for none
+// (gated 57 tokens 52.1 -> 49.6 us, 16 tokens x 14336 x 4096 15.1 -> 14.1).
 
 constexpr int kStreamThreads = 6 * 32;
 
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
     for (int it = issued < kStages ? 0 : issued - kStages; it < issued; ++it)
       (void)mbar_wait_bounded(&sm.full[it % kStages], (it / kStages) & 1);
   }
-  cluster_sync();  // every CTA's partial sums are in place
+  if (splits > 1) cluster_sync();  // every CTA's partial sums are in place
   __syncwarp();
   if (warp == 1) tmem_dealloc<false>(tmem, Smem::kColumns);
 
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
         store_out4(a, t0 + j, n0 + col, scaled4(c[i][0], alpha));
     }
   }
-  cluster_sync();  // nobody reads this CTA's sums any more
+  if (splits > 1) cluster_sync();  // nobody reads this CTA's sums any more
 }
 
 // ------------------------------------------------------------- tile kernel
