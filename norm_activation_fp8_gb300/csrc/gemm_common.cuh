@@ -26,8 +26,9 @@ namespace {
 
 // Waits for a barrier phase; a wait that gives up is recorded for the CTA,
 // which reports it when it ends.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile uint32_t *failed) {
-  if (mbar_wait_bounded(bar, parity)) return true;
+  if (mbar_wait_bounded<CLUSTER>(bar, parity)) return true;
   *failed = 1;
   return false;
 }
@@ -37,10 +38,15 @@ __device__ __forceinline__ bool warp_wait_phase(uint64_t *bar, uint32_t parity, 
   return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, failed));
 }
 
-// The same where a look at the phase (mbar_try_wait) was taken some time ago.
+// The same where a look at the phase (mbar_look) was taken some time ago.
+// CLUSTER: behind what any CTA of the cluster wrote before it arrived.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait_phase(bool seen, uint64_t *bar, uint32_t parity,
                                                 volatile uint32_t *failed) {
-  return __all_sync(0xFFFFFFFFu, seen) || warp_wait_phase(bar, parity, failed);
+  const bool ok =
+      __all_sync(0xFFFFFFFFu, seen) || __all_sync(0xFFFFFFFFu, wait_phase<CLUSTER>(bar, parity, failed));
+  if constexpr (CLUSTER) acquire_cluster_written();
+  return ok;
 }
 
 // A barrier of `threads` threads that tells all of them whether any passed true.

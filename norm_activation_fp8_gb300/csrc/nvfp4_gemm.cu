@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (j > 0 && !(ok = warp_wait_phase(&sm.acc_free, (j - 1) & 1, &sm.failed))) break;
       for (int kb = 0; kb < num_k; ++kb) {
         const int part = kb % kGroup;
-        if (part == 0 && !(ok = warp_wait_phase(seen_sf, &sm.sf_full[group & 1], (group >> 1) & 1, &sm.failed)))
+        if (part == 0 && !(ok = warp_wait_phase<true>(seen_sf, &sm.sf_full[group & 1], (group >> 1) & 1, &sm.failed)))
           break;
         if (!(ok = warp_wait_phase(seen, &sm.full[s], lap & 1, &sm.failed))) break;
         if (VG_GEMM_FORCED_TIMEOUT(sm, j == 0 && kb == 0)) {

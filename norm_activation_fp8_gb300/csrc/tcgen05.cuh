@@ -116,13 +116,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same behind writes to this CTA's shared memory that products (of either
-// CTA) read here: the writers' fence_proxy_async_smem() has made them visible
-// to those reads, and they are this CTA's own memory, so the arrival needs no
-// wider scope than the CTA's (a release at cluster scope took 1150 to 1900
-// cycles).
+// The same behind writes to this CTA's shared memory: a release at cluster
+// scope, without which a thread of another CTA that sees the arrival need not
+// see the writes (it waits with warp_wait_phase<true>()).  Restricted to shared
+// memory: a release of all memory took 1150 to 1900 cycles.
 __device__ __forceinline__ void mbar_arrive_cluster_written(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  mbar_arrive_cluster(bar);
 }
 
 // Four fp32 values at a cluster address.

@@ -51,22 +51,41 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// CLUSTER: the phase's arrivals come from the cluster's other CTAs too; behind
+// it acquire_cluster_written() before what they wrote is used.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
   return done != 0;
+}
+
+// Orders what follows behind the writes to shared memory that the cluster's CTAs
+// released (mbar_arrive_cluster_written()) before the arrivals that were seen.
+__device__ __forceinline__ void acquire_cluster_written() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
 // Whether the phase with the given parity is over, without waiting: asked now,
 // the answer taken later.  The answer rests in a predicate register N (0 or 1)
 // that VG_LOOKS declares for the whole kernel: as a value of the same statement
-// it would hold up what is issued in between, some 120 cycles.
+// it would hold up what is issued in between, some 120 cycles.  Look 0 is for
+// arrivals of this CTA, look 1 as mbar_try_wait<true>().
 #define VG_LOOKS asm volatile(".reg .pred vg_look0, vg_look1;")
 template <int N>
 __device__ __forceinline__ void mbar_look(uint64_t *bar, uint32_t parity) {
@@ -74,7 +93,9 @@ __device__ __forceinline__ void mbar_look(uint64_t *bar, uint32_t parity) {
     asm volatile("mbarrier.test_wait.parity.shared::cta.b64 vg_look0, [%0], %1;" ::"r"(smem_u32(bar)), "r"(parity)
                  : "memory");
   else
-    asm volatile("mbarrier.test_wait.parity.shared::cta.b64 vg_look1, [%0], %1;" ::"r"(smem_u32(bar)), "r"(parity)
+    asm volatile("mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 vg_look1, [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "r"(parity)
                  : "memory");
 }
 template <int N>
@@ -89,9 +110,10 @@ __device__ __forceinline__ bool mbar_seen() {
 
 // Waits for the barrier's phase with the given parity; false after
 // kWaitLimit polls.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitLimit; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
   return false;
 }
 
