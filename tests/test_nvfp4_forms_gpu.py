@@ -1,13 +1,17 @@
 """Every kernel form of the NVFP4 products: each token tile with each split of K,
 plain and gated, rows of scales of whole 16 bytes (K a multiple of 256) and not.
-The sums of each form are held in fp32.
+The sums of each form are held in fp32, and the debug build, which checks every
+access against its tensor, gives the same results and finds nothing.
 
 Tolerance: none.  The plain results are the correctly rounded ones, and what the
 gated form's codes may be follows from check_gated() with exact g and u."""
+import numpy as np
 import pytest
 
 import norm_activation_fp8_gb300 as vg
+from norm_activation_fp8_gb300 import build
 from test_nvfp4_gemm_gpu import check_gated, one, packed, scaled
+from test_nvfp4_layer_gpu import _gated, _gemm, _with
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +106,29 @@ def test_the_gated_check_sees_a_lost_bit():
     for off in (c + alpha * 2.0 ** -8, c - alpha * 2.0 ** -8):
         with pytest.raises(AssertionError):
             check_gated(q4, sf, off[:, :I], off[:, I:], zero, zero, 100.0)
+
+
+FORMS = [(_gemm, *x) for x in PLAIN] + [(_gated, *x) for x in GATED]
+IDS = [f"{f.__name__[1:]}-{T}-{N}-{K}" for f, T, N, K in FORMS]
+
+
+@pytest.mark.parametrize("op,T,N,K", FORMS, ids=IDS)
+def test_debug_build_matches_and_reports_nothing(op, T, N, K, monkeypatch):
+    run = op(T, N, K)
+    want, st0 = _with(vg.load(), run, monkeypatch)
+    got, st = _with(vg.load(build.build_debug()), run, monkeypatch)
+    assert st0 == 0 and st == 0, (st0, st)
+    for k, v in want.items():
+        assert np.array_equal(got[k], v), k
+
+
+@pytest.mark.parametrize("op,T,N,K", FORMS, ids=IDS)
+def test_out_of_range_accesses_are_flagged_and_skipped(op, T, N, K, monkeypatch):
+    """With every tensor of tokens reported one row short: the last token's scale
+    reads and the stores of its row are flagged, the other rows stay."""
+    run = op(T, N, K)
+    want, _ = _with(vg.load(), run, monkeypatch)
+    got, st = _with(vg.load(build.build_debug(shrunk=True)), run, monkeypatch)
+    assert st == vg.DEVICE_OUT_OF_BOUNDS, st
+    for k, v in want.items():
+        assert np.array_equal(got[k][:-1], v[:-1]), k
