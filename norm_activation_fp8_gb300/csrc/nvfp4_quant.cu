@@ -162,8 +162,10 @@ __global__ void __launch_bounds__(kThreads) nvfp4_dequantize_kernel(const Nvfp4A
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     const int64_t i = first + k * kThreads + threadIdx.x;
-    // decode(sf) / gs, correctly rounded: one step from the reciprocal (the
-    // division itself takes its slow way for a zero scale)
+    // decode(sf) / gs, correctly rounded: Markstein's correction of the product
+    // with the correctly rounded reciprocal, by its exact remainder (nothing
+    // under- or overflows unless gs is `far`; checked for every pair of
+    // significands).  The division itself takes its slow way for a zero scale.
     const float d = e4m3_value(s[k]), q = d * inv;
     const float r = far ? __fdiv_rn(d, gs) : fmaf(fmaf(-q, gs, d), inv, q);
     const float2 r2 = make_float2(r, r);
