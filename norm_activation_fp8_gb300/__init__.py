@@ -547,7 +547,7 @@ def _block_gemm_sizes(a, a_scale, w, w_scale, a_options, dev):
     """T, N and K of an FP8 product's checked operands."""
     _, fp8, f32, _, _ = _kinds()
     N, K = _rows(w, "w")
-    T, kb = a.shape[0], K // BLOCK
+    T, kb = a.shape[0] if len(a.shape) else -1, K // BLOCK
     scales = (kb, (T + 3) // 4 * 4) if a_options & COLUMN_MAJOR else (T, kb)
     if (a.shape != (T, K) or a_scale.shape != scales or w_scale.shape != ((N + BLOCK - 1) // BLOCK, kb)
             or a.dtype not in fp8 or a.get_device() != dev or not a.is_contiguous()
@@ -723,7 +723,7 @@ def _fp4_gemm_sizes(a, a_scale, w, w_scale, alpha, dev):
     u8, fp8, _, f32, _ = _nvfp4_kinds()
     shape = w.shape
     N, half = shape if len(shape) == 2 else _rows(w, "w")
-    T = a.shape[0]
+    T = a.shape[0] if len(a.shape) else -1
     if (half % 8 or a.shape != (T, half) or a_scale.shape != (T, half // 8) or w_scale.shape != (N, half // 8)
             or a.dtype != u8 or a.get_device() != dev or not a.is_contiguous()
             or w.dtype != u8 or w.get_device() != dev or not w.is_contiguous()
