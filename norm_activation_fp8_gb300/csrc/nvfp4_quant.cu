@@ -198,10 +198,13 @@ cudaError_t launch_quantize(const Nvfp4Args &a, cudaStream_t s) {
 
 }  // namespace
 
-// Few blocks: one a thread (33 x 8192, in a run of calls, 1.25 us; four a thread
-// 1.97); many: four (16384 x 4096 25.7 us, 6.7 TB/s; one a thread 28.5).
+// Few blocks: one a thread; many: four, whose loads are on their way together.
+// One and four, in a run of calls, in us: 33 x 8192 1.7, 3.1; 1024 x 4096 3.3, 3.9;
+// 2048 x 4096 5.8, 6.7; 4096 x 4096 9.3, 9.9; 6000 x 4096 11.9, 11.7 (rows apart
+// 13.5, 14.4); 8192 x 4096 16.7, 16.2 (8191 rows, apart 19.3, 20.1); 10000 x 4096
+// apart 21.0, 20.8; 16384 x 4096 30.4, 27.4 (apart 36.7, 36.0).
 cudaError_t launch_nvfp4_quantize(const Nvfp4Args &a, cudaStream_t s) {
-  return a.T * a.nch < 1 << 20 ? launch_quantize<1>(a, s) : launch_quantize<4>(a, s);
+  return a.T * a.nch < 1 << 22 ? launch_quantize<1>(a, s) : launch_quantize<4>(a, s);
 }
 
 cudaError_t launch_nvfp4_dequantize(const Nvfp4Args &a, cudaStream_t s) {
