@@ -448,6 +448,8 @@ vg_status vg_fp8_block_gemm_silu_mul_fp8(uint8_t *q, float *scale, const uint8_t
  *   global_scale  in  fp32 [1], device, > 0 and finite (a usual one: 6 * 448
  *                 over the tensor's largest magnitude)
  *   num_tokens T >= 0; n: a multiple of 16 in [16, VG_MAX_ROW]; T * n < 2^41
+ *   (the products read rows of a multiple of 64).  q4 is 16-byte aligned: rows
+ *   from any one on are an output where n is a multiple of 32
  * A NaN never wins the amax and its code is a saturated one; a block with an
  * infinity gets the scale 448, and the infinity +-6.
  */

@@ -87,7 +87,7 @@ __device__ __forceinline__ void store_scales(uint8_t *dst, int lane, const uint4
 // Scales of 128 rows and a group of kGroup stages.  A row's scales of a group are
 // 64 bytes: four lanes load them, so that a load of the warp touches eight rows
 // (a lane a row and stage: 32 lines a load, of which an SM asks for one in about
-// two cycles; the tile kernel fell from 7700 to 4876 TFLOP/s).  p0: this lane's
+// two cycles; 4096 x 8192 x 28672 395 instead of 297 us).  p0: this lane's
 // 16 bytes of row lane / 4.  line(x, j): the distance of row 8 x + 32 j from it
 // in the tensor (in bytes it fits 32 bits); place(x, j): in the tile, where rows
 // from `left` on are not there.
@@ -448,15 +448,18 @@ __global__ void __launch_bounds__(kStreamThreads, TN <= 64 ? 2 : 1)
 // pairs of a cluster share a tile's K and add their sums through distributed
 // shared memory in a fixed order.
 //
-// What bounds it, at 8192 x 8192 x 8192 (168 to 182 us by box, 6030 to 6530
-// TFLOP/s in a burst; in a long run the power limit, 4093 x 8192 x 28672 293 us
-// and then 328): a product of a pair takes 135 cycles, a stage's four 540. The
+// What bounds it, at 8192 x 8192 x 8192 (164 to 182 us by box, 6030 to 6700
+// TFLOP/s in a burst; in a long run the power limit, 4093 x 8192 x 28672 284 us
+// and then 324): a product of a pair takes 135 cycles, a stage's four 540. The
 // issuing thread takes some 500 a stage (16 copies and products 130, two commits
 // 80, the waits' votes 130, a look ahead 50, descriptors 50; the answer to the
 // look taken at once was 120 more, 182 -> 193 us).  Between two tiles some 600
 // cycles pass until the shared columns are read.  One wave of short tiles is
-// bound by its start and end: 1024 x 4096 x 4096 12.3 us, 2.4 of them from the
-// wait for the previous grid to the first products, 2.2 for the epilogue.
+// bound by its start and end: 1024 x 4096 x 4096 12.4 us, 2.4 of them from the
+// wait for the previous grid to the first products, 2.2 for the epilogue.  With
+// most SMs at work a stage takes 0.30 to 0.35 us where eight pairs take 0.21
+// (gated 0.28); which of the clock, the L2 and the scales' loads does that has not
+// been measured apart.
 // Narrow TMA boxes for the scales (64 bytes a row) were slower (4096 x 8192 x
 // 28672 290 -> 331 us): they hold up the data's.
 
@@ -929,10 +932,12 @@ cudaError_t launch_form(const Fp4GemmArgs &a, const GemmPlan &p, int sms, cudaSt
 
 }  // namespace
 
-// Which kernel, and its split, by an estimate of either one's time, in
-// microseconds (fitted on GB300 to T = 1..2048, N = 1024..28672, K =
-// 4096..28672, plain and gated; over those 117 sizes the choice was on average
-// 1.5 %, at most 12 % above the best one):
+// Which kernel, and its split, by a cost of either one, in microseconds (fitted
+// on GB300 to T = 1..2048, N = 1024..28672, K = 4096..28672, plain and gated;
+// over those 117 sizes the choice was on average 1.5 %, at most 12 % above the
+// best one).  It ranks forms and is no forecast: where tiles fill the chip a stage
+// takes up to 0.35 us, and it is 15 to 25 % low (8192 x 8192 x 8192 140 us, 164 to
+// 182 measured), but there no other form comes near (the stream kernel's 440).
 //   tile kernel    8.1 (one share) .. 10 (four) for start and end, 1.2 for each
 //                  further wave of pairs, and 0.26 per stage of K or the
 //                  weight's bytes at 6 TB/s, whichever is longer

@@ -86,6 +86,10 @@ __device__ __forceinline__ void acquire_cluster_written() {
 // that VG_LOOKS declares for the whole kernel: as a value of the same statement
 // it would hold up what is issued in between, some 120 cycles.  Look 0 is for
 // arrivals of this CTA, look 1 as mbar_try_wait<true>().
+// The compiler does not know of the registers.  What keeps that sound: all three
+// are volatile statements, which stay in the order they are written in; a kernel
+// has VG_LOOKS once (a second copy would not assemble) and ahead of every look;
+// and every path to a mbar_seen<N>() passes a mbar_look<N>().
 #define VG_LOOKS asm volatile(".reg .pred vg_look0, vg_look1;")
 template <int N>
 __device__ __forceinline__ void mbar_look(uint64_t *bar, uint32_t parity) {
